@@ -8,23 +8,23 @@ include/hmd.h); this package is its ctypes binding plus the seeded input generat
 from ._lib import (BF16, BatchPlan, group_sequences, mixer_decode_step_batch, DEVERR_GATE, DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_SLOT, DEVERR_TIMEOUT, F32, FA, GDN,
                    KDA, SWA, DecodeIO, HmdError, KVCache, StateCache, attn_decode,
                    attn_decode_static_ws, attn_prefill, attn_prefill_ext, attn_decode_workspace_size,
-                   attn_verify,
+                   attn_verify, attn_verify_scored, attn_verify_scored_workspace_size,
                    attn_verify_workspace_size, delta_rule_decode, delta_rule_decode_act,
                    delta_rule_decode_chain,
                    delta_rule_decode_to, delta_rule_prefill_chunked_act,
                    delta_rule_prefill_chunked, delta_rule_prefill_chunked_ws,
                    delta_rule_prefill_workspace_size, hmd_device_errors, hmd_last_error,
-                   hmd_status_string, hmd_test_arm_copy_skip, hmd_version, lib,
+                   hmd_status_string, hmd_test_arm_copy_skip, hmd_version, kv_cache_evict, lib,
                    mixer_decode_step)
 
 __all__ = ["BF16", "BatchPlan", "group_sequences", "mixer_decode_step_batch", "DEVERR_GATE", "DEVERR_PAGE", "DEVERR_SEQLEN", "DEVERR_SLOT", "DEVERR_TIMEOUT", "F32", "FA",
            "GDN", "KDA", "SWA", "DecodeIO", "HmdError", "KVCache", "StateCache", "attn_decode",
            "attn_decode_static_ws", "attn_decode_workspace_size", "attn_prefill", "attn_prefill_ext",
-           "attn_verify",
+           "attn_verify", "attn_verify_scored", "attn_verify_scored_workspace_size",
            "attn_verify_workspace_size", "delta_rule_decode", "delta_rule_decode_act",
            "delta_rule_decode_chain",
            "delta_rule_decode_to", "delta_rule_prefill_chunked_act",
            "delta_rule_prefill_chunked", "delta_rule_prefill_chunked_ws",
            "delta_rule_prefill_workspace_size", "hmd_device_errors", "hmd_last_error",
-           "hmd_status_string", "hmd_test_arm_copy_skip", "hmd_version", "lib",
+           "hmd_status_string", "hmd_test_arm_copy_skip", "hmd_version", "kv_cache_evict", "lib",
            "mixer_decode_step"]

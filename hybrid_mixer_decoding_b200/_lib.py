@@ -63,6 +63,13 @@ _SIGS = {
     "attn_verify_workspace_size": (_sz, [_c_int] * 9),
     "attn_verify": (_c_int, [_c_int] * 9 + [_vp] * 5 + [_c_int, _vp, _c_int, _vp, _c_int, _vp,
                                              _vp, _sz, _vp]),
+    "attn_verify_scored_workspace_size": (_sz, [_c_int] * 7),
+    "attn_verify_scored": (_c_int, [_c_int] * 6 + [_vp] * 5 + [_c_int, _vp, _c_int, _vp, _c_int,
+                                                             _vp, _c_int, _c_int, _vp, _vp, _vp,
+                                                             _sz, _vp]),
+    "kv_cache_evict": (_c_int, [_c_int] * 6 + [_vp, _vp, _c_int, _vp, _c_int, _vp, _c_int, _vp,
+                                               _c_int, _c_int, _vp, _vp, _c_int, _vp, _c_int, _vp,
+                                               _vp, _vp]),
     "attn_decode": (_c_int, [_c_int] * 7 + [_vp] * 5 + [_c_int, _vp, _c_int, _vp, _c_int, _vp,
                                                       _vp, _sz, _vp]),
     "attn_prefill": (_c_int, [_c_int] * 8 + [_vp] * 5 + [_c_int, _vp, _c_int, _vp, _vp]),
@@ -141,6 +148,26 @@ def _contig(*ts):
     for t in ts:
         if t is not None and not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
+
+
+def _expect(dtype, **tensors) -> None:
+    """Every given tensor is a contiguous one of `dtype` on the current device."""
+    tensors = {name: t for name, t in tensors.items() if t is not None}
+    for name, t in tensors.items():
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    for name, t in tensors.items():
+        if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} must be on the current CUDA device, not {t.device}")
+
+
+def _shape(t, *want, name) -> None:
+    """t has the wanted sizes (None: any)."""
+    if t is not None and (t.dim() != len(want) or
+                          any(w is not None and w != n for w, n in zip(want, t.shape))):
+        raise ValueError(f"{name} must have shape {want}, not {tuple(t.shape)}")
 
 
 def delta_rule_decode(kind, q, k, v, beta, log_gate, state, o, slots=None, scale=1.0,
@@ -293,6 +320,68 @@ def attn_verify(kind, window, ring_pages, q, new_k, new_v, k_pool, v_pool, page_
                            _p(workspace), workspace.numel() * workspace.element_size(),
                            _stream(stream))
     _check("attn_verify", st)
+
+
+def attn_verify_scored_workspace_size(n_q, B, Hq, Hkv, d, page_tokens, max_seq_len) -> int:
+    return int(lib().attn_verify_scored_workspace_size(n_q, B, Hq, Hkv, d, page_tokens,
+                                                       max_seq_len))
+
+
+def attn_verify_scored(q, new_k, new_v, k_pool, v_pool, weights, page_table, seq_lens,
+                       max_seq_len, o, workspace, slots=None, stream=None) -> None:
+    """attn_verify over an FA cache that also adds every key's softmax weight to weights
+    [n_slots,Hkv,w_len] fp32 (see include/hmd.h); n_q = 1 is the decode step. q,o [B,n_q,Hq,d];
+    new_k,new_v [B,n_q,Hkv,d]; slots int32 [B] or None (row b)."""
+    _expect(torch.bfloat16, q=q, new_k=new_k, new_v=new_v, k_pool=k_pool, v_pool=v_pool, o=o)
+    _expect(torch.float32, weights=weights)
+    _expect(torch.int32, page_table=page_table, seq_lens=seq_lens, slots=slots)
+    _expect(workspace.dtype, workspace=workspace)
+    B, n_q, Hq, d = q.shape
+    n_pages, Hkv, PT, _ = k_pool.shape
+    _shape(o, B, n_q, Hq, d, name="o")
+    for name, t in (("new_k", new_k), ("new_v", new_v)):
+        _shape(t, B, n_q, Hkv, d, name=name)
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        _shape(t, n_pages, Hkv, PT, d, name=name)
+    _shape(weights, None, Hkv, None, name="weights")
+    _shape(page_table, B, None, name="page_table")
+    _shape(seq_lens, B, name="seq_lens")
+    _shape(slots, B, name="slots")
+    st = lib().attn_verify_scored(n_q, B, Hq, Hkv, d, PT, _p(q), _p(new_k), _p(new_v), _p(k_pool),
+                                  _p(v_pool), n_pages, _p(page_table), page_table.shape[1],
+                                  _p(seq_lens), int(max_seq_len), _p(weights), weights.shape[2],
+                                  weights.shape[0], _p(slots), _p(o), _p(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("attn_verify_scored", st)
+
+
+def kv_cache_evict(budget, recent, k_pool, v_pool, page_table, seq_lens, max_seq_len, weights,
+                   dst_table, weights_out, kept, new_lens, slots=None, stream=None) -> None:
+    """Keep, per sequence and kv-head, the `recent` last entries and those with the largest
+    accumulated weight, `budget` in all, packed in their order (see include/hmd.h). pools
+    [n_pages,Hkv,64,d] bf16; weights, weights_out [n_slots,Hkv,*] fp32; kept int32
+    [B,Hkv,budget]; new_lens int32 [B]. dst_table may be page_table, weights_out weights and
+    new_lens seq_lens (in place)."""
+    _expect(torch.bfloat16, k_pool=k_pool, v_pool=v_pool)
+    _expect(torch.float32, weights=weights, weights_out=weights_out)
+    _expect(torch.int32, page_table=page_table, seq_lens=seq_lens, dst_table=dst_table, kept=kept,
+            new_lens=new_lens, slots=slots)
+    n_pages, Hkv, PT, d = k_pool.shape
+    B = seq_lens.shape[0]
+    _shape(v_pool, n_pages, Hkv, PT, d, name="v_pool")
+    _shape(page_table, B, None, name="page_table")
+    _shape(dst_table, B, None, name="dst_table")
+    _shape(weights, None, Hkv, None, name="weights")
+    _shape(weights_out, weights.shape[0], Hkv, None, name="weights_out")
+    _shape(kept, B, Hkv, int(budget), name="kept")
+    _shape(new_lens, B, name="new_lens")
+    _shape(slots, B, name="slots")
+    st = lib().kv_cache_evict(int(budget), int(recent), B, Hkv, d, PT, _p(k_pool), _p(v_pool),
+                              n_pages, _p(page_table), page_table.shape[1], _p(seq_lens),
+                              int(max_seq_len), _p(weights), weights.shape[2], weights.shape[0],
+                              _p(slots), _p(dst_table), dst_table.shape[1], _p(weights_out),
+                              weights_out.shape[2], _p(kept), _p(new_lens), _stream(stream))
+    _check("kv_cache_evict", st)
 
 
 def attn_decode_static_ws(kind, window, q, new_k, new_v, k_pool, v_pool, page_table, seq_lens,

@@ -25,6 +25,9 @@
 // a kv-head share the MMA's 16 rows (and the one pass over the pages), each row with its own
 // causal limit, and every new token is appended. n_q = 1 is the decode step.
 // Kernel 2 (combine): log-sum-exp merge of the splits into bf16 o.
+// Scored form (attn_verify_scored): the split kernel also stores every row's scaled scores, and
+// kernel 2 carries further blocks that turn them into softmax weights, which need the maximum and
+// sum over all splits, and add them up per key.
 // The step is HBM-bound (K and V are read once: ~4 flop per byte); the design goal is to keep
 // enough page copies in flight to stream at the HBM rate.
 #include <cuda.h>
@@ -58,6 +61,8 @@ struct SplitParams {
     const int32_t *rows;  // launch row r runs batch row rows[r] (NULL: r itself)
     float *ws_ml;   // [B*nq*Hq][n_splits][2]: running max (log2 domain), sum of exponentials
     float *ws_acc;  // [B*nq*Hq][n_splits][D]
+    float *ws_s;    // scored form: [B*Hkv][nq*G][s_len] scaled scores (log2 domain)
+    int s_len;      // positions per row of ws_s, a multiple of kPT
     int B, Hq, Hkv, group, nq, n_pages, max_pages, window, swa, ring_pages;
     int n_splits, pages_per_split, max_seq_len;
     float scale_log2;  // log2(e) / sqrt(d)
@@ -138,7 +143,8 @@ __device__ __forceinline__ void load_q(const SplitParams &p, int b, int g, int l
 // pages of 32 consecutive tiles (one coalesced page-table load per 32 tiles, fetched a chunk
 // ahead), and lane 0 issues each tile's TMA copies and records the tile's page in shared memory
 // before arming the stage's barrier. The tile loop itself reads no global memory.
-template <int D>
+// SCORED: every (row, key) score of the range is stored too, masked ones as -inf.
+template <int D, bool SCORED>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const SplitParams p) {
@@ -224,6 +230,12 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         const int r = rr ? r1 : r0;
         row_hi[rr] = r < rows ? first_new + r / G : -1;
         row_lo[rr] = (p.swa && row_hi[rr] + 1 > p.window) ? row_hi[rr] + 1 - p.window : 0;
+    }
+    float *s_row[2] = {nullptr, nullptr};  // this thread's two rows of the stored scores
+    if constexpr (SCORED) {
+        float *s0 = p.ws_s + ((size_t)it.r * p.Hkv + it.g) * rows * p.s_len;
+        s_row[0] = s0 + (size_t)r0 * p.s_len;
+        s_row[1] = s0 + (size_t)r1 * p.s_len;
     }
     float m_run[2] = {-INFINITY, -INFINITY};
     float l_run[2] = {0.f, 0.f};
@@ -314,6 +326,17 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     mx[e >> 1] = fmaxf(mx[e >> 1], sc[j][e]);
                 }
             }
+            if constexpr (SCORED) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int rr = 0; rr < 2; ++rr) {
+                        if ((rr ? r1 : r0) < rows)
+                            *reinterpret_cast<float2 *>(s_row[rr] + base + warp * 16 + j * 8 + cq) =
+                                make_float2(sc[j][2 * rr], sc[j][2 * rr + 1]);
+                    }
+                }
+            }
             float corr[2], mu[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -354,6 +377,13 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     mma_bf16_16816(oacc[2 * nn], pa, v0, v1);
                     mma_bf16_16816(oacc[2 * nn + 1], pa, v2, v3);
                 }
+            }
+        }
+        if constexpr (SCORED) {
+            if (!tile_ok) {  // no copy: these keys get no weight
+                for (int idx = tid; idx < rows * kPT; idx += kThreads)
+                    p.ws_s[(((size_t)it.r * p.Hkv + it.g) * rows + idx / kPT) * p.s_len + base +
+                           idx % kPT] = -INFINITY;
             }
         }
         __syncthreads();  // every warp is done with stage s
@@ -443,6 +473,102 @@ __global__ void __launch_bounds__(D) attn_combine_kernel(const float *ws_ml, con
     o[ob * D + dim] = __float2bfloat16_rn(den > 0.f ? num / den : 0.f);
 }
 
+// Kernel 2 of the scored form: one launch, two kinds of blocks of 128 threads. The first
+// n_row_blocks merge the splits of 128 / D query rows into o, as attn_combine_kernel does; the
+// others each take one (sequence, kv-head) and kScoreKeys keys: with M_r and l_r the maximum and
+// sum over all splits, key j received sum_r 2^(s_rj - M_r) / l_r from the group's rows, which is
+// added to its accumulated weight (a new token's slot starts from 0). Every key has one thread
+// and its rows are added in order, so results do not depend on scheduling. A sequence whose
+// length was refused or whose range gave up keeps its weights.
+constexpr int kScoreKeys = 512;
+struct ScoreParams {
+    const float *ws_ml, *ws_acc, *ws_s;
+    const int32_t *seq_lens, *slots;
+    float *weights;  // [n_slots][Hkv][w_len]
+    __nv_bfloat16 *o;
+    int Hq, Hkv, nq, n_splits, s_len, max_seq_len, n_slots, w_len, n_rows, n_row_blocks, n_chunks;
+};
+template <int D>
+__global__ void __launch_bounds__(128) attn_combine_scored_kernel(const ScoreParams p) {
+    constexpr int RPB = 128 / D;  // query rows per merging block
+    const int tid = threadIdx.x;
+    griddep_launch_dependents();
+    griddep_wait();  // the partials and scores are the split kernel's output
+    if ((int)blockIdx.x < p.n_row_blocks) {
+        const int bh = blockIdx.x * RPB + tid / D, dim = tid % D;
+        if (bh >= p.n_rows) return;
+        const float *ml = p.ws_ml + (size_t)bh * p.n_splits * 2;
+        float M = -INFINITY;
+        for (int s = 0; s < p.n_splits; ++s) {
+            M = fmaxf(M, ml[2 * s]);
+            if (ml[2 * s + 1] < 0.f) return;  // a range that gave up: o stays as it was
+        }
+        float num = 0.f, den = 0.f;
+        if (M != -INFINITY) {
+            for (int s = 0; s < p.n_splits; ++s) {
+                const float f = exp2f(ml[2 * s] - M);
+                num += f * p.ws_acc[((size_t)bh * p.n_splits + s) * D + dim];
+                den += f * ml[2 * s + 1];
+            }
+        }
+        p.o[(size_t)bh * D + dim] = __float2bfloat16_rn(den > 0.f ? num / den : 0.f);
+        return;
+    }
+    __shared__ float s_max[kMaxGroup], s_inv[kMaxGroup];
+    __shared__ int s_missing;
+    const int i = (int)blockIdx.x - p.n_row_blocks;
+    const int bg = i / p.n_chunks, chunk = i - bg * p.n_chunks;
+    const int b = bg / p.Hkv, g = bg - b * p.Hkv;
+    const int L = p.seq_lens[b], G = p.Hq / p.Hkv, R = p.nq * G;
+    if (L < p.nq || L > p.max_seq_len || chunk * kScoreKeys >= L) return;
+    const int slot = p.slots ? p.slots[b] : b;
+    if (slot < 0 || slot >= p.n_slots) {
+        if (tid == 0) atomicOr(&g_err, HMD_DEVERR_SLOT);
+        return;
+    }
+    if (tid == 0) s_missing = 0;
+    __syncthreads();
+    for (int r = tid >> 5; r < R; r += 4) {  // a warp per row: the row's statistics
+        const int ti = r / G, lane = tid & 31;
+        const size_t row = ((size_t)b * p.nq + ti) * p.Hq + g * G + (r - ti * G);
+        const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + row * p.n_splits;
+        float M = -INFINITY, l = 0.f;
+        bool missing = false;
+        for (int s = lane; s < p.n_splits; s += 32) {
+            const float2 v = ml[s];
+            missing |= v.y < 0.f;
+            const float m2 = fmaxf(M, v.x);
+            if (m2 != -INFINITY) l = l * exp2f(M - m2) + v.y * exp2f(v.x - m2);
+            M = m2;
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1) {
+            const float Mo = __shfl_xor_sync(0xffffffffu, M, off);
+            const float lo = __shfl_xor_sync(0xffffffffu, l, off);
+            const float m2 = fmaxf(M, Mo);
+            if (m2 != -INFINITY) l = l * exp2f(M - m2) + lo * exp2f(Mo - m2);
+            M = m2;
+        }
+        if (__any_sync(0xffffffffu, missing) && lane == 0) s_missing = 1;
+        if (lane == 0) {
+            s_max[r] = M == -INFINITY ? 0.f : M;
+            s_inv[r] = l > 0.f ? 1.f / l : 0.f;
+        }
+    }
+    __syncthreads();
+    if (s_missing) return;
+    const float *sc = p.ws_s + (size_t)bg * R * p.s_len;
+    float *w = p.weights + ((size_t)slot * p.Hkv + g) * p.w_len;
+#pragma unroll
+    for (int u = 0; u < kScoreKeys / 128; ++u) {
+        const int j = chunk * kScoreKeys + u * 128 + tid;
+        if (j >= L) break;
+        float a = 0.f;
+        for (int r = 0; r < R; ++r) a += exp2f(sc[(size_t)r * p.s_len + j] - s_max[r]) * s_inv[r];
+        w[j] = j < L - p.nq ? w[j] + a : a;
+    }
+}
+
 // ---- host side --------------------------------------------------------------------------
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -478,13 +604,21 @@ bool make_pool_map(CUtensorMap *m, void *pool, int n_pages, int Hkv, int d) {
            CUDA_SUCCESS;
 }
 
+// Positions per row of the scored form's stored scores: whole pages.
+int scored_len(int max_seq_len) { return (max_seq_len + kPT - 1) / kPT * kPT; }
+
 template <int D>
 cudaError_t launch_d(const AttnDecodeArgs &a, const AttnPlan &plan, cudaStream_t s) {
     const int group = a.Hq / a.Hkv;
     constexpr int smem = smem_bytes<D>();
     const cudaError_t attr_err = once_per_device([] {
-        return cudaFuncSetAttribute(attn_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    smem_bytes<D>());
+        cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<D, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             smem_bytes<D>());
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(attn_split_kernel<D, true>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+        return e;
     });
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap tmk, tmv;
@@ -513,7 +647,25 @@ cudaError_t launch_d(const AttnDecodeArgs &a, const AttnPlan &plan, cudaStream_t
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
     p.skip_cta = a.skip.cta;
     p.wait_ns = a.skip.wait_ns;
-    cudaError_t e = launch_pdl(attn_split_kernel<D>, dim3((unsigned)plan.n_ctas), dim3(kThreads),
+    if (a.weights) {
+        p.s_len = scored_len(a.max_seq_len);
+        p.ws_s = p.ws_ml + plan.ws_bytes / sizeof(float);
+        cudaError_t e = launch_pdl(attn_split_kernel<D, true>, dim3((unsigned)plan.n_ctas),
+                                   dim3(kThreads), smem, s, tmk, tmv, p);
+        if (e != cudaSuccess) return e;
+        ScoreParams sp{};
+        sp.ws_ml = p.ws_ml; sp.ws_acc = p.ws_acc; sp.ws_s = p.ws_s;
+        sp.seq_lens = a.seq_lens; sp.slots = a.slots; sp.weights = a.weights;
+        sp.o = static_cast<__nv_bfloat16 *>(a.o);
+        sp.Hq = a.Hq; sp.Hkv = a.Hkv; sp.nq = a.nq; sp.n_splits = plan.n_splits;
+        sp.s_len = p.s_len; sp.max_seq_len = a.max_seq_len; sp.n_slots = a.n_slots;
+        sp.w_len = a.w_len; sp.n_rows = a.B * a.nq * a.Hq;
+        sp.n_row_blocks = (sp.n_rows + 128 / D - 1) / (128 / D);
+        sp.n_chunks = (a.max_seq_len + kScoreKeys - 1) / kScoreKeys;
+        const unsigned grid = (unsigned)(sp.n_row_blocks + a.B * a.Hkv * sp.n_chunks);
+        return launch_pdl(attn_combine_scored_kernel<D>, dim3(grid), dim3(128), 0, s, sp);
+    }
+    cudaError_t e = launch_pdl(attn_split_kernel<D, false>, dim3((unsigned)plan.n_ctas), dim3(kThreads),
                                smem, s, tmk, tmv, p);
     if (e != cudaSuccess) return e;
     return launch_pdl(attn_combine_kernel<D>, dim3((unsigned)(n_run * a.nq * a.Hq)), dim3(D), 0, s,
@@ -569,6 +721,12 @@ AttnPlan attn_decode_plan(bool swa, int window, int B, int Hq, int Hkv, int d, i
     const size_t rows = (size_t)B * nq * Hq * splits;
     pl.ws_bytes = (((rows * 2 + 3) & ~static_cast<size_t>(3)) + rows * d) * sizeof(float);
     return pl;
+}
+
+size_t attn_scored_ws_bytes(int nq, int B, int Hq, int Hkv, int d, int page_tokens,
+                            int max_seq_len) {
+    const AttnPlan pl = attn_decode_plan(false, 0, B, Hq, Hkv, d, page_tokens, max_seq_len, nq);
+    return pl.ws_bytes + (size_t)B * nq * Hq * scored_len(max_seq_len) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {

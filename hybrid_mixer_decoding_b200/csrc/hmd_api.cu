@@ -122,7 +122,7 @@ hmd_status_t hmd_device_errors(hmd_stream_t stream, uint32_t *bits, int clear) {
     if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return fail(HMD_ERR_CUDA);
     *bits = hmd::delta_decode_read_errors(clear != 0) | hmd::attn_decode_read_errors(clear != 0) |
             hmd::delta_prefill_read_errors(clear != 0) | hmd::delta_prefill_scan_read_errors(clear != 0) |
-            hmd::attn_prefill_tc_read_errors(clear != 0);
+            hmd::attn_prefill_tc_read_errors(clear != 0) | hmd::kv_evict_read_errors(clear != 0);
     return HMD_OK;
 }
 
@@ -421,13 +421,21 @@ size_t attn_decode_workspace_size(hmd_kind_t kind, int window, int B, int Hq, in
 }  // extern "C"
 
 namespace {
+// The accumulated-weight rows of attn_verify_scored.
+struct WeightRows {
+    float *w;
+    int w_len, n_slots;
+    const int32_t *slots;
+};
+
 // attn_verify over the batch rows `rows` (device, n_rows of them; NULL: every row of B).
 hmd_status_t attn_run(hmd_kind_t kind, int window, int ring_pages, int n_q, int B, int Hq,
                       int Hkv, int d, int page_tokens, const void *q, const void *new_k,
                       const void *new_v, void *k_pool, void *v_pool, int n_pages,
                       const int32_t *page_table, int max_pages, const int32_t *seq_lens,
                       int max_seq_len, void *o, void *workspace, size_t ws_bytes,
-                      const int32_t *rows, int n_rows, hmd_stream_t stream) {
+                      const int32_t *rows, int n_rows, hmd_stream_t stream,
+                      const WeightRows *weights = nullptr) {
     if (kind != HMD_FA && kind != HMD_SWA) return fail(HMD_ERR_ARG);
     if (kind == HMD_SWA && window < 1) return fail(HMD_ERR_ARG);
     if (B < 0 || n_q < 1 || Hq < 1 || Hkv < 1 || d < 1 || page_tokens < 1 || n_pages < 1 ||
@@ -454,8 +462,19 @@ hmd_status_t attn_run(hmd_kind_t kind, int window, int ring_pages, int n_q, int 
         return fail(HMD_ERR_ARG);
     const hmd::AttnPlan pl = hmd::attn_decode_plan(kind == HMD_SWA, window, rows ? n_rows : B, Hq,
                                                    Hkv, d, page_tokens, max_seq_len, n_q);
-    if (ws_bytes < pl.ws_bytes) return fail(HMD_ERR_SHAPE);
+    const size_t need_ws = weights ? hmd::attn_scored_ws_bytes(n_q, B, Hq, Hkv, d, page_tokens,
+                                                               max_seq_len)
+                                   : pl.ws_bytes;
+    if (ws_bytes < need_ws) return fail(HMD_ERR_SHAPE);
     hmd::AttnDecodeArgs a{};
+    if (weights) {
+        if (!weights->w) return fail(HMD_ERR_ARG);
+        if (weights->w_len < max_seq_len || weights->n_slots < 0 ||
+            (!weights->slots && weights->n_slots < B))
+            return fail(HMD_ERR_SHAPE);
+        a.weights = weights->w; a.w_len = weights->w_len;
+        a.n_slots = weights->n_slots; a.slots = weights->slots;
+    }
     a.swa = kind == HMD_SWA; a.window = window; a.ring_pages = ring_pages; a.nq = n_q;
     a.rows = rows; a.n_rows = n_rows;
     a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.d = d;
@@ -493,6 +512,63 @@ hmd_status_t attn_decode(hmd_kind_t kind, int window, int B, int Hq, int Hkv, in
     return attn_verify(kind, window, ring, 1, B, Hq, Hkv, d, page_tokens, q, new_k, new_v, k_pool,
                        v_pool, n_pages, page_table, max_pages, seq_lens, max_seq_len, o,
                        workspace, ws_bytes, stream);
+}
+
+// ---- eviction by accumulated weight ------------------------------------------------------
+
+size_t attn_verify_scored_workspace_size(int n_q, int B, int Hq, int Hkv, int d, int page_tokens,
+                                         int max_seq_len) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || d < 1 || max_seq_len < 1 || n_q < 1) return 16;
+    return hmd::attn_scored_ws_bytes(n_q, B, Hq, Hkv, d, page_tokens, max_seq_len);
+}
+
+hmd_status_t attn_verify_scored(int n_q, int B, int Hq, int Hkv, int d, int page_tokens,
+                                const void *q, const void *new_k, const void *new_v,
+                                void *k_pool, void *v_pool, int n_pages,
+                                const int32_t *page_table, int max_pages,
+                                const int32_t *seq_lens, int max_seq_len, float *weights,
+                                int w_len, int n_slots, const int32_t *slots, void *o,
+                                void *workspace, size_t ws_bytes, hmd_stream_t stream) {
+    const WeightRows rows{weights, w_len, n_slots, slots};
+    return attn_run(HMD_FA, 0, 0, n_q, B, Hq, Hkv, d, page_tokens, q, new_k, new_v, k_pool,
+                    v_pool, n_pages, page_table, max_pages, seq_lens, max_seq_len, o, workspace,
+                    ws_bytes, nullptr, 0, stream, &rows);
+}
+
+hmd_status_t kv_cache_evict(int budget, int recent, int B, int Hkv, int d, int page_tokens,
+                            void *k_pool, void *v_pool, int n_pages, const int32_t *page_table,
+                            int max_pages, const int32_t *seq_lens, int max_seq_len,
+                            const float *weights, int w_len, int n_slots, const int32_t *slots,
+                            const int32_t *dst_table, int dst_max_pages, float *weights_out,
+                            int w_out_len, int32_t *kept, int32_t *new_lens,
+                            hmd_stream_t stream) {
+    if (B < 0 || Hkv < 1 || d < 1 || page_tokens < 1 || n_pages < 1 || max_pages < 1 ||
+        max_seq_len < 1 || w_len < 1 || n_slots < 0 || dst_max_pages < 1 || w_out_len < 1 ||
+        budget < 1 || recent < 0 || recent > budget)
+        return fail(HMD_ERR_SHAPE);
+    if (B == 0) return HMD_OK;
+    if (!k_pool || !v_pool || !page_table || !seq_lens || !weights || !dst_table ||
+        !weights_out || !kept || !new_lens)
+        return fail(HMD_ERR_ARG);
+    if ((d != 64 && d != 128) || page_tokens != 64) return fail(HMD_ERR_UNSUPPORTED);
+    const long long keep = std::min(budget, max_seq_len);
+    if ((long long)max_pages * page_tokens < max_seq_len ||
+        (long long)dst_max_pages * page_tokens < keep || w_len < max_seq_len || w_out_len < keep ||
+        (!slots && n_slots < B) || (dst_table == page_table && dst_max_pages != max_pages) ||
+        (weights_out == weights && w_out_len != w_len))
+        return fail(HMD_ERR_SHAPE);
+    // grids of one block per (sequence, kv-head) and 64 rows, or 16 columns
+    if ((long long)B * Hkv * std::max<long long>(keep / 64 + 1, d / 16 + 1) >= (1LL << 31))
+        return fail(HMD_ERR_UNSUPPORTED);
+    if (!aligned16(k_pool) || !aligned16(v_pool)) return fail(HMD_ERR_ARG);
+    hmd::EvictArgs a{};
+    a.B = B; a.Hkv = Hkv; a.d = d; a.budget = budget; a.recent = recent;
+    a.k_pool = k_pool; a.v_pool = v_pool; a.n_pages = n_pages; a.page_table = page_table;
+    a.max_pages = max_pages; a.seq_lens = seq_lens; a.max_seq_len = max_seq_len;
+    a.weights = weights; a.w_len = w_len; a.n_slots = n_slots; a.slots = slots;
+    a.dst_table = dst_table; a.dst_max_pages = dst_max_pages; a.weights_out = weights_out;
+    a.w_out_len = w_out_len; a.kept = kept; a.new_lens = new_lens;
+    return from_cuda(hmd::launch_kv_evict(a, as_stream(stream)));
 }
 
 // ---- caches ------------------------------------------------------------------------------

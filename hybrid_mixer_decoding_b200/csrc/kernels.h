@@ -159,6 +159,11 @@ struct AttnDecodeArgs {
     void *workspace;
     size_t ws_bytes;
     CopySkip skip;  // fault injection (tests only); inactive by default
+    // scored form (FA, every row of B): weights [n_slots][Hkv][w_len] gains every key's softmax
+    // weight; sequence b uses row slots[b] (NULL: b). NULL weights: the plain form
+    float *weights = nullptr;
+    const int32_t *slots = nullptr;
+    int n_slots = 0, w_len = 0;
 };
 struct AttnPlan {
     int n_splits;         // key ranges per (sequence, kv-head)
@@ -169,8 +174,33 @@ struct AttnPlan {
 AttnPlan attn_decode_plan(bool swa, int window, int B, int Hq, int Hkv, int d, int page_tokens,
                           int max_seq_len, int nq);
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s);
+// workspace of the scored form: the plan's partials and every row's scores
+size_t attn_scored_ws_bytes(int nq, int B, int Hq, int Hkv, int d, int page_tokens,
+                            int max_seq_len);
 bool attn_decode_supported(int d, int page_tokens, int group, int nq);
 uint32_t attn_decode_read_errors(bool clear);
+
+// Eviction from a paged cache (kv_evict.cu): see kv_cache_evict in hmd.h.
+struct EvictArgs {
+    int B, Hkv, d, budget, recent;
+    void *k_pool, *v_pool;
+    int n_pages;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *seq_lens;
+    int max_seq_len;
+    const float *weights;  // [n_slots][Hkv][w_len]
+    int w_len, n_slots;
+    const int32_t *slots;
+    const int32_t *dst_table;
+    int dst_max_pages;
+    float *weights_out;  // [n_slots][Hkv][w_out_len]
+    int w_out_len;
+    int32_t *kept;      // [B][Hkv][budget]
+    int32_t *new_lens;  // [B]
+};
+cudaError_t launch_kv_evict(const EvictArgs &a, cudaStream_t s);
+uint32_t kv_evict_read_errors(bool clear);
 
 struct DeltaPrefillArgs {
     int kind;

@@ -1,0 +1,309 @@
+// Eviction from a paged KV cache by accumulated attention weight.
+//
+// Of a sequence's L entries, each kv-head keeps the `recent` latest and, of the n = L - recent
+// others, those with the largest accumulated weight, `budget` in all, and packs them in their
+// order: kept[0] < kept[1] < ..., entry kept[i] moves to position i. Attention over a set of keys
+// does not depend on their order, so the packed cache decodes as the same set of keys.
+//
+// Kernel 1 (choose), one CTA per (sequence, kv-head): the m-th largest of n weights is found
+// digit by digit (11, 11 and 10 bits of the weight's order-preserving integer, a histogram in
+// shared memory per digit). Then each of the 32 warps counts and, after one scan over the warps,
+// writes the entries of its own contiguous stretch: above the threshold, or equal to it while
+// equal ones are still wanted, lowest index first. The weights are read once, into shared
+// memory, up to kCacheKeys of them; longer sequences read them again per digit (from L2).
+// Kernel 2 (move): rows of K and V and the weights go to their places. Into other pages, every
+// row is independent. Within the same pages, kept[i] >= i means that a destination is a source
+// of earlier rows only: one CTA owns one 64-byte column of the rows of a (sequence, kv-head) and
+// walks them in order, a barrier between a block's loads and its stores.
+// Both are bound by memory: kernel 2 reads and writes each kept row once, kernel 1 reads each
+// weight once.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "ptx.cuh"
+#include "../../include/hmd.h"
+
+namespace hmd {
+namespace {
+
+__device__ unsigned int g_err;
+
+constexpr int kPT = 64;               // tokens per page
+constexpr int kChooseThreads = 1024;
+constexpr int kWarps = kChooseThreads / 32;
+constexpr int kBins = 2048;           // 11 bits a digit
+constexpr int kCacheKeys = 49152;     // weights held in shared memory: 192 KiB
+constexpr int kMoveThreads = 256;
+constexpr int kRowsPerBlock = 64;     // rows moved by one CTA into other pages
+
+// Order-preserving integer of a weight; -0 is 0, and NaN comes above everything.
+__device__ __forceinline__ uint32_t order_key(float w) {
+    if (w != w) return 0xffffffffu;
+    const uint32_t u = __float_as_uint(w + 0.f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+struct Row {
+    int L, slot, n_keep, n_old, m;  // n_old: entries before the recent ones, m of them are kept
+    bool ok;
+};
+__device__ __forceinline__ Row row_of(const EvictArgs &a, int b) {
+    Row r;
+    r.L = a.seq_lens[b];
+    r.slot = a.slots ? a.slots[b] : b;
+    r.ok = r.L >= 0 && r.L <= a.max_seq_len && r.slot >= 0 && r.slot < a.n_slots;
+    if (!r.ok) r.L = 0;
+    r.n_keep = min(r.L, a.budget);
+    const int recent = min(r.L, a.recent);
+    r.n_old = r.L - recent;
+    r.m = r.n_keep - recent;
+    return r;
+}
+
+__global__ void __launch_bounds__(kChooseThreads, 1) evict_choose_kernel(const EvictArgs a) {
+    extern __shared__ uint32_t keys[];  // order keys of the first min(n_old, kCacheKeys) entries
+    __shared__ uint32_t hist[kBins];
+    __shared__ uint32_t warp_gt[kWarps], warp_eq[kWarps];
+    __shared__ uint32_t s_digit, s_left;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int b = blockIdx.x / a.Hkv, g = blockIdx.x - b * a.Hkv;
+    griddep_launch_dependents();
+    griddep_wait();  // the weights and lengths come from the steps before
+    const Row r = row_of(a, b);
+    if (!r.ok && tid == 0 && g == 0) {
+        const int L = a.seq_lens[b];
+        atomicOr(&g_err, (L < 0 || L > a.max_seq_len) ? HMD_DEVERR_SEQLEN : HMD_DEVERR_SLOT);
+    }
+    int32_t *kept = a.kept + ((size_t)b * a.Hkv + g) * a.budget;
+    for (int i = r.n_keep + tid; i < a.budget; i += kChooseThreads) kept[i] = -1;
+    for (int i = r.m + tid; i < r.n_keep; i += kChooseThreads) kept[i] = r.n_old + (i - r.m);
+    if (r.m == r.n_old) {  // nothing to evict
+        for (int i = tid; i < r.m; i += kChooseThreads) kept[i] = i;
+        return;
+    }
+    if (r.m == 0) return;  // the recent ones alone
+    const float *w = a.weights + ((size_t)r.slot * a.Hkv + g) * a.w_len;
+    const int n = r.n_old, n_cached = min(n, kCacheKeys);
+    auto key_at = [&](int i) { return i < n_cached ? keys[i] : order_key(w[i]); };
+    for (int i = tid; i < n_cached; i += kChooseThreads) keys[i] = order_key(w[i]);
+    // the m-th largest key: `left` of the keys that share the digits found so far are wanted
+    uint32_t prefix = 0, mask = 0, left = (uint32_t)r.m;
+#pragma unroll 1
+    for (int digit = 0; digit < 3; ++digit) {
+        const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+        const uint32_t bits = digit == 2 ? 0x3ffu : 0x7ffu;
+        for (int i = tid; i < kBins; i += kChooseThreads) hist[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kChooseThreads) {
+            const uint32_t k = key_at(i);
+            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & bits], 1u);
+        }
+        __syncthreads();
+        // counts from the largest digit down: thread t holds digits 2047 - 2t and 2046 - 2t
+        const uint32_t c0 = hist[kBins - 1 - 2 * tid], c1 = hist[kBins - 2 - 2 * tid];
+        uint32_t sum = c0 + c1;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += up;
+        }
+        if (lane == 31) warp_gt[warp] = sum;
+        __syncthreads();
+        uint32_t before = sum - c0 - c1;  // keys with a larger digit
+        for (int v = 0; v < warp; ++v) before += warp_gt[v];
+        if (before < left && left <= before + c0) {
+            s_digit = kBins - 1 - 2 * tid;
+            s_left = left - before;
+        } else if (before + c0 < left && left <= before + c0 + c1) {
+            s_digit = kBins - 2 - 2 * tid;
+            s_left = left - before - c0;
+        }
+        __syncthreads();
+        prefix |= s_digit << shift;
+        mask |= bits << shift;
+        left = s_left;
+    }
+    // each warp's stretch of whole 32-entry groups: count, scan over the warps, write
+    const int per_warp = ((n + 31) / 32 + kWarps - 1) / kWarps * 32;
+    const int i0 = min(n, warp * per_warp), i1 = min(n, i0 + per_warp);
+    uint32_t n_gt = 0, n_eq = 0;
+    for (int i = i0 + lane; i < i1; i += 32) {
+        const uint32_t k = key_at(i);
+        n_gt += k > prefix;
+        n_eq += k == prefix;
+    }
+    n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+    n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+    if (lane == 0) {
+        warp_gt[warp] = n_gt;
+        warp_eq[warp] = n_eq;
+    }
+    __syncthreads();
+    uint32_t gt = 0, eq = 0;  // keys above and at the threshold before this stretch
+    for (int v = 0; v < warp; ++v) {
+        gt += warp_gt[v];
+        eq += warp_eq[v];
+    }
+    for (int i = i0; i < i1; i += 32) {
+        const uint32_t k = i + lane < i1 ? key_at(i + lane) : 0u;
+        const uint32_t is_gt = __ballot_sync(0xffffffffu, i + lane < i1 && k > prefix);
+        const uint32_t is_eq = __ballot_sync(0xffffffffu, i + lane < i1 && k == prefix);
+        const uint32_t below = (1u << lane) - 1u;
+        const uint32_t my_gt = gt + __popc(is_gt & below), my_eq = eq + __popc(is_eq & below);
+        const bool take = ((is_gt >> lane) & 1u) || (((is_eq >> lane) & 1u) && my_eq < left);
+        if (take) kept[my_gt + min(my_eq, left)] = i + lane;
+        gt += __popc(is_gt);
+        eq += __popc(is_eq);
+    }
+}
+
+// Row address of position i under a table (nullptr and an error for a page outside the pool).
+__device__ __forceinline__ size_t row_index(const EvictArgs &a, const int32_t *table, int max_pages,
+                                            int b, int g, int i, bool &ok) {
+    const int lp = i / kPT;
+    const int pg = lp < max_pages ? table[(size_t)b * max_pages + lp] : -1;
+    ok = pg >= 0 && pg < a.n_pages;
+    if (!ok) atomicOr(&g_err, HMD_DEVERR_PAGE);
+    return ((size_t)pg * a.Hkv + g) * kPT + i % kPT;
+}
+
+// Into other pages: one CTA per (sequence, kv-head, 64 rows); d / 8 lanes carry a row of K and
+// the same row of V, 16 bytes each.
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int n_chunks,
+                                                                  bool move_weights) {
+    griddep_launch_dependents();
+    griddep_wait();  // kept is the choosing kernel's output
+    const int tid = threadIdx.x, bg = blockIdx.x / n_chunks, chunk = blockIdx.x - bg * n_chunks;
+    const int b = bg / a.Hkv, g = bg - b * a.Hkv;
+    const int32_t *kept = a.kept + (size_t)bg * a.budget;
+    if (g == 0 && chunk == 0 && tid == 0) a.new_lens[b] = row_of(a, b).n_keep;
+    const int row0 = chunk * kRowsPerBlock, lpr = a.d / 8, rows_at_once = kMoveThreads / lpr;
+    const int c = (tid % lpr) * 8;
+    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k_pool);
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_pool);
+#pragma unroll 4
+    for (int i = row0 + tid / lpr; i < min(row0 + kRowsPerBlock, a.budget); i += rows_at_once) {
+        const int j = kept[i];
+        if (j < 0) break;
+        bool ok_s, ok_d;
+        const size_t src = row_index(a, a.page_table, a.max_pages, b, g, j, ok_s) * a.d + c;
+        const size_t dst = row_index(a, a.dst_table, a.dst_max_pages, b, g, i, ok_d) * a.d + c;
+        if (!ok_s || !ok_d) continue;
+        const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(k + src));
+        const uint4 y = __ldcs(reinterpret_cast<const uint4 *>(v + src));
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.k_pool) + dst) = x;
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.v_pool) + dst) = y;
+    }
+    if (move_weights && tid < kRowsPerBlock && row0 + tid < a.budget) {
+        const int j = kept[row0 + tid];
+        const int slot = a.slots ? a.slots[b] : b;
+        if (j >= 0)
+            a.weights_out[((size_t)slot * a.Hkv + g) * a.w_out_len + row0 + tid] =
+                a.weights[((size_t)slot * a.Hkv + g) * a.w_len + j];
+    }
+}
+
+// Within the same pages: CTA (sequence, kv-head, column). Columns 0 .. d/32-1 are 64-byte
+// columns of K, the next d/32 of V, the last one the weights (if they are packed in place).
+__global__ void __launch_bounds__(kMoveThreads) evict_pack_kernel(const EvictArgs a, int n_cols,
+                                                                  bool pack_rows) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x, bg = blockIdx.x / n_cols, col = blockIdx.x - bg * n_cols;
+    const int b = bg / a.Hkv, g = bg - b * a.Hkv;
+    const int32_t *kept = a.kept + (size_t)bg * a.budget;
+    if (pack_rows && bg % a.Hkv == 0 && col == 0 && tid == 0) a.new_lens[b] = row_of(a, b).n_keep;
+    if (!pack_rows || col == a.d / 16) {  // the weights: 4-byte rows
+        const int slot = a.slots ? a.slots[b] : b;
+        if (slot < 0 || slot >= a.n_slots) return;  // reported by the choosing kernel
+        const float *w = a.weights + ((size_t)slot * a.Hkv + g) * a.w_len;
+        float *out = a.weights_out + ((size_t)slot * a.Hkv + g) * a.w_out_len;
+        for (int i0 = 0; i0 < a.budget; i0 += 4 * kMoveThreads) {
+            float x[4];
+            int j[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * kMoveThreads + tid;
+                j[u] = i < a.budget ? kept[i] : -1;
+                x[u] = j[u] >= 0 ? w[j[u]] : 0.f;
+            }
+            __syncthreads();  // every load of this block before any store into its sources
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (j[u] >= 0) out[i0 + u * kMoveThreads + tid] = x[u];
+        }
+        return;
+    }
+    const int cols = a.d / 32;
+    __nv_bfloat16 *pool = static_cast<__nv_bfloat16 *>(col < cols ? a.k_pool : a.v_pool);
+    const int c = (col % cols) * 32 + (tid & 3) * 8;
+    constexpr int kRows = kMoveThreads / 4, kUnroll = 8;
+    for (int i0 = 0; i0 < a.budget; i0 += kUnroll * kRows) {
+        uint4 x[kUnroll];
+        int j[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * kRows + tid / 4;
+            j[u] = i < a.budget ? kept[i] : -1;
+            if (j[u] == i) j[u] = -1;  // already there
+            if (j[u] >= 0) {
+                bool ok;
+                const size_t src = row_index(a, a.page_table, a.max_pages, b, g, j[u], ok);
+                if (ok) x[u] = *reinterpret_cast<const uint4 *>(pool + src * a.d + c);
+                else j[u] = -1;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (j[u] < 0) continue;
+            bool ok;
+            const size_t dst = row_index(a, a.page_table, a.max_pages, b, g,
+                                         i0 + u * kRows + tid / 4, ok);
+            if (ok) *reinterpret_cast<uint4 *>(pool + dst * a.d + c) = x[u];
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_evict(const EvictArgs &a, cudaStream_t s) {
+    const cudaError_t attr_err = once_per_device([] {
+        return cudaFuncSetAttribute(evict_choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kCacheKeys * 4);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    const int heads = a.B * a.Hkv;
+    const int smem = std::min(a.max_seq_len, kCacheKeys) * 4;
+    cudaError_t e = launch_pdl(evict_choose_kernel, dim3((unsigned)heads), dim3(kChooseThreads),
+                               (size_t)smem, s, a);
+    if (e != cudaSuccess) return e;
+    const bool same_pages = a.dst_table == a.page_table, same_weights = a.weights_out == a.weights;
+    if (!same_pages) {
+        const int keep = std::min(a.budget, a.max_seq_len);
+        const int n_chunks = (keep + kRowsPerBlock - 1) / kRowsPerBlock;
+        e = launch_pdl(evict_move_kernel, dim3((unsigned)(heads * n_chunks)), dim3(kMoveThreads), 0,
+                       s, a, n_chunks, !same_weights);
+        if (e != cudaSuccess || !same_weights) return e;
+        return launch_pdl(evict_pack_kernel, dim3((unsigned)heads), dim3(kMoveThreads), 0, s, a, 1,
+                          false);
+    }
+    // packing the weights in order is right whether or not weights_out is another buffer
+    const int n_cols = a.d / 16 + 1;
+    return launch_pdl(evict_pack_kernel, dim3((unsigned)(heads * n_cols)), dim3(kMoveThreads), 0, s,
+                      a, n_cols, true);
+}
+
+uint32_t kv_evict_read_errors(bool clear) {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_err, sizeof v) != cudaSuccess) return 0;
+    if (clear && v) {
+        const unsigned int z = 0;
+        cudaMemcpyToSymbol(g_err, &z, sizeof z);
+    }
+    return v;
+}
+
+}  // namespace hmd

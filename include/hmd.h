@@ -317,6 +317,62 @@ HMD_API hmd_status_t attn_decode_static_ws(hmd_kind_t kind, int window, int B, i
                                            int max_seq_len, void *o, hmd_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* Eviction by accumulated attention weight (FA caches). attn_verify_scored is the decode /    */
+/* verification step that also adds up, per sequence, kv-head and key, the softmax weight the */
+/* key has received; kv_cache_evict then keeps a sequence's most recent entries and the ones   */
+/* with the largest accumulated weight. The paper has no counterpart: it bounds the cache that */
+/* its FA layers grow with the context.                                                        */
+/* ------------------------------------------------------------------------------------------ */
+
+/* attn_verify (FA; n_q = 1 is the decode step) with the weights added up:
+ *   weights [n_slots][Hkv][w_len] fp32 (device), w_len >= max_seq_len; sequence b uses row
+ *   slots[b] (device int32; NULL: b). With p the softmax weights of the call, key j of kv-head g
+ *   gains sum over the n_q tokens and the group's query heads of p_j; the slots of the new tokens
+ *   (positions L - n_q .. L - 1) start from 0, so a fresh row needs no clearing beyond the
+ *   positions a prefill filled. Entries from L on are left as they were.
+ * No two sequences of a call may share a row. To count a prompt's last queries, prefill all but
+ * its last n_q tokens and run those through this call. A bad slot skips the sequence's weights
+ * and sets HMD_DEVERR_SLOT; o and the append are those of attn_verify, bit for bit.
+ *   workspace: at least attn_verify_scored_workspace_size(...) bytes (attn_verify's partials and
+ *   4 bytes per query row and key).
+ * Supported: as attn_verify.                                                                  */
+HMD_API size_t attn_verify_scored_workspace_size(int n_q, int B, int Hq, int Hkv, int d,
+                                                 int page_tokens, int max_seq_len);
+HMD_API hmd_status_t attn_verify_scored(int n_q, int B, int Hq, int Hkv, int d, int page_tokens,
+                                        const void *q, const void *new_k, const void *new_v,
+                                        void *k_pool, void *v_pool, int n_pages,
+                                        const int32_t *page_table, int max_pages,
+                                        const int32_t *seq_lens, int max_seq_len, float *weights,
+                                        int w_len, int n_slots, const int32_t *slots, void *o,
+                                        void *workspace, size_t ws_bytes, hmd_stream_t stream);
+
+/* Keeps min(L, budget) of the L = seq_lens[b] entries of every sequence: per kv-head the
+ * min(L, recent) last ones and, of the others, those with the largest weights (equal weights: the
+ * lowest position; a NaN counts as the largest), and packs them in their order.
+ *   weights [n_slots][Hkv][w_len], slots: as above; w_len >= max_seq_len.
+ *   kept [B][Hkv][budget] int32 (device, out): the position each entry came from, ascending; -1
+ *   from min(L, budget) on. new_lens [B] int32 (device, out): min(L, budget); may be seq_lens.
+ *   Entry kept[b][g][i] moves to position i under dst_table [B][dst_max_pages] (pages of the same
+ *   pools), its weight to weights_out[slot][g][i] (rows of w_out_len).
+ *   In place: dst_table == page_table (with dst_max_pages == max_pages), and, independently,
+ *   weights_out == weights (with w_out_len == w_len); pages shared between sequences must not be
+ *   packed in place. Otherwise no page of dst_table may hold an entry of any sequence of the
+ *   call, and weights_out may not overlap weights. Slots from min(L, budget) on keep what they
+ *   held. L = 0 is an empty row; a length outside [0, max_seq_len] or a bad slot sets the error
+ *   word, and the sequence comes out empty (new length 0, nothing moved); a bad page's rows are
+ *   not moved and set HMD_DEVERR_PAGE.
+ * Supported: bf16 pools, d in {64, 128}; page_tokens == 64; 0 <= recent <= budget, budget >= 1.
+ * Attention does not depend on the order of the keys, so decoding continues at new_lens[b] + 1.  */
+HMD_API hmd_status_t kv_cache_evict(int budget, int recent, int B, int Hkv, int d, int page_tokens,
+                                    void *k_pool, void *v_pool, int n_pages,
+                                    const int32_t *page_table, int max_pages,
+                                    const int32_t *seq_lens, int max_seq_len,
+                                    const float *weights, int w_len, int n_slots,
+                                    const int32_t *slots, const int32_t *dst_table,
+                                    int dst_max_pages, float *weights_out, int w_out_len,
+                                    int32_t *kept, int32_t *new_lens, hmd_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Caches and the placement dispatcher.                                                       */
 /* A placement selects one mixer per layer and can change between requests without reloading */
 /* weights (abstract; gist.science summary, section 2d "Inference and serving"). The library  */
