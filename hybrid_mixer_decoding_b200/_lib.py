@@ -70,6 +70,10 @@ _SIGS = {
     "kv_cache_evict": (_c_int, [_c_int] * 6 + [_vp, _vp, _c_int, _vp, _c_int, _vp, _c_int, _vp,
                                                _c_int, _c_int, _vp, _vp, _c_int, _vp, _c_int, _vp,
                                                _vp, _vp]),
+    "attn_latent_decode_workspace_size": (_sz, [_c_int] * 8),
+    "attn_latent_decode": (_c_int, [_c_int] * 7 + [_c_float, _vp, _vp, _vp, ctypes.c_int64, _vp,
+                                                 ctypes.c_int64, _vp, _c_int, _vp, _c_int, _vp,
+                                                 _c_int, _vp, _vp, _sz, _vp]),
     "attn_decode": (_c_int, [_c_int] * 7 + [_vp] * 5 + [_c_int, _vp, _c_int, _vp, _c_int, _vp,
                                                       _vp, _sz, _vp]),
     "attn_prefill": (_c_int, [_c_int] * 8 + [_vp] * 5 + [_c_int, _vp, _c_int, _vp, _vp]),
@@ -382,6 +386,48 @@ def kv_cache_evict(budget, recent, k_pool, v_pool, page_table, seq_lens, max_seq
                               _p(slots), _p(dst_table), dst_table.shape[1], _p(weights_out),
                               weights_out.shape[2], _p(kept), _p(new_lens), _stream(stream))
     _check("kv_cache_evict", st)
+
+
+def attn_latent_decode_workspace_size(n_q, B, H, d, d_c, d_r, page_tokens, max_seq_len) -> int:
+    return int(lib().attn_latent_decode_workspace_size(n_q, B, H, d, d_c, d_r, page_tokens,
+                                                       max_seq_len))
+
+
+def _latent_weights(H, d, d_c, w_uk, w_uv):
+    """Elements between heads of w_uk and w_uv [H,d,d_c]: each head's block is dense, the heads
+    may be further apart (slices of one [H,2d,d_c] projection)."""
+    for name, w in (("w_uk", w_uk), ("w_uv", w_uv)):
+        _shape(w, H, d, d_c, name=name)
+        if w.stride()[1:] != (d_c, 1):
+            raise ValueError(f"{name}: every head's [d,d_c] block must be contiguous")
+        _expect(torch.bfloat16, **{name: w[0]})
+    return max(w_uk.stride(0), d * d_c), max(w_uv.stride(0), d * d_c)
+
+
+def attn_latent_decode(q, new_c, w_uk, w_uv, pool, page_table, seq_lens, max_seq_len, o, workspace,
+                       scale=None, stream=None) -> None:
+    """Latent attention of n_q new tokens per sequence against the paged latent cache, absorbed
+    form (see include/hmd.h). q [B,n_q,H,d+64]; new_c [B,n_q,d_c+64]; w_uk,w_uv [H,d,d_c]; pool
+    [n_pages,64,d_c+64]; o [B,n_q,H,d]; scale None: 1 / sqrt(d + 64)."""
+    _expect(torch.bfloat16, q=q, new_c=new_c, pool=pool, o=o)
+    _expect(torch.int32, page_table=page_table, seq_lens=seq_lens)
+    _expect(workspace.dtype, workspace=workspace)
+    B, n_q, H, dq = q.shape
+    d, (n_pages, PT, row) = o.shape[-1], pool.shape
+    d_r = dq - d
+    d_c = row - d_r
+    _shape(o, B, n_q, H, d, name="o")
+    _shape(new_c, B, n_q, row, name="new_c")
+    _shape(page_table, B, None, name="page_table")
+    _shape(seq_lens, B, name="seq_lens")
+    uk, uv = _latent_weights(H, d, d_c, w_uk, w_uv)
+    st = lib().attn_latent_decode(n_q, B, H, d, d_c, d_r, PT,
+                                  dq ** -0.5 if scale is None else float(scale), _p(q), _p(new_c),
+                                  _p(w_uk), uk, _p(w_uv), uv, _p(pool), n_pages, _p(page_table),
+                                  page_table.shape[1], _p(seq_lens), int(max_seq_len), _p(o),
+                                  _p(workspace), workspace.numel() * workspace.element_size(),
+                                  _stream(stream))
+    _check("attn_latent_decode", st)
 
 
 def attn_decode_static_ws(kind, window, q, new_k, new_v, k_pool, v_pool, page_table, seq_lens,

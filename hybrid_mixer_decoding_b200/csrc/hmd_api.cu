@@ -122,7 +122,8 @@ hmd_status_t hmd_device_errors(hmd_stream_t stream, uint32_t *bits, int clear) {
     if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return fail(HMD_ERR_CUDA);
     *bits = hmd::delta_decode_read_errors(clear != 0) | hmd::attn_decode_read_errors(clear != 0) |
             hmd::delta_prefill_read_errors(clear != 0) | hmd::delta_prefill_scan_read_errors(clear != 0) |
-            hmd::attn_prefill_tc_read_errors(clear != 0) | hmd::kv_evict_read_errors(clear != 0);
+            hmd::attn_prefill_tc_read_errors(clear != 0) | hmd::kv_evict_read_errors(clear != 0) |
+            hmd::latent_decode_read_errors(clear != 0);
     return HMD_OK;
 }
 
@@ -514,6 +515,28 @@ hmd_status_t attn_decode(hmd_kind_t kind, int window, int B, int Hq, int Hkv, in
                        workspace, ws_bytes, stream);
 }
 
+}  // extern "C"
+
+namespace {
+// Sizes of a latent call against its table, weights and the launch limits.
+hmd_status_t latent_bounds(int B, long long tokens, int H, int d, int d_c, int page_tokens,
+                           int n_pages, int max_pages, long long max_len, int64_t w_uk_head,
+                           int64_t w_uv_head) {
+    if ((long long)max_pages * page_tokens < max_len) return HMD_ERR_SHAPE;
+    const long long w = (long long)d * d_c;
+    if (w_uk_head < w || w_uv_head < w || w_uk_head % 8 || w_uv_head % 8) return HMD_ERR_SHAPE;
+    // row coordinates, flat page counts and launch grids are 32-bit; heads and token blocks are
+    // grid dimensions
+    const long long pages = (max_len + page_tokens - 1) / page_tokens;
+    if ((long long)n_pages * page_tokens >= (1LL << 31) || B * pages >= (1LL << 31) ||
+        tokens * H >= (1LL << 31) || tokens >= (1LL << 19) || H > 65535)
+        return HMD_ERR_UNSUPPORTED;
+    return HMD_OK;
+}
+}  // namespace
+
+extern "C" {
+
 // ---- eviction by accumulated weight ------------------------------------------------------
 
 size_t attn_verify_scored_workspace_size(int n_q, int B, int Hq, int Hkv, int d, int page_tokens,
@@ -569,6 +592,47 @@ hmd_status_t kv_cache_evict(int budget, int recent, int B, int Hkv, int d, int p
     a.dst_table = dst_table; a.dst_max_pages = dst_max_pages; a.weights_out = weights_out;
     a.w_out_len = w_out_len; a.kept = kept; a.new_lens = new_lens;
     return from_cuda(hmd::launch_kv_evict(a, as_stream(stream)));
+}
+
+// ---- latent attention ----------------------------------------------------------------------
+
+size_t attn_latent_decode_workspace_size(int n_q, int B, int H, int d, int d_c, int d_r,
+                                         int page_tokens, int max_seq_len) {
+    if (n_q < 1 || B < 1 || H < 1 || max_seq_len < 1 ||
+        !hmd::latent_supported(d, d_c, d_r, page_tokens))
+        return 16;
+    return hmd::latent_decode_ws_bytes(n_q, B, H, d_c, max_seq_len);
+}
+
+hmd_status_t attn_latent_decode(int n_q, int B, int H, int d, int d_c, int d_r, int page_tokens,
+                                float scale, const void *q, const void *new_c, const void *w_uk,
+                                int64_t w_uk_head, const void *w_uv, int64_t w_uv_head,
+                                void *pool, int n_pages, const int32_t *page_table,
+                                int max_pages, const int32_t *seq_lens, int max_seq_len, void *o,
+                                void *workspace, size_t ws_bytes, hmd_stream_t stream) {
+    if (n_q < 1 || B < 0 || H < 1 || d < 1 || d_c < 1 || d_r < 1 || page_tokens < 1 ||
+        n_pages < 1 || max_pages < 1 || max_seq_len < 1)
+        return fail(HMD_ERR_SHAPE);
+    if (B == 0) return HMD_OK;
+    if (!q || !new_c || !w_uk || !w_uv || !pool || !page_table || !seq_lens || !o || !workspace)
+        return fail(HMD_ERR_ARG);
+    if (!(scale > 0.f && scale <= 3.0e38f)) return fail(HMD_ERR_ARG);
+    if (!hmd::latent_supported(d, d_c, d_r, page_tokens)) return fail(HMD_ERR_UNSUPPORTED);
+    const hmd_status_t st = latent_bounds(B, (long long)n_q * B, H, d, d_c, page_tokens, n_pages,
+                                          max_pages, max_seq_len, w_uk_head, w_uv_head);
+    if (st != HMD_OK) return fail(st);
+    if (!aligned16(q) || !aligned16(new_c) || !aligned16(w_uk) || !aligned16(w_uv) ||
+        !aligned16(pool) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(o) & 3u))
+        return fail(HMD_ERR_ARG);
+    if (ws_bytes < hmd::latent_decode_ws_bytes(n_q, B, H, d_c, max_seq_len))
+        return fail(HMD_ERR_SHAPE);
+    hmd::LatentDecodeArgs a{};
+    a.nq = n_q; a.B = B; a.H = H; a.d = d; a.d_c = d_c; a.scale = scale;
+    a.q = q; a.new_c = new_c; a.w_uk = w_uk; a.w_uv = w_uv;
+    a.w_uk_head = w_uk_head; a.w_uv_head = w_uv_head;
+    a.pool = pool; a.n_pages = n_pages; a.page_table = page_table; a.max_pages = max_pages;
+    a.seq_lens = seq_lens; a.max_seq_len = max_seq_len; a.o = o; a.workspace = workspace;
+    return from_cuda(hmd::launch_latent_decode(a, as_stream(stream)));
 }
 
 // ---- caches ------------------------------------------------------------------------------

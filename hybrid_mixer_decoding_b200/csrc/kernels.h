@@ -202,6 +202,26 @@ struct EvictArgs {
 cudaError_t launch_kv_evict(const EvictArgs &a, cudaStream_t s);
 uint32_t kv_evict_read_errors(bool clear);
 
+// Latent attention (latent_decode.cu, latent_prefill.cu): see attn_latent_* in hmd.h.
+struct LatentDecodeArgs {
+    int nq, B, H, d, d_c;
+    float scale;
+    const void *q, *new_c, *w_uk, *w_uv;
+    long long w_uk_head, w_uv_head;  // elements from one head's weights to the next
+    void *pool;
+    int n_pages;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *seq_lens;
+    int max_seq_len;
+    void *o;
+    void *workspace;
+};
+bool latent_supported(int d, int d_c, int d_r, int page_tokens);
+size_t latent_decode_ws_bytes(int nq, int B, int H, int d_c, int max_seq_len);
+cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t s);
+uint32_t latent_decode_read_errors(bool clear);
+
 struct DeltaPrefillArgs {
     int kind;
     int B, T, H, dk, dv;

@@ -373,6 +373,46 @@ HMD_API hmd_status_t kv_cache_evict(int budget, int recent, int B, int Hkv, int 
                                     int32_t *kept, int32_t *new_lens, hmd_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* Latent attention: keys and values of all H heads from one shared vector a token. A cached   */
+/* token is one row [c (d_c) ; k_r (d_r)]; head h's key is [W_uk[h] c ; k_r] and its value     */
+/* W_uv[h] c, its query [q_n (d) ; q_r (d_r)]: position j gets the score                       */
+/* scale * (q_n . W_uk[h] c_j + q_r . k_rj), softmax over j <= the query's position. Any        */
+/* positional rotation of q_r and k_r is the caller's. The paper has no counterpart: it is the  */
+/* full-attention mixer with a cache of (d_c + d_r) * 2 bytes a token instead of               */
+/* 4 * Hkv * d.                                                                               */
+/* Pool [n_pages][page_tokens][d_c + d_r] bf16: position p of sequence b is row                */
+/* p % page_tokens of page page_table[b][p / page_tokens]. W_uk, W_uv: [H] blocks of [d][d_c]   */
+/* bf16, consecutive heads w_uk_head (w_uv_head) elements apart (multiples of 8, >= d * d_c), so  */
+/* that one [H][2 d][d_c] projection can hold both.                                            */
+/* Supported: d in {64, 128}; d_c in {128, 256, 384, 512}; d_r == 64; page_tokens == 64; any H.  */
+/* ------------------------------------------------------------------------------------------ */
+
+/* Absorbed form, n_q new tokens per sequence (n_q = 1: the decode step): appends their rows and
+ * attends as attn_verify does (token i sits at position L - n_q + i), reading the cache once for
+ * all heads and tokens.
+ *   q [B][n_q][H][d + d_r]; new_c [B][n_q][d_c + d_r]; o [B][n_q][H][d], all bf16.
+ *   seq_lens [B] int32 (device), each in [n_q, max_seq_len], or 0: an unused row of the batch
+ *   (nothing is appended, its o is zero). Another length does the same and sets
+ *   HMD_DEVERR_SEQLEN. scale: usually 1 / sqrt(d + d_r).
+ *   A page outside the pool sets HMD_DEVERR_PAGE and its keys are left out. Cached rows must be
+ *   finite; rows behind a sequence may hold anything.
+ *   workspace: at least attn_latent_decode_workspace_size(...) bytes (0 is never returned; the
+ *   figure follows the launch plan for exactly these arguments), not in use by another call
+ *   while this one runs. Allocates nothing.
+ * q, new_c, the weights, pool and workspace 16-byte aligned, o 4-byte aligned. The queries on the
+ * latent and the latent output are carried as bf16 pairs (16 bits), the softmax weights are
+ * rounded to bf16 before their product with c; sums are fp32.                                   */
+HMD_API size_t attn_latent_decode_workspace_size(int n_q, int B, int H, int d, int d_c, int d_r,
+                                                 int page_tokens, int max_seq_len);
+HMD_API hmd_status_t attn_latent_decode(int n_q, int B, int H, int d, int d_c, int d_r,
+                                        int page_tokens, float scale, const void *q,
+                                        const void *new_c, const void *w_uk, int64_t w_uk_head,
+                                        const void *w_uv, int64_t w_uv_head, void *pool,
+                                        int n_pages, const int32_t *page_table, int max_pages,
+                                        const int32_t *seq_lens, int max_seq_len, void *o,
+                                        void *workspace, size_t ws_bytes, hmd_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Caches and the placement dispatcher.                                                       */
 /* A placement selects one mixer per layer and can change between requests without reloading */
 /* weights (abstract; gist.science summary, section 2d "Inference and serving"). The library  */

@@ -1,0 +1,210 @@
+"""attn_latent_decode on the GPU against the expanded definition in 64 bits.
+
+Tolerance: o is rounded once to bf16 (2^-8 of the value) and its softmax weights are rounded to bf16
+(2^-8 of sum_j p_j |v_j|, with |v_j| <= |W_uv| |c_j|). The query on the latent and the latent
+output are bf16 pairs (2^-17 relative), which with fp32 sums moves a score by at most
+2^-15 * sum|terms|: 2^-14 * that more on sum_j p_j |v_j|.
+"""
+import pytest
+import torch
+
+import hybrid_mixer_decoding_b200 as hmd
+
+pytestmark = pytest.mark.gpu
+PT, DR = 64, 64
+BF = torch.bfloat16
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+class Latent:
+    """A batch's paged latent cache in random order, the rows behind each sequence NaN."""
+
+    def __init__(self, lens, H, d, d_c, seed, max_len=None, w_scale=1.0, joint=False):
+        g = self.g = torch.Generator(device="cuda").manual_seed(seed)
+        self.lens_list, self.H, self.d, self.d_c = list(lens), H, d, d_c
+        B, self.max_len = len(lens), max_len or max(1, max(lens))
+        per = -(-self.max_len // PT)
+        self.table = torch.randperm(B * per, generator=g, device="cuda").to(torch.int32).view(B, per)
+        self.pool = self.randn(B * per, PT, d_c + DR)
+        for b, L in enumerate(lens):
+            t = self.table[b].long()
+            self.pool[t[-(-L // PT):]] = float("nan")
+            if L % PT:
+                self.pool[t[L // PT], L % PT:] = float("nan")
+        if joint:  # both up-projections as slices of one weight
+            w = self.randn(H, 2 * d, d_c, scale=w_scale * d_c ** -0.5)
+            self.w_uk, self.w_uv = w[:, :d], w[:, d:]
+        else:
+            self.w_uk = self.randn(H, d, d_c, scale=w_scale * d_c ** -0.5)
+            self.w_uv = self.randn(H, d, d_c, scale=d_c ** -0.5)
+        self.lens = i32(self.lens_list)
+
+    def randn(self, *s, scale=1.0):
+        return (torch.randn(*s, generator=self.g, device="cuda") * scale).to(BF)
+
+    def rows(self, b, n):
+        return self.pool[self.table[b].long()].reshape(-1, self.d_c + DR)[:n]
+
+    def workspace(self, nq):
+        return torch.empty(hmd.attn_latent_decode_workspace_size(
+            nq, len(self.lens_list), self.H, self.d, self.d_c, DR, PT, self.max_len),
+            dtype=torch.uint8, device="cuda")
+
+    def decode(self, q, new_c, scale=None, ws=None, o=None):
+        o = torch.full((*q.shape[:3], self.d), 9.0, device="cuda", dtype=BF) if o is None else o
+        hmd.attn_latent_decode(q, new_c, self.w_uk, self.w_uv, self.pool, self.table, self.lens,
+                               self.max_len, o, self.workspace(q.shape[1]) if ws is None else ws,
+                               scale=scale)
+        return o
+
+    def new(self, nq):
+        B = len(self.lens_list)
+        return self.randn(B, nq, self.H, self.d + DR), self.randn(B, nq, self.d_c + DR)
+
+
+def reference(c, b, C, q, first, scale):
+    """o [n, H, d] and its tolerance for n queries from position `first` over the rows C."""
+    n, C = q.shape[0], C.double()
+    hidden = torch.arange(len(C), device="cuda")[None] > first + torch.arange(n, device="cuda")[:, None]
+    K = torch.einsum("jc,hnc->hjn", C[:, :c.d_c], c.w_uk.double())
+    V = torch.einsum("jc,hvc->hjv", C[:, :c.d_c], c.w_uv.double())
+    Va = torch.einsum("jc,hvc->hjv", C[:, :c.d_c].abs(), c.w_uv.double().abs())
+    qn, qr = q.double().transpose(0, 1).split([c.d, DR], -1)  # [H, n, .]
+    x = (qn @ K.transpose(1, 2) + qr @ C[:, c.d_c:].T) * scale
+    terms = (qn.abs() @ torch.einsum("jc,hnc->hjn", C[:, :c.d_c].abs(), c.w_uk.double().abs()).transpose(1, 2)
+             + qr.abs() @ C[:, c.d_c:].abs().T).amax() * scale
+    p = torch.softmax(x.masked_fill(hidden, -torch.inf), -1)
+    ref = (p @ V).transpose(0, 1)
+    # the weights' rounding acts on p_j c_j, 512 dims of which W_uv mixes: |W_uv| |c| bounds |v|, and
+    # independent roundings average; the bound without averaging is the one used
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -14 * terms) * (p @ Va).transpose(0, 1)
+    rms = (p ** 2 @ V ** 2).sqrt().transpose(0, 1)  # independent roundings of the keys' weights
+    return ref, tol, rms
+
+
+def check_decode(c, q, new_c, o, scale=None):
+    nq = q.shape[1]
+    scale = (c.d + DR) ** -0.5 if scale is None else scale
+    for b, L in enumerate(c.lens_list):
+        if L == 0:
+            assert (o[b] == 0).all()
+            continue
+        C = c.rows(b, L)
+        assert torch.equal(C[L - nq:], new_c[b])  # the append
+        ref, tol, rms = reference(c, b, C, q[b], L - nq, scale)
+        err = (o[b].double() - ref).abs()
+        assert (err <= tol).all(), (b, L, (err / tol).max().item())
+        # and far inside it on the whole: the output's rounding, and the weights' at random signs
+        typical = (2.0 ** -8 * ref.abs() + 2.0 ** -8 * rms).square().mean().sqrt()
+        assert err.square().mean().sqrt() <= typical
+
+
+@pytest.mark.parametrize("H,d,d_c,nq", [(16, 128, 512, 1), (32, 128, 512, 1), (5, 64, 256, 1),
+                                        (16, 64, 128, 2), (20, 128, 384, 3), (40, 64, 512, 2),
+                                        (1, 128, 256, 4), (33, 64, 128, 1), (32, 128, 512, 4)])
+def test_decode_ragged(H, d, d_c, nq):
+    lens = [max(nq, n) for n in (1, 2, 63, 64, 65, 127, 128, 129, 300, 1000, 4, 777)]
+    c = Latent(lens, H, d, d_c, seed=H + nq, max_len=1100)
+    q, new_c = c.new(nq)
+    before = c.pool.clone()
+    o = c.decode(q, new_c)
+    check_decode(c, q, new_c, o)
+    for b, L in enumerate(lens):  # nothing else of the pool changed
+        for i in range(nq):
+            before[c.table[b, (L - nq + i) // PT], (L - nq + i) % PT] = new_c[b, i]
+    assert torch.equal(before.view(torch.int16), c.pool.view(torch.int16))
+    assert hmd.hmd_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("B,L", [(1, 1), (1, 65), (1, 20000), (2, 30011), (150, 70), (300, 1)])
+def test_decode_batches_and_lengths(B, L):
+    lens = [max(1, L - 13 * b) for b in range(B)]
+    c = Latent(lens, 8, 64, 256, seed=B)
+    q, new_c = c.new(1)
+    check_decode(c, q, new_c, c.decode(q, new_c))
+    assert hmd.hmd_device_errors(clear=True) == 0
+
+
+def test_decode_unused_rows_and_a_bad_length():
+    c = Latent([0, 130, 0, 0, 64, 0], 16, 128, 512, seed=1, max_len=200)
+    q, new_c = c.new(2)
+    check_decode(c, q, new_c, c.decode(q, new_c))
+    assert hmd.hmd_device_errors(clear=True) == 0
+    c.lens[1] = 201
+    o = c.decode(q, new_c)
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVERR_SEQLEN
+    assert (o[1] == 0).all()
+    c.lens[1] = 1  # shorter than the new tokens
+    o = c.decode(q, new_c)
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVERR_SEQLEN
+    c.lens_list[1], c.lens[1] = 130, 130
+    c.lens.zero_()
+    assert (c.decode(q, new_c) == 0).all()
+    assert hmd.hmd_device_errors(clear=True) == 0
+
+
+def test_decode_leaves_out_a_bad_page():
+    c = Latent([300], 16, 128, 512, seed=2)
+    q, new_c = c.new(1)
+    c.table[0, 1] = -5
+    o = c.decode(q, new_c)
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVERR_PAGE
+    good = torch.cat([torch.arange(64), torch.arange(128, 300)]).cuda()
+    t = c.table[0].long().clone()
+    t[1] = 0
+    C = c.pool[t].reshape(-1, 576)[:300][good]
+    ref, tol, _ = reference(c, 0, C, q[0], len(C) - 1, 192 ** -0.5)
+    assert ((o[0].double() - ref).abs() <= tol).all()
+
+
+def test_decode_steep_softmax_joint_weights_and_scale():
+    """Large scores that grow along the sequence (the exponent base moves again and again), weights
+    that are slices of one projection, an explicit scale."""
+    c = Latent([900, 333], 16, 128, 512, seed=3, w_scale=4.0, joint=True)
+    ramp = torch.linspace(0.02, 3.0, c.max_len, device="cuda")
+    for b, L in enumerate(c.lens_list):
+        pos = torch.arange(L, device="cuda")
+        c.pool[c.table[b].long()[pos // PT], pos % PT] *= ramp[:L, None].to(BF)
+    q, new_c = c.new(1)
+    check_decode(c, q, new_c, c.decode(q, new_c, scale=0.2), scale=0.2)
+
+
+def test_decode_is_deterministic_and_captured():
+    c = Latent([500, 80, 1000], 32, 128, 512, seed=4, max_len=1024)
+    q, new_c = c.new(1)
+    ws, o = c.workspace(1), torch.empty(3, 1, 32, 128, device="cuda", dtype=BF)
+    ws.fill_(0xff)  # NaN everywhere: nothing is read before it is written
+    c.decode(q, new_c, ws=ws, o=o)
+    ref = o.clone()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            c.decode(q, new_c, ws=ws, o=o)
+            c.decode(q, new_c, ws=ws, o=o)
+    o.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, ref)
+    # the captured call follows lengths changed on the device
+    c.lens_list = [400, 64, 7]
+    c.lens.copy_(i32(c.lens_list))
+    g.replay()
+    torch.cuda.synchronize()
+    check_decode(c, q, new_c, o)
+
+
+def test_verify_equals_successive_decode_steps():
+    nq = 3
+    c = Latent([200, 64, 131], 16, 128, 512, seed=5)
+    q, new_c = c.new(nq)
+    pool = c.pool.clone()
+    o = c.decode(q, new_c)
+    c.pool.copy_(pool)
+    for i in range(nq):
+        c.lens.copy_(i32([L - nq + 1 + i for L in c.lens_list]))
+        oi = c.decode(q[:, i:i + 1].contiguous(), new_c[:, i:i + 1].contiguous())
+        assert (oi[:, 0].double() - o[:, i].double()).abs().max() <= 2.0 ** -6 * o.double().abs().max()
