@@ -16,6 +16,7 @@ STATUS = {0: "HMD_OK", 1: "HMD_ERR_ARG", 2: "HMD_ERR_SHAPE", 3: "HMD_ERR_DTYPE",
           4: "HMD_ERR_OOM", 5: "HMD_ERR_CUDA", 6: "HMD_ERR_UNSUPPORTED",
           7: "HMD_ERR_DEVICE_CHECK"}
 DEVERR_TIMEOUT, DEVERR_PAGE, DEVERR_SLOT, DEVERR_SEQLEN, DEVERR_GATE = 0x1, 0x2, 0x4, 0x8, 0x10
+DEVWARN_RANGE = 0x20
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhmd.so")
 _lib = None
@@ -74,6 +75,10 @@ _SIGS = {
     "attn_latent_decode": (_c_int, [_c_int] * 7 + [_c_float, _vp, _vp, _vp, ctypes.c_int64, _vp,
                                                  ctypes.c_int64, _vp, _c_int, _vp, _c_int, _vp,
                                                  _c_int, _vp, _vp, _sz, _vp]),
+    "attn_latent_prefill_workspace_size": (_sz, [_c_int] * 8),
+    "attn_latent_prefill": (_c_int, [_c_int] * 7 + [_c_float, _vp, _vp, _vp, ctypes.c_int64, _vp,
+                                                  ctypes.c_int64, _vp, _c_int, _vp, _vp, _c_int,
+                                                  _vp, _c_int, _vp, _vp, _sz, _vp]),
     "attn_decode": (_c_int, [_c_int] * 7 + [_vp] * 5 + [_c_int, _vp, _c_int, _vp, _c_int, _vp,
                                                       _vp, _sz, _vp]),
     "attn_prefill": (_c_int, [_c_int] * 8 + [_vp] * 5 + [_c_int, _vp, _c_int, _vp, _vp]),
@@ -400,8 +405,10 @@ def _latent_weights(H, d, d_c, w_uk, w_uv):
         _shape(w, H, d, d_c, name=name)
         if w.stride()[1:] != (d_c, 1):
             raise ValueError(f"{name}: every head's [d,d_c] block must be contiguous")
+        if H > 1 and w.stride(0) < d * d_c:
+            raise ValueError(f"{name}: the heads' blocks must not overlap")
         _expect(torch.bfloat16, **{name: w[0]})
-    return max(w_uk.stride(0), d * d_c), max(w_uv.stride(0), d * d_c)
+    return tuple(w.stride(0) if H > 1 else d * d_c for w in (w_uk, w_uv))
 
 
 def attn_latent_decode(q, new_c, w_uk, w_uv, pool, page_table, seq_lens, max_seq_len, o, workspace,
@@ -428,6 +435,39 @@ def attn_latent_decode(q, new_c, w_uk, w_uv, pool, page_table, seq_lens, max_seq
                                   _p(workspace), workspace.numel() * workspace.element_size(),
                                   _stream(stream))
     _check("attn_latent_decode", st)
+
+
+def attn_latent_prefill_workspace_size(B, T, H, d, d_c, d_r, page_tokens, max_prefix=0) -> int:
+    return int(lib().attn_latent_prefill_workspace_size(B, T, H, d, d_c, d_r, page_tokens,
+                                                        max_prefix))
+
+
+def attn_latent_prefill(q, c, w_uk, w_uv, pool, page_table, o, workspace, prefix_lens=None,
+                        max_prefix=0, prompt_lens=None, scale=None, stream=None) -> None:
+    """Latent attention of prompts after a cached prefix (or none), expanded form (see
+    include/hmd.h). q [B,T,H,d+64]; c [B,T,d_c+64]; w_uk,w_uv [H,d,d_c]; pool
+    [n_pages,64,d_c+64]; o [B,T,H,d]; prefix_lens, prompt_lens int32 [B] or None; scale None:
+    1 / sqrt(d + 64)."""
+    _expect(torch.bfloat16, q=q, c=c, pool=pool, o=o)
+    _expect(torch.int32, page_table=page_table, prefix_lens=prefix_lens, prompt_lens=prompt_lens)
+    _expect(workspace.dtype, workspace=workspace)
+    B, T, H, dq = q.shape
+    d, (n_pages, PT, row) = o.shape[-1], pool.shape
+    d_r = dq - d
+    d_c = row - d_r
+    _shape(o, B, T, H, d, name="o")
+    _shape(c, B, T, row, name="c")
+    _shape(page_table, B, None, name="page_table")
+    _shape(prefix_lens, B, name="prefix_lens")
+    _shape(prompt_lens, B, name="prompt_lens")
+    uk, uv = _latent_weights(H, d, d_c, w_uk, w_uv)
+    st = lib().attn_latent_prefill(B, T, H, d, d_c, d_r, PT,
+                                   dq ** -0.5 if scale is None else float(scale), _p(q), _p(c),
+                                   _p(w_uk), uk, _p(w_uv), uv, _p(prefix_lens), int(max_prefix),
+                                   _p(prompt_lens), _p(pool), n_pages, _p(page_table),
+                                   page_table.shape[1], _p(o), _p(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("attn_latent_prefill", st)
 
 
 def attn_decode_static_ws(kind, window, q, new_k, new_v, k_pool, v_pool, page_table, seq_lens,

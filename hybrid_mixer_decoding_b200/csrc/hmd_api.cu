@@ -123,7 +123,8 @@ hmd_status_t hmd_device_errors(hmd_stream_t stream, uint32_t *bits, int clear) {
     *bits = hmd::delta_decode_read_errors(clear != 0) | hmd::attn_decode_read_errors(clear != 0) |
             hmd::delta_prefill_read_errors(clear != 0) | hmd::delta_prefill_scan_read_errors(clear != 0) |
             hmd::attn_prefill_tc_read_errors(clear != 0) | hmd::kv_evict_read_errors(clear != 0) |
-            hmd::latent_decode_read_errors(clear != 0);
+            hmd::latent_decode_read_errors(clear != 0) |
+            hmd::latent_prefill_read_errors(clear != 0);
     return HMD_OK;
 }
 
@@ -633,6 +634,52 @@ hmd_status_t attn_latent_decode(int n_q, int B, int H, int d, int d_c, int d_r, 
     a.pool = pool; a.n_pages = n_pages; a.page_table = page_table; a.max_pages = max_pages;
     a.seq_lens = seq_lens; a.max_seq_len = max_seq_len; a.o = o; a.workspace = workspace;
     return from_cuda(hmd::launch_latent_decode(a, as_stream(stream)));
+}
+
+size_t attn_latent_prefill_workspace_size(int B, int T, int H, int d, int d_c, int d_r,
+                                          int page_tokens, int max_prefix) {
+    if (B < 1 || T < 1 || H < 1 || max_prefix < 0 ||
+        !hmd::latent_supported(d, d_c, d_r, page_tokens))
+        return 16;
+    return hmd::latent_prefill_ws_bytes(B, T, H, d, max_prefix);
+}
+
+hmd_status_t attn_latent_prefill(int B, int T, int H, int d, int d_c, int d_r, int page_tokens,
+                                 float scale, const void *q, const void *c, const void *w_uk,
+                                 int64_t w_uk_head, const void *w_uv, int64_t w_uv_head,
+                                 const int32_t *prefix_lens, int max_prefix,
+                                 const int32_t *prompt_lens, void *pool, int n_pages,
+                                 const int32_t *page_table, int max_pages, void *o,
+                                 void *workspace, size_t ws_bytes, hmd_stream_t stream) {
+    if (B < 0 || T < 0 || H < 1 || d < 1 || d_c < 1 || d_r < 1 || page_tokens < 1 ||
+        n_pages < 1 || max_pages < 1 || max_prefix < 0)
+        return fail(HMD_ERR_SHAPE);
+    if (B == 0 || T == 0) return HMD_OK;
+    if (!q || !c || !w_uk || !w_uv || !pool || !page_table || !o || !workspace)
+        return fail(HMD_ERR_ARG);
+    if (!(scale > 0.f && scale <= 3.0e38f)) return fail(HMD_ERR_ARG);
+    if (!hmd::latent_supported(d, d_c, d_r, page_tokens)) return fail(HMD_ERR_UNSUPPORTED);
+    if (!prefix_lens) max_prefix = 0;
+    const long long span = (long long)T + max_prefix;
+    const hmd_status_t st = latent_bounds(B, 0, H, d, d_c, page_tokens, n_pages, max_pages, span,
+                                          w_uk_head, w_uv_head);
+    if (st != HMD_OK) return fail(st);
+    // positions, tensor-map rows and grids are 32-bit
+    if (span >= (1LL << 30) || (span / 128 + 1) * B * H >= (1LL << 31) ||
+        span * B >= (1LL << 31))
+        return fail(HMD_ERR_UNSUPPORTED);
+    if (!aligned16(q) || !aligned16(c) || !aligned16(w_uk) || !aligned16(w_uv) ||
+        !aligned16(pool) || !aligned16(workspace) || !aligned16(o))
+        return fail(HMD_ERR_ARG);
+    if (ws_bytes < hmd::latent_prefill_ws_bytes(B, T, 1, d, max_prefix)) return fail(HMD_ERR_SHAPE);
+    hmd::LatentPrefillArgs a{};
+    a.B = B; a.T = T; a.H = H; a.d = d; a.d_c = d_c; a.scale = scale;
+    a.q = q; a.c = c; a.w_uk = w_uk; a.w_uv = w_uv;
+    a.w_uk_head = w_uk_head; a.w_uv_head = w_uv_head;
+    a.prefix_lens = prefix_lens; a.max_prefix = max_prefix; a.prompt_lens = prompt_lens;
+    a.pool = pool; a.n_pages = n_pages; a.page_table = page_table; a.max_pages = max_pages;
+    a.o = o; a.workspace = workspace; a.ws_bytes = ws_bytes;
+    return from_cuda(hmd::launch_latent_prefill(a, as_stream(stream)));
 }
 
 // ---- caches ------------------------------------------------------------------------------

@@ -92,6 +92,9 @@ bool make_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, int esize, void *base,
 bool make_tmap_tokens_sw128(CUtensorMap *m, void *base, long long n_tok, int heads, int d);
 bool make_tmap_bthd(CUtensorMap *m, CUtensorMapDataType dt, int esize, const void *base, int B,
                     int T, int H, int d, int box_d, bool sw128);
+bool make_tmap_blocks_sw128(CUtensorMap *m, CUtensorMapDataType dt, const void *base,
+                            long long heads, long long head_stride, long long rows, int cols,
+                            int box_rows);
 bool make_tmap_pool_sw128(CUtensorMap *m, void *pool, int n_pages, int heads, int d);
 
 // Input activations of the delta-rule mixers, fused into their kernels when A_log is set: the
@@ -221,6 +224,27 @@ bool latent_supported(int d, int d_c, int d_r, int page_tokens);
 size_t latent_decode_ws_bytes(int nq, int B, int H, int d_c, int max_seq_len);
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t s);
 uint32_t latent_decode_read_errors(bool clear);
+
+struct LatentPrefillArgs {
+    int B, T, H, d, d_c;
+    float scale;
+    const void *q, *c, *w_uk, *w_uv;
+    long long w_uk_head, w_uv_head;
+    const int32_t *prefix_lens;  // NULL: none
+    int max_prefix;
+    const int32_t *prompt_lens;  // NULL: T everywhere
+    void *pool;
+    int n_pages;
+    const int32_t *page_table;
+    int max_pages;
+    void *o;
+    void *workspace;
+    size_t ws_bytes;
+};
+// bytes for `heads` heads at once (the call runs in groups of as many heads as fit)
+size_t latent_prefill_ws_bytes(int B, int T, int heads, int d, int max_prefix);
+cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t s);
+uint32_t latent_prefill_read_errors(bool clear);
 
 struct DeltaPrefillArgs {
     int kind;

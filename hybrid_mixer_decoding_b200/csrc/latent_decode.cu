@@ -34,6 +34,7 @@
 
 #include "kernels.h"
 #include "ptx.cuh"
+#include "softmax.cuh"
 #include "../../include/hmd.h"
 
 namespace hmd {
@@ -279,19 +280,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
-}
-// Bounded wait that also gives up as soon as another thread of the CTA raised `abort`.
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int *abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            *abort = 1;
-            return false;
-        }
-    }
 }
 // 16 lanes x 64 columns of TMEM words: register 4j + e of thread t holds lane (base + t / 4 +
 // 8 (e / 2)), column 8j + 2 (t % 4) + e % 2.

@@ -1,0 +1,737 @@
+// Latent attention, expanded form: the new tokens of prompts, after a cached prefix or none.
+//
+// A cached token is one row [c (d_c) ; k_r (64)] shared by every head; head h's key is
+// [W_uk[h] c ; k_r], its value W_uv[h] c. With many queries per key the expanded form does the
+// least arithmetic (2 d + 64 products a (query, key) pair and head, against 2 d_c + 64 absorbed), so
+// every key and value is formed once, into a workspace, and attended as usual. It is bound by the
+// tensor cores: attention's products, and 4 d d_c flop per (token, head) to expand.
+//
+// The intermediate keys, values, queries and softmax weights are fp16, not bf16: rounding keys,
+// values and weights to bf16 would each add the error of the bf16 output itself; fp16's 2^-12 adds
+// nothing visible. Its range is 65504: larger keys, values or queries are clipped and reported
+// (HMD_DEVWARN_RANGE).
+//
+// Kernel 1 (rows): appends the new rows to the cache and converts every position's shared part
+// k_r to fp16. Kernel 2 (expand): one CTA per (128 positions, a share of the heads): the latent
+// rows stay in shared memory, the heads' weights stream through a ring; per head
+//     [K_h ; V_h] [128 x 2d] = C [128 x d_c] [W_uk[h] ; W_uv[h]]^T     tcgen05, M = 128, N = 2d
+// with two accumulators in TMEM, so one head's results are stored while the next is computed.
+// Kernel 3 (attend): one CTA per (sequence, head, 256 queries): two query tiles of 128 whose
+// softmax groups alternate with the tensor core, as in the FA prefill; K tiles are d/64 + 1
+// blocks (the last one k_r, shared by the heads), V tiles d/64, all in one ring of blocks.
+// If the workspace holds fewer heads than H, kernels 2 and 3 run once per group of heads.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "ptx.cuh"
+#include "softmax.cuh"
+#include "../../include/hmd.h"
+
+namespace hmd {
+namespace {
+
+__device__ unsigned int g_err;
+
+constexpr int kPT = 64;              // tokens per page
+constexpr int kDR = 64;              // the rows' part shared as it is by every head's key
+constexpr int kTile = 128;           // positions per key tile, queries per query tile
+constexpr uint32_t kBlk = kTile * 128;  // one [128 rows][128 B] block, 128-byte swizzle
+constexpr float kHalfMax = 65504.f;
+constexpr float kLazy = 8.f;         // log2 headroom before a row's exponent base moves
+
+// Instruction descriptor of kind::f16 with fp16 A/B and fp32 D: the bf16 one with both type fields 0.
+constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
+    return idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// Clips to fp16's range; true if anything was outside it.
+__device__ __forceinline__ bool clip_half(float &x) {
+    const bool out = fabsf(x) > kHalfMax;
+    if (out) x = copysignf(kHalfMax, x);
+    return out;
+}
+
+struct PrefillParams {
+    const __nv_bfloat16 *q, *c;
+    __nv_bfloat16 *pool, *o;
+    const int32_t *prefix_lens, *prompt_lens, *page_table;
+    int B, T, H, dc, max_prefix, n_pages, max_pages;
+    int s_pad;              // positions per sequence in the workspace, whole tiles
+    int h0, heads;          // this launch's heads h0 .. h0 + heads - 1
+    int splits, per_split;  // kernel 2: shares of the heads
+    int n_qb;               // kernel 3: query blocks of 256
+    float scale_log2;
+    __half *kr;             // [B][s_pad][64]
+    __half *k, *v;          // [B][heads][s_pad][d]
+};
+
+// A sequence's cached positions and new tokens; both 0 if the lengths were refused.
+struct Seq {
+    int prefix, n, total;
+    bool ok;
+};
+__device__ __forceinline__ Seq seq_of(const PrefillParams &p, int b) {
+    Seq s;
+    s.prefix = p.prefix_lens ? p.prefix_lens[b] : 0;
+    s.n = p.prompt_lens ? p.prompt_lens[b] : p.T;
+    s.ok = s.prefix >= 0 && s.prefix <= p.max_prefix && s.n >= 0 && s.n <= p.T;
+    if (!s.ok) s.prefix = s.n = 0;
+    s.total = s.n > 0 ? s.prefix + s.n : 0;  // nothing is attended without new tokens
+    return s;
+}
+__device__ __forceinline__ int page_of(const PrefillParams &p, int b, int pos) {
+    const int lp = pos / kPT;
+    const int pg = lp < p.max_pages ? p.page_table[(size_t)b * p.max_pages + lp] : -1;
+    return pg >= 0 && pg < p.n_pages ? pg : -1;
+}
+
+// ---- kernel 1: a warp per position ---------------------------------------------------------------
+__global__ void __launch_bounds__(256) latent_rows_kernel(const PrefillParams p, int span) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, row_w = p.dc + kDR;
+    const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int b = (int)(i / span), pos = (int)(i - (long long)b * span);
+    if (b >= p.B) return;
+    const Seq s = seq_of(p, b);
+    if (!s.ok && pos == 0 && lane == 0) atomicOr(&g_err, HMD_DEVERR_SEQLEN);
+    if (pos >= s.total) return;
+    const int pg = page_of(p, b, pos);
+    if (pg < 0 && lane == 0) atomicOr(&g_err, HMD_DEVERR_PAGE);
+    __nv_bfloat16 *cached = p.pool + ((size_t)max(pg, 0) * kPT + pos % kPT) * row_w;
+    const __nv_bfloat16 *src = cached;
+    if (pos >= s.prefix) {
+        src = p.c + ((size_t)b * p.T + pos - s.prefix) * row_w;
+        if (pg >= 0)
+            for (int c = lane * 8; c < row_w; c += 256)
+                *reinterpret_cast<uint4 *>(cached + c) = *reinterpret_cast<const uint4 *>(src + c);
+    }
+    uint32_t kr = 0;
+    if (pg >= 0 || src != cached) {
+        const uint32_t x = *reinterpret_cast<const uint32_t *>(src + p.dc + lane * 2);
+        float lo = bf16_lo(x), hi = bf16_hi(x);
+        const bool out_lo = clip_half(lo), out_hi = clip_half(hi);
+        if (out_lo || out_hi) atomicOr(&g_err, HMD_DEVWARN_RANGE);
+        kr = pack_f16x2(lo, hi);
+    }
+    *reinterpret_cast<uint32_t *>(p.kr + ((size_t)b * p.s_pad + pos) * kDR + lane * 2) = kr;
+}
+
+// ---- kernel 2 ------------------------------------------------------------------------------------
+constexpr int kExpandThreads = 192;
+template <int D>
+struct ExpandSmem {
+    static constexpr uint32_t W_STAGE = 2 * D * 128;  // [W_uk ; W_uv] rows x 64 latent dims
+    static constexpr int NW = 3;                      // stages: what is left beside 512 dims of C
+    static constexpr uint32_t OFF_A = 0, OFF_W = 8 * kBlk;
+    static constexpr uint32_t OFF_MISC = OFF_W + NW * W_STAGE;
+    static constexpr uint32_t BYTES = OFF_MISC + 256 + 1024;
+    static constexpr uint32_t ALLOC = BYTES > 118784 ? BYTES : 118784;  // one CTA per SM
+    static constexpr int B_A = 0, B_WFULL = 1, B_WFREE = B_WFULL + NW, B_ACC = B_WFREE + NW,
+                         B_READ = B_ACC + 2, B_END = B_READ + 2, N_BARS = B_END + 1;
+};
+static_assert(ExpandSmem<128>::ALLOC <= 232448, "shared memory per CTA");
+
+// 32 bytes to global memory in one store
+__device__ __forceinline__ void store_32b(void *dst, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kExpandThreads, 1)
+latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant__ CUtensorMap tmk,
+                 const __grid_constant__ CUtensorMap tmv, const PrefillParams p) {
+    using SM = ExpandSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+    const uint32_t sb = smem_u32(sm), bars = sb + SM::OFF_MISC;
+    auto bar = [&](int i) { return bars + 8 * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SM::OFF_MISC + 8 * SM::N_BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + SM::OFF_MISC + 8 * SM::N_BARS + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tiles = p.s_pad / kTile, tile = blockIdx.x / p.splits;
+    const int b = tile / tiles, pos0 = (tile - b * tiles) * kTile;
+    const int ha = (blockIdx.x % p.splits) * p.per_split, hb = min(p.heads, ha + p.per_split);
+    const int n_kc = p.dc / 64, n_steps = hb - ha;
+    griddep_launch_dependents();
+    griddep_wait();  // the appended rows are kernel 1's
+    const Seq s = seq_of(p, b);
+    if (pos0 >= s.total || n_steps <= 0) return;
+    if (tid == 0) {
+        for (int i = 0; i < SM::N_BARS; ++i)
+            mbar_init(bar(i), (i == SM::B_READ || i == SM::B_READ + 1) ? 4 : 1);
+        fence_barrier_init();
+        *abort_flag = 0;
+    }
+    if (warp == 5) {
+        __syncwarp();
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            // the tile's two pages of latent rows: blocks of 64 dims (a missing page's rows hold
+            // anything; their results are stored as zeros)
+            int pg[2];
+            uint32_t bytes = 0;
+            for (int h = 0; h < 2; ++h) {
+                pg[h] = pos0 + h * kPT < s.total ? page_of(p, b, pos0 + h * kPT) : -1;
+                if (pg[h] >= 0) bytes += n_kc * (kBlk / 2);
+            }
+            mbar_arrive_expect_tx(bar(SM::B_A), bytes);
+            for (int h = 0; h < 2; ++h)
+                if (pg[h] >= 0)
+                    for (int kc = 0; kc < n_kc; ++kc)
+                        tma_load_2d(sb + SM::OFF_A + kc * kBlk + h * (kBlk / 2), &tmc, bar(SM::B_A),
+                                    kc * 64, pg[h] * kPT);
+            bool ok = true;
+            int n = 0;
+            for (int st = 0; st < n_steps && ok; ++st) {
+                for (int kc = 0; kc < n_kc; ++kc, ++n) {
+                    const int w = n % SM::NW;
+                    if (n >= SM::NW) ok = wait_or_abort(bar(SM::B_WFREE + w), (n / SM::NW - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    const uint32_t dst = sb + SM::OFF_W + w * SM::W_STAGE;
+                    mbar_arrive_expect_tx(bar(SM::B_WFULL + w), SM::W_STAGE);
+                    tma_load_3d(dst, &tmk, bar(SM::B_WFULL + w), kc * 64, 0, p.h0 + ha + st);
+                    tma_load_3d(dst + D * 128, &tmv, bar(SM::B_WFULL + w), kc * 64, 0, p.h0 + ha + st);
+                }
+            }
+            if (!ok) {
+                // the copies in flight land (bounded) before shared memory is released
+                atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+                (void)mbar_wait_bounded(bar(SM::B_A), 0);
+                for (int i = max(0, n - SM::NW); i < n; ++i)
+                    (void)mbar_wait_bounded(bar(SM::B_WFULL + i % SM::NW), (i / SM::NW) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        if (lane == 0) {
+            const uint64_t d_a = smem_desc_sw128(sb + SM::OFF_A, 16, 1024);
+            const uint64_t d_w = smem_desc_sw128(sb + SM::OFF_W, 16, 1024);
+            constexpr uint32_t ID = idesc_bf16(128, 2 * D, 0, 0);
+            bool ok = wait_or_abort(bar(SM::B_A), 0, abort_flag);
+            int n = 0;
+            for (int st = 0; st < n_steps && ok; ++st) {
+                if (st >= 2) ok = wait_or_abort(bar(SM::B_READ + (st & 1)), ((st >> 1) - 1) & 1, abort_flag);
+                for (int kc = 0; kc < n_kc && ok; ++kc, ++n) {
+                    const int w = n % SM::NW;
+                    ok = wait_or_abort(bar(SM::B_WFULL + w), (n / SM::NW) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16(tmem + (st & 1) * 256, d_a + ((kc * kBlk + kk * 32) >> 4),
+                                  d_w + ((w * SM::W_STAGE + kk * 32) >> 4), ID, (kc > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit(bar(SM::B_WFREE + w));
+                }
+                if (ok) umma_commit(bar(SM::B_ACC + (st & 1)));
+            }
+            if (!ok) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+            umma_commit(bar(SM::B_END));  // every product is done before TMEM goes (bounded)
+            (void)mbar_wait_bounded(bar(SM::B_END), 0);
+        }
+        __syncwarp();
+    } else {
+        const int pos = pos0 + warp * 32 + lane;
+        const bool live = pos < s.total && page_of(p, b, pos) >= 0;
+        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        bool out = false;
+        for (int st = 0; st < n_steps; ++st) {
+            bool ok = wait_or_abort(bar(SM::B_ACC + (st & 1)), (st >> 1) & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                if (lane == 0) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+                break;
+            }
+            tc_fence_after();
+            const size_t row = (((size_t)b * p.heads + ha + st) * p.s_pad + pos) * D;
+#pragma unroll 1
+            for (int c = 0; c < 2 * D; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + (st & 1) * 256 + c + lanes, r);
+                tmem_wait_ld();
+                __half *dst = c < D ? p.k + row + c : p.v + row + (c - D);
+                float big = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(__uint_as_float(r[j])));
+                if (live && big > kHalfMax) {
+                    out = true;
+                    for (int j = 0; j < 32; ++j) {
+                        float x = __uint_as_float(r[j]);
+                        clip_half(x);
+                        r[j] = __float_as_uint(x);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        pk[j] = live ? pack_f16x2(__uint_as_float(r[16 * h + 2 * j]),
+                                                  __uint_as_float(r[16 * h + 2 * j + 1]))
+                                     : 0u;
+                    store_32b(dst + 16 * h, pk);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(SM::B_READ + (st & 1)));
+        }
+        if (out) atomicOr(&g_err, HMD_DEVWARN_RANGE);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---- kernel 3 ------------------------------------------------------------------------------------
+constexpr int kSoftmax = 256;                  // softmax threads: two groups of four warps
+constexpr int kAttThreads = kSoftmax + 64;     // + the MMA warp (8) and the TMA warp (9)
+template <int D>
+struct AttendSmem {
+    static constexpr int KB = D / 64 + 1, VB = D / 64, NB = KB + VB;  // blocks of a key tile
+    static constexpr int NR = 8;                                      // blocks in the ring
+    static constexpr uint32_t Q_TILE = KB * kBlk;
+    static constexpr uint32_t OFF_Q = 0, OFF_R = 2 * Q_TILE;
+    static constexpr uint32_t OFF_BAR = OFF_R + NR * kBlk;
+    static constexpr uint32_t BYTES = OFF_BAR + 256 + 1024;
+    static constexpr uint32_t ALLOC = BYTES > 118784 ? BYTES : 118784;  // one CTA per SM
+    static constexpr int B_FULL = 0, B_FREE = NR, B_S = 2 * NR, B_P = B_S + 2, B_O = B_P + 2,
+                         B_END = B_O + 2, N_BARS = B_END + 1;
+};
+static_assert(AttendSmem<128>::ALLOC <= 232448, "shared memory per CTA");
+
+template <int D>
+__global__ void __launch_bounds__(kAttThreads, 1)
+latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                            const __grid_constant__ CUtensorMap tmr, const PrefillParams p) {
+    using SM = AttendSmem<D>;
+    constexpr int KB = SM::KB, VB = SM::VB, NB = SM::NB, NR = SM::NR;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+    const uint32_t sb = smem_u32(sm), bars = sb + SM::OFF_BAR;
+    auto bar = [&](int i) { return bars + 8 * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SM::OFF_BAR + 8 * SM::N_BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + SM::OFF_BAR + 8 * SM::N_BARS + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int bh = blockIdx.x % (p.B * p.heads);
+    const int qb = p.n_qb - 1 - (int)(blockIdx.x / (p.B * p.heads));  // longest blocks first
+    const int b = bh / p.heads, hl = bh - b * p.heads, h = p.h0 + hl;
+    griddep_launch_dependents();
+    griddep_wait();
+    const Seq s = seq_of(p, b);
+    const int t_first = qb * 2 * kTile, t_last = min(s.n, t_first + 2 * kTile) - 1;
+    if (t_first >= s.n) return;
+    // key tiles of each query tile: up to its last row's position (none without rows)
+    const int nt0 = (s.prefix + min(t_last, t_first + kTile - 1)) / kTile + 1;
+    const int nt1 = t_last >= t_first + kTile ? (s.prefix + t_last) / kTile + 1 : 0;
+    const int n_tiles = max(nt0, nt1);
+    if (tid == 0) {
+        for (int i = 0; i < SM::N_BARS; ++i) mbar_init(bar(i), (i == SM::B_P || i == SM::B_P + 1) ? 4 : 1);
+        fence_barrier_init();
+        *abort_flag = 0;
+    }
+    if (warp == 8) {
+        __syncwarp();
+        tmem_alloc(smem_u32(tmem_slot), 512);  // query tile j: S_j (and P_j) at 256 j, O_j at 256 j + 128
+        tmem_relinquish();
+    }
+    // Q rows -> shared memory as fp16, one row per softmax thread
+    const int qt = (warp >> 2) & 1, row = tid & (kTile - 1);
+    const int t_row = t_first + qt * kTile + row;
+    const bool row_ok = t_row <= t_last;
+    const int pos_row = s.prefix + t_row;  // the row's position: its last key
+    if (tid < kSoftmax) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q + (((size_t)b * p.T + (row_ok ? t_row : 0)) * p.H + h) * (D + kDR));
+        bool out = false;
+#pragma unroll
+        for (int c = 0; c < (D + kDR) / 8; ++c) {
+            const uint4 x = row_ok ? src[c] : make_uint4(0, 0, 0, 0);
+            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float lo = bf16_lo(in[e]), hi = bf16_hi(in[e]);
+                out |= clip_half(lo);
+                out |= clip_half(hi);
+                y[e] = pack_f16x2(lo, hi);
+            }
+            *reinterpret_cast<uint4 *>(sm + SM::OFF_Q + qt * SM::Q_TILE + (c >> 3) * kBlk + row * 128 +
+                                       (((c & 7) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        if (out) atomicOr(&g_err, HMD_DEVWARN_RANGE);
+        fence_proxy_async_smem();  // Q is read by the tensor cores
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 9) {
+        // ================= copies: block n of the stream of tiles into slot n % NR ==============
+        if (lane == 0) {
+            bool ok = true;
+            int n = 0;
+            for (int i = 0; i < n_tiles && ok; ++i) {
+#pragma unroll 1
+                for (int u = 0; u < NB; ++u, ++n) {
+                    const int slot = n % NR;
+                    if (n >= NR) ok = wait_or_abort(bar(SM::B_FREE + slot), (n / NR - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    const uint32_t dst = sb + SM::OFF_R + slot * kBlk, fb = bar(SM::B_FULL + slot);
+                    mbar_arrive_expect_tx(fb, kBlk);
+                    if (u < KB - 1) tma_load_3d(dst, &tmk, fb, u * 64, i * kTile, bh);
+                    else if (u == KB - 1) tma_load_3d(dst, &tmr, fb, 0, i * kTile, b);
+                    else tma_load_3d(dst, &tmv, fb, (u - KB) * 64, i * kTile, bh);
+                }
+            }
+            if (!ok) {
+                // the copies in flight land (bounded) before shared memory is released
+                atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+                for (int i = max(0, n - NR); i < n; ++i)
+                    (void)mbar_wait_bounded(bar(SM::B_FULL + i % NR), (i / NR) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ================= products (one lane): O_0(i), S_0(i+1), O_1(i), S_1(i+1) =================
+        if (lane == 0) {
+            const uint64_t d_q = smem_desc_sw128(sb + SM::OFF_Q, 16, 1024);
+            const uint64_t d_k = smem_desc_sw128(sb + SM::OFF_R, 16, 1024);
+            const uint64_t d_v = smem_desc_sw128(sb + SM::OFF_R, kBlk, 1024);
+            constexpr uint32_t ID_S = idesc_f16(128, kTile, 0, 0);
+            constexpr uint32_t ID_O = idesc_f16(128, D, 0, 1), ID_O64 = idesc_f16(128, 64, 0, 1);
+            auto wait_blocks = [&](int n, int count) {
+                bool ok = true;
+                for (int u = n; u < n + count && ok; ++u)
+                    ok = wait_or_abort(bar(SM::B_FULL + u % NR), (u / NR) & 1, abort_flag);
+                return ok;
+            };
+            auto free_blocks = [&](int n, int count) {
+                for (int u = n; u < n + count; ++u) umma_commit(bar(SM::B_FREE + u % NR));
+            };
+            auto issue_s = [&](int j, int i) {  // S_j = Q_j K_i^T
+#pragma unroll
+                for (int kk = 0; kk < KB * 4; ++kk) {
+                    const uint32_t slot = (uint32_t)(i * NB + (kk >> 2)) % NR;
+                    umma_bf16(tmem + 256 * j, d_q + ((j * SM::Q_TILE + (kk >> 2) * kBlk + (kk & 3) * 32) >> 4),
+                              d_k + ((slot * kBlk + (kk & 3) * 32) >> 4), ID_S, kk > 0);
+                }
+                umma_commit(bar(SM::B_S + j));
+            };
+            auto issue_o = [&](int j, int i) {  // O_j (+)= P_j V_i, P_j from TMEM
+                const uint32_t slot = (uint32_t)(i * NB + KB) % NR;
+                const uint32_t o = tmem + 256 * j + 128, pj = tmem + 256 * j;
+                if (VB == 1 || slot + 1 < NR) {
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        umma_bf16_ts(o, pj + 8 * kk, d_v + ((slot * kBlk + kk * 2048) >> 4), ID_O,
+                                     (i > 0 || kk > 0) ? 1u : 0u);
+                } else {  // the tile's second block is at the ring's start: 64 dims at a time
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            umma_bf16_ts(o + 64 * v, pj + 8 * kk,
+                                         d_v + (((v ? 0 : slot) * kBlk + kk * 2048) >> 4), ID_O64,
+                                         (i > 0 || kk > 0) ? 1u : 0u);
+                }
+            };
+            bool ok = wait_blocks(0, KB);
+            if (ok) {
+                tc_fence_after();
+                issue_s(0, 0);
+                if (nt1 > 0) issue_s(1, 0);
+                free_blocks(0, KB);
+            }
+            for (int i = 0; i < n_tiles && ok; ++i) {
+#pragma unroll 1
+                for (int j = 0; j < 2 && ok; ++j) {
+                    const int nt = j ? nt1 : nt0;
+                    if (j == 0) ok = wait_blocks(i * NB + KB, VB);
+                    if (ok && i < nt) {
+                        ok = wait_or_abort(bar(SM::B_P + j), i & 1, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_o(j, i);
+                        if (i == nt - 1) umma_commit(bar(SM::B_O + j));
+                    }
+                    if (!ok) break;
+                    if (j == 1) free_blocks(i * NB + KB, VB);
+                    if (i + 1 < n_tiles) {
+                        if (j == 0) ok = wait_blocks((i + 1) * NB, KB);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (i + 1 < nt) issue_s(j, i + 1);
+                        if (j == 1) free_blocks((i + 1) * NB, KB);
+                    }
+                }
+            }
+            if (!ok) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+            umma_commit(bar(SM::B_END));  // every product is done before TMEM goes (bounded)
+            (void)mbar_wait_bounded(bar(SM::B_END), 0);
+        }
+        __syncwarp();
+    } else if ((qt ? nt1 : nt0) > 0) {
+        // ================= softmax: query tile qt, one thread per row ==========================
+        const int nt = qt ? nt1 : nt0;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t s_col = lane_base + 256 * qt, o_col = s_col + 128;
+        float m_base = -INFINITY, l_run = 0.f;
+        bool ok = true;
+        for (int i = 0; i < nt && ok; ++i) {
+            ok = wait_or_abort(bar(SM::B_S + qt), i & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);  // the TMEM accesses below run converged
+            if (!ok) break;
+            tc_fence_after();
+            float x[kTile];
+            {
+                uint32_t r[64];
+                tmem_ld64(s_col, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(r[j]);
+                tmem_ld64(s_col + 64, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 64; ++j) x[64 + j] = __uint_as_float(r[j]);
+            }
+            const int j0 = i * kTile;
+            if (!(row_ok && j0 + kTile - 1 <= pos_row)) {
+#pragma unroll
+                for (int j = 0; j < kTile; ++j) x[j] = (row_ok && j0 + j <= pos_row) ? x[j] : -INFINITY;
+            }
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // short chains
+#pragma unroll
+            for (int j = 0; j < kTile; j += 8) {
+                mx4[0] = max3(mx4[0], x[j], x[j + 1]);
+                mx4[1] = max3(mx4[1], x[j + 2], x[j + 3]);
+                mx4[2] = max3(mx4[2], x[j + 4], x[j + 5]);
+                mx4[3] = max3(mx4[3], x[j + 6], x[j + 7]);
+            }
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+            const bool move = mx > m_base + kLazy;
+            float f = 1.f;  // factor of the row's earlier output and sum
+            if (move) {
+                f = exp2f(m_base - mx);  // 0 while the row had no key (m_base = -inf)
+                m_base = mx;
+                l_run *= f;
+            }
+            const float mu = (m_base == -INFINITY) ? 0.f : m_base;
+            __syncwarp();  // the row-dependent branches above rejoin before the TMEM stores
+            {
+                const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nmu2 = f2(-mu, -mu);
+                uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < kTile / 32; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) {
+                        const uint64_t y = f2_fma(f2(x[c * 32 + 2 * u], x[c * 32 + 2 * u + 1]), sc2, nmu2);
+                        uint64_t e;
+                        if ((u & 3) == 3) {
+                            e = exp2_fma_x2(y);
+                        } else {
+                            float a0, a1;
+                            f2_split(y, a0, a1);
+                            e = f2(ex2_approx(a0), ex2_approx(a1));
+                        }
+                        acc[u & 1] = f2_add(acc[u & 1], e);
+                        float e0, e1;
+                        f2_split(e, e0, e1);
+                        pk[u] = pack_f16x2(e0, e1);
+                    }
+                    tmem_st16(s_col + 16 * c, pk);
+                }
+                float a0, a1, b0, b1;
+                f2_split(acc[0], a0, a1);
+                f2_split(acc[1], b0, b1);
+                l_run += (a0 + a1) + (b0 + b1);
+            }
+            // the row's earlier output to the new base (the product into it is done: S_j(i) was
+            // issued after O_j(i-1))
+            if (__any_sync(0xffffffffu, move) && i > 0) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32(o_col + 32 * c, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+                    tmem_st32(o_col + 32 * c, r);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(SM::B_P + qt));
+        }
+        if (ok) ok = wait_or_abort(bar(SM::B_O + qt), 0, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            tc_fence_after();
+            const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+            uint4 *dst = reinterpret_cast<uint4 *>(p.o + (((size_t)b * p.T + t_row) * p.H + h) * D);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                __syncwarp();  // converged for the TMEM load after the row-dependent stores
+                uint32_t r[32];
+                tmem_ld32(o_col + 32 * c, r);
+                tmem_wait_ld();
+                if (row_ok) {
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const float *v = reinterpret_cast<const float *>(r + 8 * q4);
+                        dst[c * 4 + q4] = make_uint4(pack_bf16x2(v[0] * inv, v[1] * inv),
+                                                     pack_bf16x2(v[2] * inv, v[3] * inv),
+                                                     pack_bf16x2(v[4] * inv, v[5] * inv),
+                                                     pack_bf16x2(v[6] * inv, v[7] * inv));
+                    }
+                }
+            }
+        } else if (lane == 0) {
+            atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+int device_sms() {
+    return once_per_device([] {
+        int dev = 0, v = 0;
+        if (cudaGetDevice(&dev) == cudaSuccess &&
+            cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
+            return v;
+        cudaGetLastError();
+        return 148;
+    });
+}
+
+size_t padded(int T, int max_prefix) {
+    return ((size_t)T + max_prefix + kTile - 1) / kTile * kTile;
+}
+
+template <int D>
+cudaError_t launch_d(const LatentPrefillArgs &a, cudaStream_t s) {
+    const cudaError_t attr_err = once_per_device([] {
+        cudaError_t e = cudaFuncSetAttribute(latent_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)ExpandSmem<D>::ALLOC);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(latent_attend_prompt_kernel<D>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AttendSmem<D>::ALLOC);
+        return e;
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    PrefillParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(a.q);
+    p.c = static_cast<const __nv_bfloat16 *>(a.c);
+    p.pool = static_cast<__nv_bfloat16 *>(a.pool);
+    p.o = static_cast<__nv_bfloat16 *>(a.o);
+    p.prefix_lens = a.prefix_lens; p.prompt_lens = a.prompt_lens; p.page_table = a.page_table;
+    p.B = a.B; p.T = a.T; p.H = a.H; p.dc = a.d_c;
+    p.max_prefix = a.prefix_lens ? a.max_prefix : 0;
+    p.n_pages = a.n_pages; p.max_pages = a.max_pages;
+    const size_t s_pad = padded(a.T, p.max_prefix);
+    p.s_pad = (int)s_pad;
+    p.n_qb = (a.T + 2 * kTile - 1) / (2 * kTile);
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    // the workspace: k_r of every position, then K and V of as many heads as fit
+    const size_t kr_bytes = (size_t)a.B * s_pad * kDR * 2, head_bytes = (size_t)a.B * s_pad * D * 2 * 2;
+    const int fit = (int)std::min<size_t>((size_t)a.H, (a.ws_bytes - kr_bytes) / head_bytes);
+    const int n_groups = (a.H + fit - 1) / fit, group = (a.H + n_groups - 1) / n_groups;
+    p.kr = static_cast<__half *>(a.workspace);
+    p.k = p.kr + kr_bytes / 2;
+    CUtensorMap tmc, tmuk, tmuv, tmr;
+    if (!make_tmap_pool_sw128(&tmc, a.pool, a.n_pages, 1, a.d_c + kDR) ||
+        !make_tmap_blocks_sw128(&tmuk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w_uk, a.H, a.w_uk_head, D, a.d_c, D) ||
+        !make_tmap_blocks_sw128(&tmuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w_uv, a.H, a.w_uv_head, D, a.d_c, D) ||
+        !make_tmap_blocks_sw128(&tmr, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.kr, a.B, (long long)s_pad * kDR,
+                                (long long)s_pad, kDR, kTile))
+        return cudaErrorInvalidValue;
+    const int span = a.T + p.max_prefix;
+    cudaError_t e = launch_pdl(latent_rows_kernel, dim3((unsigned)(((long long)a.B * span + 7) / 8)), dim3(256),
+                               0, s, p, span);
+    for (int h0 = 0; h0 < a.H && e == cudaSuccess; h0 += group) {
+        p.h0 = h0;
+        p.heads = std::min(group, a.H - h0);
+        p.v = p.k + (size_t)a.B * p.heads * s_pad * D;
+        // shares of the heads per position tile: the fewest rounds of CTAs, each costing its heads
+        // and about one more for loading the tile's latent rows
+        const long long tiles = (long long)a.B * (s_pad / kTile), sms = device_sms();
+        long long best = -1;
+        for (int n = 1; n <= p.heads; ++n) {
+            const int per = (p.heads + n - 1) / n;
+            const long long cost = (tiles * n + sms - 1) / sms * (per + 1);
+            if (best < 0 || cost < best) {
+                best = cost;
+                p.splits = n;
+                p.per_split = per;
+            }
+        }
+        CUtensorMap tmk, tmv;
+        const long long bh = (long long)a.B * p.heads;
+        if (!make_tmap_blocks_sw128(&tmk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.k, bh, (long long)s_pad * D,
+                                    (long long)s_pad, D, kTile) ||
+            !make_tmap_blocks_sw128(&tmv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.v, bh, (long long)s_pad * D,
+                                    (long long)s_pad, D, kTile))
+            return cudaErrorInvalidValue;
+        e = launch_pdl(latent_kv_kernel<D>, dim3((unsigned)(tiles * p.splits)), dim3(kExpandThreads),
+                       ExpandSmem<D>::ALLOC, s, tmc, tmuk, tmuv, p);
+        if (e != cudaSuccess) break;
+        e = launch_pdl(latent_attend_prompt_kernel<D>, dim3((unsigned)(p.n_qb * bh)), dim3(kAttThreads),
+                       AttendSmem<D>::ALLOC, s, tmk, tmv, tmr, p);
+    }
+    return e;
+}
+
+}  // namespace
+
+size_t latent_prefill_ws_bytes(int B, int T, int heads, int d, int max_prefix) {
+    return (size_t)B * padded(T, max_prefix) * (kDR + 2 * (size_t)d * heads) * 2;
+}
+
+cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t s) {
+    return a.d == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s);
+}
+
+uint32_t latent_prefill_read_errors(bool clear) {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_err, sizeof v) != cudaSuccess) return 0;
+    if (clear && v) {
+        const unsigned int z = 0;
+        cudaMemcpyToSymbol(g_err, &z, sizeof z);
+    }
+    return v;
+}
+
+}  // namespace hmd

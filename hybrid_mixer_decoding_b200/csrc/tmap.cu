@@ -80,6 +80,24 @@ bool make_tmap_bthd(CUtensorMap *m, CUtensorMapDataType dt, int esize, const voi
            CUDA_SUCCESS;
 }
 
+// Blocks [heads][rows][cols] of 16-bit values, `head_stride` elements from one to the next, as a
+// 3-D tensor (cols, rows, heads) read in boxes of 64 columns x box_rows rows of one block with the
+// 128-byte swizzle: one box is a [box_rows][128 B] tile. Rows past `rows` read as zero.
+bool make_tmap_blocks_sw128(CUtensorMap *m, CUtensorMapDataType dt, const void *base,
+                            long long heads, long long head_stride, long long rows, int cols,
+                            int box_rows) {
+    EncodeTiledFn enc = encode();
+    if (!enc) return false;
+    const cuuint64_t gdim[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)heads};
+    const cuuint64_t gstride[2] = {(cuuint64_t)cols * 2, (cuuint64_t)head_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, dt, 3, const_cast<void *>(base), gdim, gstride, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 // A paged pool [n_pages][heads][64][d] bf16 viewed as [n_pages*heads*64 rows][d], read in boxes
 // of 64 rows x 64 dims with the 128-byte swizzle: one box is half of one page of one head.
 bool make_tmap_pool_sw128(CUtensorMap *m, void *pool, int n_pages, int heads, int d) {

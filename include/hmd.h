@@ -57,6 +57,8 @@ typedef enum {
 #define HMD_DEVERR_PAGE      0x2u  /* a page-table entry was outside [0, n_pages) */
 #define HMD_DEVERR_SLOT      0x4u  /* a state-slot index was outside [0, n_slots) */
 #define HMD_DEVERR_SEQLEN    0x8u  /* a sequence length was < 1 or above the stated maximum */
+#define HMD_DEVWARN_RANGE    0x20u /* a value outside fp16's range was clipped to it
+                                      (attn_latent_prefill) */
 #define HMD_DEVERR_GATE      0x10u /* reserved: no longer raised (the chunked prefill accepts
                                       every gate range) */
 
@@ -411,6 +413,33 @@ HMD_API hmd_status_t attn_latent_decode(int n_q, int B, int H, int d, int d_c, i
                                         int n_pages, const int32_t *page_table, int max_pages,
                                         const int32_t *seq_lens, int max_seq_len, void *o,
                                         void *workspace, size_t ws_bytes, hmd_stream_t stream);
+
+/* Expanded form, for prompts: T new tokens per sequence after prefix_lens[b] cached positions.
+ * Appends their rows and attends causally: token t sits at position prefix_lens[b] + t.
+ *   q [B][T][H][d + d_r]; c [B][T][d_c + d_r]; o [B][T][H][d], all bf16.
+ *   prefix_lens: device int32 [B], any values in [0, max_prefix]; NULL: no prefix.
+ *   prompt_lens: device int32 [B] in [0, T], the sequence's new tokens; the rows of q, c and o
+ *   behind them are neither read nor written. NULL: T everywhere. Other lengths set
+ *   HMD_DEVERR_SEQLEN and skip the sequence.
+ *   Needs max_pages >= ceil((max_prefix + T) / page_tokens). A page outside the pool sets
+ *   HMD_DEVERR_PAGE; that sequence's outputs are then not meaningful.
+ *   workspace: the expanded keys and values, fp16. Any size works from the
+ *   attn_latent_prefill_workspace_size(...) of H = 1 up; with less than that of all H heads the
+ *   heads run in groups (same results, bit for bit). Not in use by another call while this one
+ *   runs. Allocates nothing.
+ * Keys, values, queries and softmax weights are rounded to fp16 (2^-11, less than the bf16
+ * output's rounding); a key, value or query beyond 65504 is clipped and sets HMD_DEVWARN_RANGE.
+ * q, c, the weights, pool, o and workspace 16-byte aligned.                                     */
+HMD_API size_t attn_latent_prefill_workspace_size(int B, int T, int H, int d, int d_c, int d_r,
+                                                  int page_tokens, int max_prefix);
+HMD_API hmd_status_t attn_latent_prefill(int B, int T, int H, int d, int d_c, int d_r,
+                                         int page_tokens, float scale, const void *q,
+                                         const void *c, const void *w_uk, int64_t w_uk_head,
+                                         const void *w_uv, int64_t w_uv_head,
+                                         const int32_t *prefix_lens, int max_prefix,
+                                         const int32_t *prompt_lens, void *pool, int n_pages,
+                                         const int32_t *page_table, int max_pages, void *o,
+                                         void *workspace, size_t ws_bytes, hmd_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
 /* Caches and the placement dispatcher.                                                       */

@@ -208,3 +208,147 @@ def test_verify_equals_successive_decode_steps():
         c.lens.copy_(i32([L - nq + 1 + i for L in c.lens_list]))
         oi = c.decode(q[:, i:i + 1].contiguous(), new_c[:, i:i + 1].contiguous())
         assert (oi[:, 0].double() - o[:, i].double()).abs().max() <= 2.0 ** -6 * o.double().abs().max()
+
+
+# ---- expanded form -------------------------------------------------------------------------------
+# o is rounded once to bf16 (2^-8 of the value). Keys, values, queries and weights are fp16 (half a
+# step, 2^-11 of each; absolute 2^-25 below 2^-14): a score moves by at most 3 * 2^-11 of its terms,
+# the weights by as much and by 2^-11 themselves and the exponential's 2^-13, the values by 2^-11.
+def prefill(c, q, new_c, prefix=None, prompt=None, heads_in_ws=None, scale=None, o=None, ws=None):
+    B, T = q.shape[:2]
+    mp = int(max(prefix)) if prefix is not None else 0
+    if ws is None:
+        ws = torch.empty(hmd.attn_latent_prefill_workspace_size(B, T, heads_in_ws or c.H, c.d, c.d_c, DR,
+                                                                PT, mp), dtype=torch.uint8, device="cuda")
+        ws.fill_(0xff)  # NaN everywhere
+    o = torch.full((B, T, c.H, c.d), 9.0, device="cuda", dtype=BF) if o is None else o
+    hmd.attn_latent_prefill(q, new_c, c.w_uk, c.w_uv, c.pool, c.table, o, ws,
+                            prefix_lens=None if prefix is None else i32(prefix), max_prefix=mp,
+                            prompt_lens=None if prompt is None else i32(prompt), scale=scale)
+    return o
+
+
+def check_prefill(c, q, new_c, o, prefix, prompt, scale=None):
+    scale = (c.d + DR) ** -0.5 if scale is None else scale
+    for b, (pre, n) in enumerate(zip(prefix, prompt)):
+        assert (o[b, n:] == 9.0).all()  # behind the prompt: as it was
+        if n == 0:
+            continue
+        C = c.rows(b, pre + n)
+        assert torch.equal(C[pre:], new_c[b, :n])  # the append
+        ref, _, rms = reference(c, b, C, q[b, :n], pre, scale)
+        qn, qr = q[b, :n].double().transpose(0, 1).split([c.d, DR], -1)
+        K = torch.einsum("jc,hnc->hjn", C.double()[:, :c.d_c], c.w_uk.double())
+        V = torch.einsum("jc,hvc->hjv", C.double()[:, :c.d_c], c.w_uv.double())
+        hidden = torch.arange(pre + n, device="cuda")[None] > pre + torch.arange(n, device="cuda")[:, None]
+        x = (qn @ K.transpose(1, 2) + qr @ C.double()[:, c.d_c:].T) * scale
+        p = torch.softmax(x.masked_fill(hidden, -torch.inf), -1)
+        terms = (qn.abs() @ K.abs().transpose(1, 2) + qr.abs() @ C.double()[:, c.d_c:].abs().T).amax() * scale
+        pv = (p @ V.abs()).transpose(0, 1)
+        err = (o[b, :n].double() - ref).abs()
+        tol = 2.0 ** -8 * ref.abs() + (2 * 3 * 2.0 ** -11 * terms + 2 * 2.0 ** -11 + 2.0 ** -13) * pv
+        assert (err <= tol).all(), (b, (err / tol).max().item())
+        typical = (2.0 ** -8 * ref.abs() + 2.0 ** -10 * rms).square().mean().sqrt()
+        assert err.square().mean().sqrt() <= typical
+
+
+@pytest.mark.parametrize("H,d,d_c,T", [(4, 128, 512, 1), (3, 128, 512, 127), (2, 64, 256, 128),
+                                       (5, 64, 128, 129), (2, 128, 384, 257), (7, 64, 512, 600),
+                                       (3, 128, 512, 1300)])
+def test_prefill_whole_prompts(H, d, d_c, T):
+    c = Latent([T, T], H, d, d_c, seed=T)
+    q, new_c = c.randn(2, T, H, d + DR), c.randn(2, T, d_c + DR)
+    o = prefill(c, q, new_c)
+    check_prefill(c, q, new_c, o, [0, 0], [T, T])
+    assert hmd.hmd_device_errors(clear=True) == 0
+    # fewer heads at a time: the same bits
+    for heads in {1, 2, H - 1} - {0, H}:
+        assert torch.equal(prefill(c, q, new_c, heads_in_ws=heads), o)
+
+
+@pytest.mark.parametrize("d,d_c", [(128, 512), (64, 256)])
+def test_prefill_after_ragged_prefixes(d, d_c):
+    prefix, prompt, T = [0, 1, 63, 64, 100, 700, 512, 5], [300, 1, 65, 128, 0, 299, 256, 7], 300
+    c = Latent([max(1, a) for a in prefix], 4, d, d_c, seed=21, max_len=1000)
+    q, new_c = c.randn(8, T, 4, d + DR), c.randn(8, T, d_c + DR)
+    for b, n in enumerate(prompt):  # padding: never read
+        q[b, n:], new_c[b, n:] = float("nan"), float("nan")
+    before = c.pool.clone()
+    o = prefill(c, q, new_c, prefix, prompt)
+    check_prefill(c, q, new_c, o, prefix, prompt)
+    assert hmd.hmd_device_errors(clear=True) == 0
+    for b, (pre, n) in enumerate(zip(prefix, prompt)):
+        pos = torch.arange(pre, pre + n, device="cuda")
+        before[c.table[b].long()[pos // PT], pos % PT] = new_c[b, :n]
+    assert torch.equal(before.view(torch.int16), c.pool.view(torch.int16))
+
+
+def test_prefill_reports_bad_lengths_pages_and_range():
+    c = Latent([100, 100], 2, 64, 128, seed=22, max_len=300)
+    q, new_c = c.randn(2, 50, 2, 128), c.randn(2, 50, 192)
+    o = prefill(c, q, new_c, [100, 64], [51, 50])
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVERR_SEQLEN
+    check_prefill(c, q, new_c, o, [0, 64], [0, 50])
+    q[1, 3, 0, 5] = 1e6
+    prefill(c, q, new_c)
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVWARN_RANGE
+    c.table[0, 0] = c.pool.shape[0]
+    q[1, 3, 0, 5] = 1.0
+    o = prefill(c, q, new_c)
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVERR_PAGE
+    check_prefill(c, q[1:], new_c[1:], o[1:], [], [])
+
+
+def test_prefill_steep_softmax_and_large_values():
+    """Scores that grow along the sequence, values of several thousand (fp16's range is 65504)."""
+    c = Latent([400], 4, 128, 512, seed=23, w_scale=3.0)
+    c.w_uv *= 512
+    q, new_c = c.randn(1, 400, 4, 192), c.randn(1, 400, 576)
+    new_c *= torch.linspace(0.05, 2.0, 400, device="cuda")[None, :, None].to(BF)
+    o = prefill(c, q, new_c, scale=0.1)
+    assert hmd.hmd_device_errors(clear=True) == 0
+    check_prefill(c, q, new_c, o, [0], [400], scale=0.1)
+
+
+def test_prefill_in_parts_then_decode():
+    """As they are used: two parts of a prompt, then decode steps and a verification pass, against
+    the definition over the whole sequence."""
+    H, d, d_c, lens = 16, 128, 512, [300, 171]
+    c = Latent([1, 1], H, d, d_c, seed=24, max_len=400)
+    C, Q = c.randn(2, 320, d_c + DR), c.randn(2, 320, H, d + DR)
+    done = [0, 0]
+    for part in ([200, 100], [100, 71]):
+        T = max(part)
+        q, new_c = torch.zeros(2, T, H, d + DR, device="cuda", dtype=BF), torch.zeros(2, T, d_c + DR, device="cuda", dtype=BF)
+        for b, n in enumerate(part):
+            q[b, :n], new_c[b, :n] = Q[b, done[b]:done[b] + n], C[b, done[b]:done[b] + n]
+        o = prefill(c, q, new_c, done, part)
+        check_prefill(c, q, new_c, o, done, part)
+        done = [a + n for a, n in zip(done, part)]
+    assert done == lens
+    for nq in (1, 1, 3):
+        done = [n + nq for n in done]
+        c.lens_list = done
+        c.lens.copy_(i32(done))
+        q = torch.stack([Q[b, L - nq:L] for b, L in enumerate(done)])
+        new_c = torch.stack([C[b, L - nq:L] for b, L in enumerate(done)])
+        check_decode(c, q, new_c, c.decode(q, new_c))
+    assert hmd.hmd_device_errors(clear=True) == 0
+
+
+def test_prefill_captured_on_another_stream():
+    c = Latent([1], 4, 64, 256, seed=25, max_len=400)
+    q, new_c = c.randn(1, 333, 4, 128), c.randn(1, 333, 320)
+    ref = prefill(c, q, new_c)
+    ws = torch.empty(hmd.attn_latent_prefill_workspace_size(1, 333, 4, 64, 256, DR, PT),
+                     dtype=torch.uint8, device="cuda")
+    o = torch.zeros_like(ref)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            prefill(c, q, new_c, o=o, ws=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, ref)
