@@ -451,26 +451,27 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
             if (q_issued > 0) (void)mbar_wait_bounded(bar(SM::B_QFULL), (q_issued - 1) & 1);
         }
     } else if (warp == 5) {
-        // ================= products (one lane), whichever is ready first =====================
-        if (lane == 0) {
-            const uint64_t d_q = smem_desc_sw128(sb + SM::OFF_Q, 16, 1024);
-            const uint64_t d_k = smem_desc_sw128(sb + SM::OFF_C, 16, 1024);    // keys x dims
-            const uint64_t d_v = smem_desc_sw128(sb + SM::OFF_C, kBlk, 1024);  // dims x keys
-            const uint64_t d_p = smem_desc_sw128(sb + SM::OFF_P, 16, 1024);
-            constexpr uint32_t ID_S = idesc_bf16(64, 2 * kRows, 0, 0);
-            constexpr uint32_t ID_O = idesc_bf16(128, kRows, 1, 0);
-            int s = 0, su = 0, pv = 0, seg = 0;
-            Walk ws = w, wp = w;  // the sequences of the next scores and of the next output product
-            bool ok = true;
-            unsigned long long t0 = 0;
-            while (pv < n_pages) {
-                bool moved = false;
-                if (pv < s && mbar_test(bar(SM::B_P + (pv & 1)), (pv >> 1) & 1)) {
-                    // O^T += C^T P^T, unit by unit; each unit's page slot is free after it
-                    tc_fence_after();
-                    if (wp.at == wp.seg_end) wp.seek(p, end);
-                    const int st = pv % NS;
-                    const bool fresh = wp.at == wp.seg_begin;
+        // ================= products, whichever is ready first (the warp converged) ===========
+        const bool lead = elect_one();
+        const uint64_t d_q = smem_desc_sw128(sb + SM::OFF_Q, 16, 1024);
+        const uint64_t d_k = smem_desc_sw128(sb + SM::OFF_C, 16, 1024);    // keys x dims
+        const uint64_t d_v = smem_desc_sw128(sb + SM::OFF_C, kBlk, 1024);  // dims x keys
+        const uint64_t d_p = smem_desc_sw128(sb + SM::OFF_P, 16, 1024);
+        constexpr uint32_t ID_S = idesc_bf16(64, 2 * kRows, 0, 0);
+        constexpr uint32_t ID_O = idesc_bf16(128, kRows, 1, 0);
+        int s = 0, su = 0, pv = 0, seg = 0;
+        Walk ws = w, wp = w;  // the sequences of the next scores and of the next output product
+        bool ok = true;
+        unsigned long long t0 = 0;
+        while (pv < n_pages) {
+            bool moved = false;
+            if (pv < s && __all_sync(0xffffffffu, mbar_test(bar(SM::B_P + (pv & 1)), (pv >> 1) & 1))) {
+                // O^T += C^T P^T, unit by unit; each unit's page slot is free after it
+                tc_fence_after();
+                if (wp.at == wp.seg_end) wp.seek(p, end);
+                const int st = pv % NS;
+                const bool fresh = __all_sync(0xffffffffu, wp.at == wp.seg_begin);
+                if (lead) {
 #pragma unroll
                     for (int u = 0; u < NP; ++u) {
 #pragma unroll
@@ -482,53 +483,65 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
                         umma_commit(free_(st, u));
                     }
                     umma_commit(bar(SM::B_O + (pv & 1)));
-                    ++wp.at;
-                    ++pv;
-                    moved = true;
-                } else if (s < n_pages && s <= pv + 1) {
-                    // S^T = C [q~hi ; q~lo]^T, unit by unit as they land (the scores before last
-                    // have been read: their output product is issued)
-                    if (ws.at == ws.seg_end) ws.seek(p, end);
-                    const int st = s % NS, u = su == 0 ? NP : su - 1;
-                    const bool q_ready = su > 0 || ws.at > ws.seg_begin ||
-                                         mbar_test(bar(SM::B_QFULL), seg & 1);
-                    if (q_ready && mbar_test(full(st, u), (s / NS) & 1)) {
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            if (u == NP && kk >= 4) break;
-                            const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
-                            umma_bf16(tmem + kTmemS + (s & 1) * 64,
-                                      d_k + ((st * PAGE + u * 2 * kBlk + off) >> 4),
-                                      d_q + ((u * 2 * kBlk + off) >> 4), ID_S,
-                                      (su == 0 && kk == 0) ? 0u : 1u);
-                        }
-                        if (u == NP) umma_commit(free_(st, NP));
-                        if (++su == NU) {
-                            umma_commit(bar(SM::B_S + (s & 1)));
-                            su = 0;
-                            ++s;
-                            if (++ws.at == ws.seg_end) {
-                                umma_commit(bar(SM::B_QFREE));
-                                ++seg;
-                            }
-                        }
-                        moved = true;
-                    }
                 }
-                if (moved) {
-                    t0 = 0;
-                } else {
-                    if (*abort_flag) ok = false;
-                    const unsigned long long now = globaltimer_ns();
-                    if (t0 == 0) t0 = now;
-                    else if (now - t0 > kWaitLimitNs) {
-                        *abort_flag = 1;
-                        ok = false;
+                __syncwarp();
+                ++wp.at;
+                ++pv;
+                moved = true;
+            } else if (s < n_pages && s <= pv + 1) {
+                // S^T = C [q~hi ; q~lo]^T, unit by unit as they land (the scores before last
+                // have been read: their output product is issued)
+                if (ws.at == ws.seg_end) ws.seek(p, end);
+                const int st = s % NS, u = su == 0 ? NP : su - 1;
+                const bool ready = (su > 0 || ws.at > ws.seg_begin || mbar_test(bar(SM::B_QFULL), seg & 1)) &&
+                                   mbar_test(full(st, u), (s / NS) & 1);
+                if (__all_sync(0xffffffffu, ready)) {
+                    tc_fence_after();
+                    const uint32_t d = tmem + kTmemS + (s & 1) * 64;
+                    const uint64_t ku = d_k + ((st * PAGE + u * 2 * kBlk) >> 4);
+                    const uint64_t qu = d_q + ((u * 2 * kBlk) >> 4);
+                    if (lead) {
+                        // the shared part comes first and starts the sums
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_bf16(d, ku + ((kk * 32) >> 4), qu + ((kk * 32) >> 4), ID_S,
+                                      (su == 0 && kk == 0) ? 0u : 1u);
+                        if (su > 0) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_bf16(d, ku + ((kBlk + kk * 32) >> 4), qu + ((kBlk + kk * 32) >> 4),
+                                          ID_S, 1u);
+                        } else {
+                            umma_commit(free_(st, NP));
+                        }
+                        if (su == NP) umma_commit(bar(SM::B_S + (s & 1)));
                     }
-                    if (!ok) break;
+                    __syncwarp();
+                    if (++su == NU) {
+                        su = 0;
+                        ++s;
+                        if (__all_sync(0xffffffffu, ++ws.at == ws.seg_end)) {
+                            if (lead) umma_commit(bar(SM::B_QFREE));
+                            ++seg;
+                        }
+                    }
+                    moved = true;
                 }
             }
+            if (moved) {
+                t0 = 0;
+            } else {
+                const unsigned long long now = globaltimer_ns();
+                if (t0 == 0) t0 = now;
+                const bool late = now - t0 > kWaitLimitNs;
+                if (late) *abort_flag = 1;
+                if (__any_sync(0xffffffffu, late || *abort_flag)) {
+                    ok = false;
+                    break;
+                }
+            }
+        }
+        if (lead) {
             if (!ok) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
             // every product is done before TMEM and shared memory go (bounded)
             umma_commit(bar(SM::B_END));

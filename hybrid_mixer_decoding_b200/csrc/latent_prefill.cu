@@ -221,27 +221,34 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         }
         __syncwarp();
     } else if (warp == 5) {
-        if (lane == 0) {
-            const uint64_t d_a = smem_desc_sw128(sb + SM::OFF_A, 16, 1024);
-            const uint64_t d_w = smem_desc_sw128(sb + SM::OFF_W, 16, 1024);
-            constexpr uint32_t ID = idesc_bf16(128, 2 * D, 0, 0);
-            bool ok = wait_or_abort(bar(SM::B_A), 0, abort_flag);
-            int n = 0;
-            for (int st = 0; st < n_steps && ok; ++st) {
-                if (st >= 2) ok = wait_or_abort(bar(SM::B_READ + (st & 1)), ((st >> 1) - 1) & 1, abort_flag);
-                for (int kc = 0; kc < n_kc && ok; ++kc, ++n) {
-                    const int w = n % SM::NW;
-                    ok = wait_or_abort(bar(SM::B_WFULL + w), (n / SM::NW) & 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
+        const bool lead = elect_one();
+        const uint64_t d_a = smem_desc_sw128(sb + SM::OFF_A, 16, 1024);
+        const uint64_t d_w = smem_desc_sw128(sb + SM::OFF_W, 16, 1024);
+        constexpr uint32_t ID = idesc_bf16(128, 2 * D, 0, 0);
+        auto wait = [&](int i, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_abort(bar(i), parity, abort_flag)) != 0;
+        };
+        bool ok = wait(SM::B_A, 0);
+        int n = 0;
+        for (int st = 0; st < n_steps && ok; ++st) {
+            if (st >= 2) ok = wait(SM::B_READ + (st & 1), ((st >> 1) - 1) & 1);
+            for (int kc = 0; kc < n_kc && ok; ++kc, ++n) {
+                const int w = n % SM::NW;
+                ok = wait(SM::B_WFULL + w, (n / SM::NW) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lead) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         umma_bf16(tmem + (st & 1) * 256, d_a + ((kc * kBlk + kk * 32) >> 4),
                                   d_w + ((w * SM::W_STAGE + kk * 32) >> 4), ID, (kc > 0 || kk > 0) ? 1u : 0u);
                     umma_commit(bar(SM::B_WFREE + w));
+                    if (kc == n_kc - 1) umma_commit(bar(SM::B_ACC + (st & 1)));
                 }
-                if (ok) umma_commit(bar(SM::B_ACC + (st & 1)));
+                __syncwarp();
             }
+        }
+        if (lead) {
             if (!ok) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
             umma_commit(bar(SM::B_END));  // every product is done before TMEM goes (bounded)
             (void)mbar_wait_bounded(bar(SM::B_END), 0);
@@ -417,79 +424,91 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         }
         __syncwarp();
     } else if (warp == 8) {
-        // ================= products (one lane): O_0(i), S_0(i+1), O_1(i), S_1(i+1) =================
-        if (lane == 0) {
-            const uint64_t d_q = smem_desc_sw128(sb + SM::OFF_Q, 16, 1024);
-            const uint64_t d_k = smem_desc_sw128(sb + SM::OFF_R, 16, 1024);
-            const uint64_t d_v = smem_desc_sw128(sb + SM::OFF_R, kBlk, 1024);
-            constexpr uint32_t ID_S = idesc_f16(128, kTile, 0, 0);
-            constexpr uint32_t ID_O = idesc_f16(128, D, 0, 1), ID_O64 = idesc_f16(128, 64, 0, 1);
-            auto wait_blocks = [&](int n, int count) {
-                bool ok = true;
-                for (int u = n; u < n + count && ok; ++u)
-                    ok = wait_or_abort(bar(SM::B_FULL + u % NR), (u / NR) & 1, abort_flag);
-                return ok;
-            };
-            auto free_blocks = [&](int n, int count) {
-                for (int u = n; u < n + count; ++u) umma_commit(bar(SM::B_FREE + u % NR));
-            };
-            auto issue_s = [&](int j, int i) {  // S_j = Q_j K_i^T
+        // ================= products: O_0(i), S_0(i+1), O_1(i), S_1(i+1) (the warp converged) ===
+        const bool lead = elect_one();
+        const uint64_t d_q = smem_desc_sw128(sb + SM::OFF_Q, 16, 1024);
+        const uint64_t d_k = smem_desc_sw128(sb + SM::OFF_R, 16, 1024);
+        const uint64_t d_v = smem_desc_sw128(sb + SM::OFF_R, kBlk, 1024);
+        constexpr uint32_t ID_S = idesc_f16(128, kTile, 0, 0);
+        constexpr uint32_t ID_O = idesc_f16(128, D, 0, 1), ID_O64 = idesc_f16(128, 64, 0, 1);
+        auto wait = [&](int i, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_abort(bar(i), parity, abort_flag)) != 0;
+        };
+        auto wait_blocks = [&](int n, int count) {
+            bool ok = true;
+            for (int u = n; u < n + count && ok; ++u) ok = wait(SM::B_FULL + u % NR, (u / NR) & 1);
+            return ok;
+        };
+        auto free_blocks = [&](int n, int count) {
+            for (int u = n; u < n + count; ++u) umma_commit(bar(SM::B_FREE + u % NR));
+        };
+        auto issue_s = [&](int j, int i) {  // S_j = Q_j K_i^T
 #pragma unroll
-                for (int kk = 0; kk < KB * 4; ++kk) {
-                    const uint32_t slot = (uint32_t)(i * NB + (kk >> 2)) % NR;
-                    umma_bf16(tmem + 256 * j, d_q + ((j * SM::Q_TILE + (kk >> 2) * kBlk + (kk & 3) * 32) >> 4),
-                              d_k + ((slot * kBlk + (kk & 3) * 32) >> 4), ID_S, kk > 0);
-                }
-                umma_commit(bar(SM::B_S + j));
-            };
-            auto issue_o = [&](int j, int i) {  // O_j (+)= P_j V_i, P_j from TMEM
-                const uint32_t slot = (uint32_t)(i * NB + KB) % NR;
-                const uint32_t o = tmem + 256 * j + 128, pj = tmem + 256 * j;
-                if (VB == 1 || slot + 1 < NR) {
+            for (int kb = 0; kb < KB; ++kb) {
+                const uint64_t k = d_k + ((((uint32_t)(i * NB + kb) % NR) * kBlk) >> 4);
+                const uint64_t q = d_q + ((j * SM::Q_TILE + kb * kBlk) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        umma_bf16_ts(o, pj + 8 * kk, d_v + ((slot * kBlk + kk * 2048) >> 4), ID_O,
-                                     (i > 0 || kk > 0) ? 1u : 0u);
-                } else {  // the tile's second block is at the ring's start: 64 dims at a time
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16(tmem + 256 * j, q + ((kk * 32) >> 4), k + ((kk * 32) >> 4), ID_S,
+                              (kb > 0 || kk > 0) ? 1u : 0u);
+            }
+            umma_commit(bar(SM::B_S + j));
+        };
+        auto issue_o = [&](int j, int i) {  // O_j (+)= P_j V_i, P_j from TMEM
+            const uint32_t slot = (uint32_t)(i * NB + KB) % NR;
+            const uint32_t o = tmem + 256 * j + 128, pj = tmem + 256 * j;
+            const uint64_t v = d_v + ((slot * kBlk) >> 4);
+            if (VB == 1 || slot + 1 < NR) {
 #pragma unroll
-                    for (int v = 0; v < 2; ++v)
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    umma_bf16_ts(o, pj + 8 * kk, v + ((kk * 2048) >> 4), ID_O, (i > 0 || kk > 0) ? 1u : 0u);
+            } else {  // the tile's second block is at the ring's start: 64 dims at a time
 #pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            umma_bf16_ts(o + 64 * v, pj + 8 * kk,
-                                         d_v + (((v ? 0 : slot) * kBlk + kk * 2048) >> 4), ID_O64,
-                                         (i > 0 || kk > 0) ? 1u : 0u);
-                }
-            };
-            bool ok = wait_blocks(0, KB);
-            if (ok) {
-                tc_fence_after();
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    umma_bf16_ts(o, pj + 8 * kk, v + ((kk * 2048) >> 4), ID_O64, (i > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    umma_bf16_ts(o + 64, pj + 8 * kk, d_v + ((kk * 2048) >> 4), ID_O64,
+                                 (i > 0 || kk > 0) ? 1u : 0u);
+            }
+        };
+        bool ok = wait_blocks(0, KB);
+        if (ok) {
+            tc_fence_after();
+            if (lead) {
                 issue_s(0, 0);
                 if (nt1 > 0) issue_s(1, 0);
                 free_blocks(0, KB);
             }
-            for (int i = 0; i < n_tiles && ok; ++i) {
+            __syncwarp();
+        }
+        for (int i = 0; i < n_tiles && ok; ++i) {
 #pragma unroll 1
-                for (int j = 0; j < 2 && ok; ++j) {
-                    const int nt = j ? nt1 : nt0;
-                    if (j == 0) ok = wait_blocks(i * NB + KB, VB);
-                    if (ok && i < nt) {
-                        ok = wait_or_abort(bar(SM::B_P + j), i & 1, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_o(j, i);
-                        if (i == nt - 1) umma_commit(bar(SM::B_O + j));
-                    }
-                    if (!ok) break;
+            for (int j = 0; j < 2 && ok; ++j) {
+                const int nt = j ? nt1 : nt0;
+                if (j == 0) ok = wait_blocks(i * NB + KB, VB);
+                if (ok && i < nt) ok = wait(SM::B_P + j, i & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lead) {
+                    if (i < nt) issue_o(j, i);
+                    if (i == nt - 1) umma_commit(bar(SM::B_O + j));
                     if (j == 1) free_blocks(i * NB + KB, VB);
-                    if (i + 1 < n_tiles) {
-                        if (j == 0) ok = wait_blocks((i + 1) * NB, KB);
-                        if (!ok) break;
-                        tc_fence_after();
+                }
+                __syncwarp();
+                if (i + 1 < n_tiles) {
+                    if (j == 0) ok = wait_blocks((i + 1) * NB, KB);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lead) {
                         if (i + 1 < nt) issue_s(j, i + 1);
                         if (j == 1) free_blocks((i + 1) * NB, KB);
                     }
+                    __syncwarp();
                 }
             }
+        }
+        if (lead) {
             if (!ok) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
             umma_commit(bar(SM::B_END));  // every product is done before TMEM goes (bounded)
             (void)mbar_wait_bounded(bar(SM::B_END), 0);
