@@ -270,17 +270,6 @@ static_assert(AttSmem<4>::ALLOC + 1024 <= 232448, "shared memory per CTA");
 // TMEM: scores of even and odd pages, then O^T of every unit
 constexpr uint32_t kTmemS = 0, kTmemO = 128, kTmemCols = 256;
 
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 // 16 lanes x 64 columns of TMEM words: register 4j + e of thread t holds lane (base + t / 4 +
 // 8 (e / 2)), column 8j + 2 (t % 4) + e % 2.
 __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
@@ -323,10 +312,12 @@ __device__ __forceinline__ bool bar_softmax_or(bool pred) {
 struct Walk {
     int b, at, seg_begin, seg_end;
     __device__ __forceinline__ void seek(const LatentParams &p, int end) {  // at == seg_end < end
-        do ++b;
-        while (p.cum[b + 1] <= at);  // skips sequences without pages; ends: cum[B] >= end > at
+        do {
+            ++b;
+            seg_end = uniform(p.cum[b + 1]);
+        } while (seg_end <= at);  // skips sequences without pages; ends: cum[B] >= end > at
         seg_begin = at;
-        seg_end = min(end, p.cum[b + 1]);
+        seg_end = min(end, seg_end);
     }
 };
 
@@ -350,7 +341,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
     int *s_first = reinterpret_cast<int *>(misc + 8);                 // first sequence of the range
     volatile int *page_ok = reinterpret_cast<volatile int *>(misc + 16);  // [NS]
     float(*s_red)[kRows] = reinterpret_cast<float(*)[kRows]>(misc + 64);  // [4][32]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int group = blockIdx.x % p.n_groups, range = blockIdx.x / p.n_groups;
 
     if (tid == 0) {
@@ -367,7 +358,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
     }
     griddep_launch_dependents();
     griddep_wait();  // the image, the appended rows and the schedule are kernel 1's
-    const int P = p.cum[p.B];
+    const int P = uniform(p.cum[p.B]);
     const int n_live = min(p.n_ranges, P);
     const int begin = range < n_live ? range_begin(range, P, n_live) : 0;
     const int end = range < n_live ? range_begin(range + 1, P, n_live) : 0;
@@ -387,12 +378,12 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
     const int n_pages = end - begin;
     Walk w;
-    w.b = n_pages > 0 ? *s_first : 0;
+    w.b = n_pages > 0 ? uniform(*s_first) : 0;
     w.at = w.seg_begin = begin;
-    w.seg_end = n_pages > 0 ? min(end, p.cum[w.b + 1]) : begin;
+    w.seg_end = n_pages > 0 ? min(end, uniform(p.cum[w.b + 1])) : begin;
 
     if (warp == 4) {
         // ================= copies: the queries of each sequence, and its pages ==============
@@ -453,77 +444,66 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
     } else if (warp == 5) {
         // ================= products, whichever is ready first (the warp converged) ===========
         const bool lead = elect_one();
-        const uint64_t d_q = smem_desc_sw128(sb + SM::OFF_Q, 16, 1024);
-        const uint64_t d_k = smem_desc_sw128(sb + SM::OFF_C, 16, 1024);    // keys x dims
-        const uint64_t d_v = smem_desc_sw128(sb + SM::OFF_C, kBlk, 1024);  // dims x keys
-        const uint64_t d_p = smem_desc_sw128(sb + SM::OFF_P, 16, 1024);
+        const Desc d_q(smem_desc_sw128(sb + SM::OFF_Q, 16, 1024));
+        const Desc d_k(smem_desc_sw128(sb + SM::OFF_C, 16, 1024));    // keys x dims
+        const Desc d_v(smem_desc_sw128(sb + SM::OFF_C, kBlk, 1024));  // dims x keys
+        const Desc d_p(smem_desc_sw128(sb + SM::OFF_P, 16, 1024));
         constexpr uint32_t ID_S = idesc_bf16(64, 2 * kRows, 0, 0);
         constexpr uint32_t ID_O = idesc_bf16(128, kRows, 1, 0);
-        int s = 0, su = 0, pv = 0, seg = 0;
+        int s = 0, pv = 0, seg = 0;
         Walk ws = w, wp = w;  // the sequences of the next scores and of the next output product
         bool ok = true;
         unsigned long long t0 = 0;
         while (pv < n_pages) {
             bool moved = false;
-            if (pv < s && __all_sync(0xffffffffu, mbar_test(bar(SM::B_P + (pv & 1)), (pv >> 1) & 1))) {
+            if (pv < s && mbar_test_warp(lead, bar(SM::B_P + (pv & 1)), (pv >> 1) & 1)) {
                 // O^T += C^T P^T, unit by unit; each unit's page slot is free after it
                 tc_fence_after();
                 if (wp.at == wp.seg_end) wp.seek(p, end);
                 const int st = pv % NS;
                 const bool fresh = __all_sync(0xffffffffu, wp.at == wp.seg_begin);
-                if (lead) {
+                const Desc v = d_v.at(st * PAGE), pt = d_p.at((pv & 1) * kRows * 128);
 #pragma unroll
-                    for (int u = 0; u < NP; ++u) {
+                for (int u = 0; u < NP; ++u) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16(tmem + kTmemO + u * kRows,
-                                      d_v + ((st * PAGE + u * 2 * kBlk + kk * 2048) >> 4),
-                                      d_p + (((pv & 1) * kRows * 128 + kk * 32) >> 4), ID_O,
-                                      (fresh && kk == 0) ? 0u : 1u);
-                        umma_commit(free_(st, u));
-                    }
-                    umma_commit(bar(SM::B_O + (pv & 1)));
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_if(lead, tmem + kTmemO + u * kRows, v.at(u * 2 * kBlk + kk * 2048),
+                                pt.at(kk * 32), ID_O, (fresh && kk == 0) ? 0u : 1u);
+                    umma_commit_if(lead, free_(st, u));
                 }
-                __syncwarp();
+                umma_commit_if(lead, bar(SM::B_O + (pv & 1)));
                 ++wp.at;
                 ++pv;
                 moved = true;
             } else if (s < n_pages && s <= pv + 1) {
-                // S^T = C [q~hi ; q~lo]^T, unit by unit as they land (the scores before last
-                // have been read: their output product is issued)
+                // S^T = C [q~hi ; q~lo]^T once the page (and a new sequence's queries) landed: lane u
+                // asks for unit u. The scores before last have been read: their output product is
+                // issued. (Unit by unit as they land, the questions cost more than the products.)
                 if (ws.at == ws.seg_end) ws.seek(p, end);
-                const int st = s % NS, u = su == 0 ? NP : su - 1;
-                const bool ready = (su > 0 || ws.at > ws.seg_begin || mbar_test(bar(SM::B_QFULL), seg & 1)) &&
-                                   mbar_test(full(st, u), (s / NS) & 1);
-                if (__all_sync(0xffffffffu, ready)) {
+                const int st = s % NS;
+                const bool asks = lane < NU || (lane == NU && ws.at == ws.seg_begin);
+                const bool ready = mbar_test_if(asks, lane < NU ? full(st, lane) : bar(SM::B_QFULL),
+                                                (lane < NU ? s / NS : seg) & 1);
+                if (__all_sync(0xffffffffu, ready || !asks)) {
+                    __syncwarp();
                     tc_fence_after();
                     const uint32_t d = tmem + kTmemS + (s & 1) * 64;
-                    const uint64_t ku = d_k + ((st * PAGE + u * 2 * kBlk) >> 4);
-                    const uint64_t qu = d_q + ((u * 2 * kBlk) >> 4);
-                    if (lead) {
-                        // the shared part comes first and starts the sums
+                    const Desc kd = d_k.at(st * PAGE);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16(d, ku + ((kk * 32) >> 4), qu + ((kk * 32) >> 4), ID_S,
-                                      (su == 0 && kk == 0) ? 0u : 1u);
-                        if (su > 0) {
+                    for (int v = 0; v < NU; ++v) {
+                        const int u = v == 0 ? NP : v - 1;  // the shared part's slot is free first
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16(d, ku + ((kBlk + kk * 32) >> 4), qu + ((kBlk + kk * 32) >> 4),
-                                          ID_S, 1u);
-                        } else {
-                            umma_commit(free_(st, NP));
+                        for (int kk = 0; kk < (u == NP ? 4 : 8); ++kk) {
+                            const uint32_t off = u * 2 * kBlk + (kk >> 2) * kBlk + (kk & 3) * 32;
+                            umma_if(lead, d, kd.at(off), d_q.at(off), ID_S, (v > 0 || kk > 0) ? 1u : 0u);
                         }
-                        if (su == NP) umma_commit(bar(SM::B_S + (s & 1)));
+                        if (u == NP) umma_commit_if(lead, free_(st, NP));
                     }
-                    __syncwarp();
-                    if (++su == NU) {
-                        su = 0;
-                        ++s;
-                        if (__all_sync(0xffffffffu, ++ws.at == ws.seg_end)) {
-                            if (lead) umma_commit(bar(SM::B_QFREE));
-                            ++seg;
-                        }
+                    umma_commit_if(lead, bar(SM::B_S + (s & 1)));
+                    ++s;
+                    if (__all_sync(0xffffffffu, ++ws.at == ws.seg_end)) {
+                        umma_commit_if(lead, bar(SM::B_QFREE));
+                        ++seg;
                     }
                     moved = true;
                 }
@@ -550,6 +530,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
         __syncwarp();
     } else {
         // ================= softmax and the partial results =====================================
+        const bool lead = elect_one();
         const int c0 = (lane & 3) * 2;  // this thread's columns: 8j + c0, 8j + c0 + 1, j < 4
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
         bool ok = true;
@@ -568,10 +549,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
             }
             for (; w.at < w.seg_end; ++w.at, ++k) {
                 const int st = k % NS, pos0 = (w.at - page0) * kPT;
-                ok = wait_or_abort(bar(SM::B_S + (k & 1)), (k >> 1) & 1, abort_flag);
+                ok = wait_or_abort_warp(lead, bar(SM::B_S + (k & 1)), (k >> 1) & 1, abort_flag);
                 // P's tile of two pages ago has been read
-                if (ok && k >= 2) ok = wait_or_abort(bar(SM::B_O + (k & 1)), ((k - 2) >> 1) & 1, abort_flag);
-                if (ok) ok = wait_or_abort(full(st, 0), (k / NS) & 1, abort_flag);  // page_ok
+                if (ok && k >= 2) ok = wait_or_abort_warp(lead, bar(SM::B_O + (k & 1)), ((k - 2) >> 1) & 1, abort_flag);
+                if (ok) ok = wait_or_abort_warp(lead, full(st, 0), (k / NS) & 1, abort_flag);  // page_ok
                 ok = !bar_softmax_or(!ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -628,7 +609,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
 #pragma unroll
                             for (int j = 0; j < 8; ++j) s_red[0][(j >> 1) * 8 + c0 + (j & 1)] = f[j];
                         bar_softmax();
-                        ok = wait_or_abort(bar(SM::B_O + ((k - 1) & 1)), ((k - 1) >> 1) & 1, abort_flag);
+                        ok = wait_or_abort_warp(lead, bar(SM::B_O + ((k - 1) & 1)), ((k - 1) >> 1) & 1, abort_flag);
                         ok = !bar_softmax_or(!ok);
                         if (!ok) break;
                         tc_fence_after();
@@ -685,7 +666,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
             }
             const size_t piece = part_index(p, range, b, group);
             float *ml = p.part_ml + piece * kRows * 2;
-            if (ok) ok = wait_or_abort(bar(SM::B_O + ((k - 1) & 1)), ((k - 1) >> 1) & 1, abort_flag);
+            if (ok) ok = wait_or_abort_warp(lead, bar(SM::B_O + ((k - 1) & 1)), ((k - 1) >> 1) & 1, abort_flag);
             ok = !bar_softmax_or(!ok);
             if (!ok) {
                 // this piece and the range's later ones are marked as missing

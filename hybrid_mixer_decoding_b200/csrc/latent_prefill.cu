@@ -157,7 +157,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     auto bar = [&](int i) { return bars + 8 * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SM::OFF_MISC + 8 * SM::N_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + SM::OFF_MISC + 8 * SM::N_BARS + 4);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int tiles = p.s_pad / kTile, tile = blockIdx.x / p.splits;
     const int b = tile / tiles, pos0 = (tile - b * tiles) * kTile;
     const int ha = (blockIdx.x % p.splits) * p.per_split, hb = min(p.heads, ha + p.per_split);
@@ -180,7 +180,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
     if (warp == 4) {
         if (lane == 0) {
@@ -222,11 +222,11 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         __syncwarp();
     } else if (warp == 5) {
         const bool lead = elect_one();
-        const uint64_t d_a = smem_desc_sw128(sb + SM::OFF_A, 16, 1024);
-        const uint64_t d_w = smem_desc_sw128(sb + SM::OFF_W, 16, 1024);
+        const Desc d_a(smem_desc_sw128(sb + SM::OFF_A, 16, 1024));
+        const Desc d_w(smem_desc_sw128(sb + SM::OFF_W, 16, 1024));
         constexpr uint32_t ID = idesc_bf16(128, 2 * D, 0, 0);
         auto wait = [&](int i, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_abort(bar(i), parity, abort_flag)) != 0;
+            return wait_or_abort_warp(lead, bar(i), parity, abort_flag);
         };
         bool ok = wait(SM::B_A, 0);
         int n = 0;
@@ -237,15 +237,13 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
                 ok = wait(SM::B_WFULL + w, (n / SM::NW) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                if (lead) {
+                const Desc a = d_a.at(kc * kBlk), wd = d_w.at(w * SM::W_STAGE);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16(tmem + (st & 1) * 256, d_a + ((kc * kBlk + kk * 32) >> 4),
-                                  d_w + ((w * SM::W_STAGE + kk * 32) >> 4), ID, (kc > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit(bar(SM::B_WFREE + w));
-                    if (kc == n_kc - 1) umma_commit(bar(SM::B_ACC + (st & 1)));
-                }
-                __syncwarp();
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_if(lead, tmem + (st & 1) * 256, a.at(kk * 32), wd.at(kk * 32), ID,
+                            (kc > 0 || kk > 0) ? 1u : 0u);
+                umma_commit_if(lead, bar(SM::B_WFREE + w));
+                if (kc == n_kc - 1) umma_commit_if(lead, bar(SM::B_ACC + (st & 1)));
             }
         }
         if (lead) {
@@ -258,11 +256,10 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         const int pos = pos0 + warp * 32 + lane;
         const bool live = pos < s.total && page_of(p, b, pos) >= 0;
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        const bool lead = elect_one();
         bool out = false;
         for (int st = 0; st < n_steps; ++st) {
-            bool ok = wait_or_abort(bar(SM::B_ACC + (st & 1)), (st >> 1) & 1, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {
+            if (!wait_or_abort_warp(lead, bar(SM::B_ACC + (st & 1)), (st >> 1) & 1, abort_flag)) {
                 if (lane == 0) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
                 break;
             }
@@ -342,7 +339,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     auto bar = [&](int i) { return bars + 8 * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SM::OFF_BAR + 8 * SM::N_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + SM::OFF_BAR + 8 * SM::N_BARS + 4);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int bh = blockIdx.x % (p.B * p.heads);
     const int qb = p.n_qb - 1 - (int)(blockIdx.x / (p.B * p.heads));  // longest blocks first
     const int b = bh / p.heads, hl = bh - b * p.heads, h = p.h0 + hl;
@@ -352,8 +349,8 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     const int t_first = qb * 2 * kTile, t_last = min(s.n, t_first + 2 * kTile) - 1;
     if (t_first >= s.n) return;
     // key tiles of each query tile: up to its last row's position (none without rows)
-    const int nt0 = (s.prefix + min(t_last, t_first + kTile - 1)) / kTile + 1;
-    const int nt1 = t_last >= t_first + kTile ? (s.prefix + t_last) / kTile + 1 : 0;
+    const int nt0 = uniform((s.prefix + min(t_last, t_first + kTile - 1)) / kTile + 1);
+    const int nt1 = uniform(t_last >= t_first + kTile ? (s.prefix + t_last) / kTile + 1 : 0);
     const int n_tiles = max(nt0, nt1);
     if (tid == 0) {
         for (int i = 0; i < SM::N_BARS; ++i) mbar_init(bar(i), (i == SM::B_P || i == SM::B_P + 1) ? 4 : 1);
@@ -395,7 +392,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
     if (warp == 9) {
         // ================= copies: block n of the stream of tiles into slot n % NR ==============
@@ -426,13 +423,13 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     } else if (warp == 8) {
         // ================= products: O_0(i), S_0(i+1), O_1(i), S_1(i+1) (the warp converged) ===
         const bool lead = elect_one();
-        const uint64_t d_q = smem_desc_sw128(sb + SM::OFF_Q, 16, 1024);
-        const uint64_t d_k = smem_desc_sw128(sb + SM::OFF_R, 16, 1024);
-        const uint64_t d_v = smem_desc_sw128(sb + SM::OFF_R, kBlk, 1024);
+        const Desc d_q(smem_desc_sw128(sb + SM::OFF_Q, 16, 1024));
+        const Desc d_k(smem_desc_sw128(sb + SM::OFF_R, 16, 1024));
+        const Desc d_v(smem_desc_sw128(sb + SM::OFF_R, kBlk, 1024));
         constexpr uint32_t ID_S = idesc_f16(128, kTile, 0, 0);
         constexpr uint32_t ID_O = idesc_f16(128, D, 0, 1), ID_O64 = idesc_f16(128, 64, 0, 1);
         auto wait = [&](int i, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_abort(bar(i), parity, abort_flag)) != 0;
+            return wait_or_abort_warp(lead, bar(i), parity, abort_flag);
         };
         auto wait_blocks = [&](int n, int count) {
             bool ok = true;
@@ -440,47 +437,44 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
             return ok;
         };
         auto free_blocks = [&](int n, int count) {
-            for (int u = n; u < n + count; ++u) umma_commit(bar(SM::B_FREE + u % NR));
+            for (int u = n; u < n + count; ++u) umma_commit_if(lead, bar(SM::B_FREE + u % NR));
         };
         auto issue_s = [&](int j, int i) {  // S_j = Q_j K_i^T
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                const uint64_t k = d_k + ((((uint32_t)(i * NB + kb) % NR) * kBlk) >> 4);
-                const uint64_t q = d_q + ((j * SM::Q_TILE + kb * kBlk) >> 4);
+                const Desc k = d_k.at(((uint32_t)(i * NB + kb) % NR) * kBlk);
+                const Desc q = d_q.at(j * SM::Q_TILE + kb * kBlk);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_bf16(tmem + 256 * j, q + ((kk * 32) >> 4), k + ((kk * 32) >> 4), ID_S,
-                              (kb > 0 || kk > 0) ? 1u : 0u);
+                    umma_if(lead, tmem + 256 * j, q.at(kk * 32), k.at(kk * 32), ID_S,
+                            (kb > 0 || kk > 0) ? 1u : 0u);
             }
-            umma_commit(bar(SM::B_S + j));
+            umma_commit_if(lead, bar(SM::B_S + j));
         };
         auto issue_o = [&](int j, int i) {  // O_j (+)= P_j V_i, P_j from TMEM
             const uint32_t slot = (uint32_t)(i * NB + KB) % NR;
             const uint32_t o = tmem + 256 * j + 128, pj = tmem + 256 * j;
-            const uint64_t v = d_v + ((slot * kBlk) >> 4);
+            const Desc v = d_v.at(slot * kBlk);
+            const uint32_t more = i > 0 ? 1u : 0u;
             if (VB == 1 || slot + 1 < NR) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                    umma_bf16_ts(o, pj + 8 * kk, v + ((kk * 2048) >> 4), ID_O, (i > 0 || kk > 0) ? 1u : 0u);
+                    umma_ts_if(lead, o, pj + 8 * kk, v.at(kk * 2048), ID_O, kk > 0 ? 1u : more);
             } else {  // the tile's second block is at the ring's start: 64 dims at a time
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                    umma_bf16_ts(o, pj + 8 * kk, v + ((kk * 2048) >> 4), ID_O64, (i > 0 || kk > 0) ? 1u : 0u);
+                    umma_ts_if(lead, o, pj + 8 * kk, v.at(kk * 2048), ID_O64, kk > 0 ? 1u : more);
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                    umma_bf16_ts(o + 64, pj + 8 * kk, d_v + ((kk * 2048) >> 4), ID_O64,
-                                 (i > 0 || kk > 0) ? 1u : 0u);
+                    umma_ts_if(lead, o + 64, pj + 8 * kk, d_v.at(kk * 2048), ID_O64, kk > 0 ? 1u : more);
             }
         };
         bool ok = wait_blocks(0, KB);
         if (ok) {
             tc_fence_after();
-            if (lead) {
-                issue_s(0, 0);
-                if (nt1 > 0) issue_s(1, 0);
-                free_blocks(0, KB);
-            }
-            __syncwarp();
+            issue_s(0, 0);
+            if (nt1 > 0) issue_s(1, 0);
+            free_blocks(0, KB);
         }
         for (int i = 0; i < n_tiles && ok; ++i) {
 #pragma unroll 1
@@ -490,21 +484,15 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                 if (ok && i < nt) ok = wait(SM::B_P + j, i & 1);
                 if (!ok) break;
                 tc_fence_after();
-                if (lead) {
-                    if (i < nt) issue_o(j, i);
-                    if (i == nt - 1) umma_commit(bar(SM::B_O + j));
-                    if (j == 1) free_blocks(i * NB + KB, VB);
-                }
-                __syncwarp();
+                if (i < nt) issue_o(j, i);
+                if (i == nt - 1) umma_commit_if(lead, bar(SM::B_O + j));
+                if (j == 1) free_blocks(i * NB + KB, VB);
                 if (i + 1 < n_tiles) {
                     if (j == 0) ok = wait_blocks((i + 1) * NB, KB);
                     if (!ok) break;
                     tc_fence_after();
-                    if (lead) {
-                        if (i + 1 < nt) issue_s(j, i + 1);
-                        if (j == 1) free_blocks((i + 1) * NB, KB);
-                    }
-                    __syncwarp();
+                    if (i + 1 < nt) issue_s(j, i + 1);
+                    if (j == 1) free_blocks((i + 1) * NB, KB);
                 }
             }
         }
@@ -519,11 +507,11 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         const int nt = qt ? nt1 : nt0;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t s_col = lane_base + 256 * qt, o_col = s_col + 128;
+        const bool lead = elect_one();
         float m_base = -INFINITY, l_run = 0.f;
         bool ok = true;
         for (int i = 0; i < nt && ok; ++i) {
-            ok = wait_or_abort(bar(SM::B_S + qt), i & 1, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);  // the TMEM accesses below run converged
+            ok = wait_or_abort_warp(lead, bar(SM::B_S + qt), i & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
             float x[kTile];
@@ -608,8 +596,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(SM::B_P + qt));
         }
-        if (ok) ok = wait_or_abort(bar(SM::B_O + qt), 0, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
+        if (ok) ok = wait_or_abort_warp(lead, bar(SM::B_O + qt), 0, abort_flag);
         if (ok) {
             tc_fence_after();
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;

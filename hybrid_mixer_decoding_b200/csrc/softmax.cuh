@@ -69,10 +69,10 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
     }
 }
 
-// One lane of a converged warp. The warps that issue tcgen05.mma run converged, take their
-// branches by warp votes and issue under this predicate: operands that the compiler can see are
-// the same in the whole warp cost one instruction each, others about 140 cycles per product
-// (measured; a 64 x 64 x 16 product takes 32, a 128 x 128 x 16 one 64).
+// A value that is the same in the whole warp, in a form in which the compiler knows it.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile(
@@ -81,6 +81,88 @@ __device__ __forceinline__ bool elect_one() {
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(p));
     return p != 0;
+}
+
+// tcgen05.mma and commit by a whole converged warp, of which only the lane with `lead` issues:
+// without a branch around them, and with the descriptors' changing low words as 32-bit values
+// equal in the warp, a product issues in the time it runs (32 cycles at 64 x 64 x 16, measured).
+// One lane in a branch of its own took 48 to 140.
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ explicit Desc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
+    __device__ __forceinline__ Desc at(uint32_t bytes) const {  // below 256 KiB: no carry
+        Desc d = *this;
+        d.lo += bytes >> 4;
+        return d;
+    }
+};
+__device__ __forceinline__ void umma_if(bool lead, uint32_t d_tmem, Desc a, Desc b, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}"
+        ::"r"(d_tmem), "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate),
+          "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts_if(bool lead, uint32_t d_tmem, uint32_t a_tmem, Desc b,
+                                           uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate),
+          "r"((uint32_t)lead)
+        : "memory");
+}
+// Whether phase `parity` of a barrier is complete, asked by the lanes with `asks` (others: false).
+__device__ __forceinline__ bool mbar_test_if(bool asks, uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %3, 0;\n\t"
+        "setp.ne.b32 p, 0, 0;\n\t"
+        "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"((uint32_t)asks)
+        : "memory");
+    return ok != 0;
+}
+// The same for a whole converged warp, asked by its lane with `lead`.
+__device__ __forceinline__ bool mbar_test_warp(bool lead, uint32_t bar, uint32_t parity) {
+    const bool ok = __any_sync(0xffffffffu, mbar_test_if(lead, bar, parity));
+    __syncwarp();  // what the asking lane has seen is seen by all: a vote alone orders nothing
+    return ok;
+}
+// wait_or_abort for a whole converged warp: one lane waits. (128 threads that spin on a barrier keep
+// the shared-memory pipe busy and slow down the warp that issues the products.)
+__device__ __forceinline__ bool wait_or_abort_warp(bool lead, uint32_t bar, uint32_t parity,
+                                                   volatile int *abort) {
+    bool done = mbar_test_warp(lead, bar, parity);
+    if (!done) {
+        const unsigned long long t0 = globaltimer_ns();
+        while (!(done = mbar_test_warp(lead, bar, parity))) {
+            const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+            if (late) *abort = 1;
+            if (__any_sync(0xffffffffu, late || *abort)) break;
+        }
+    }
+    return done;
+}
+__device__ __forceinline__ void umma_commit_if(bool lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(bar), "r"((uint32_t)lead)
+        : "memory");
 }
 
 }  // namespace hmd
