@@ -126,27 +126,44 @@ __global__ void __launch_bounds__(kAbsThreads) latent_absorb_kernel(const Latent
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_launch_dependents();
     griddep_wait();
+    const int n_tok = p.B * p.nq, dq = D + kDR, row_w = p.dc + kDR;
     if (blockIdx.x == gridDim.x - 1) {
         schedule_block(p);
         return;
     }
+    const int n_app = (n_tok + kAbsThreads / 32 - 1) / (kAbsThreads / 32);
+    if (blockIdx.x >= gridDim.x - 1 - n_app) {
+        // append: a warp copies the row of token (b, i) to position L - nq + i
+        const int tok = (blockIdx.x - (gridDim.x - 1 - n_app)) * (kAbsThreads / 32) + warp;
+        if (tok >= n_tok) return;
+        const int b = tok / p.nq, L = p.seq_lens[b];
+        if (L < p.nq || L > p.max_seq_len) return;
+        const int pos = L - p.nq + (tok - b * p.nq);
+        const int pg = p.page_table[(size_t)b * p.max_pages + pos / kPT];
+        if (pg < 0 || pg >= p.n_pages) {
+            if (lane == 0) atomicOr(&g_err, HMD_DEVERR_PAGE);
+            return;
+        }
+        __nv_bfloat16 *dst = p.pool + ((size_t)pg * kPT + pos % kPT) * row_w;
+        for (int c = lane * 8; c < row_w; c += 256)
+            *reinterpret_cast<uint4 *>(dst + c) =
+                *reinterpret_cast<const uint4 *>(p.new_c + (size_t)tok * row_w + c);
+        return;
+    }
     const int n_cols = p.dc / 128;
     const int cc = blockIdx.x % n_cols, h = (blockIdx.x / n_cols) % p.H;
-    const int tok0 = blockIdx.x / (n_cols * p.H) * kAbsTok, n_tok = p.B * p.nq;
-    const int rows = min(kAbsTok, n_tok - tok0), dq = D + kDR, row_w = p.dc + kDR;
-    // operands to shared memory
+    const int tok0 = blockIdx.x / (n_cols * p.H) * kAbsTok;
+    const int rows = min(kAbsTok, n_tok - tok0);
+    // operands to shared memory, all copies in flight at once
     const __nv_bfloat16 *w = p.w_uk + h * p.w_uk_head + cc * 128;
     for (int idx = tid; idx < D * 16; idx += kAbsThreads) {
         const int n = idx >> 4, c = (idx & 15) * 8;
-        *reinterpret_cast<uint4 *>(&sm.w[n][c]) =
-            *reinterpret_cast<const uint4 *>(w + (size_t)n * p.dc + c);
+        cp_async16(smem_u32(&sm.w[n][c]), w + (size_t)n * p.dc + c);
     }
     for (int idx = tid; idx < kAbsTok * (D / 8); idx += kAbsThreads) {
         const int r = idx / (D / 8), c = idx % (D / 8) * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-            v = *reinterpret_cast<const uint4 *>(p.q + ((size_t)(tok0 + r) * p.H + h) * dq + c);
-        *reinterpret_cast<uint4 *>(&sm.q[r][c]) = v;
+        if (r < rows) cp_async16(smem_u32(&sm.q[r][c]), p.q + ((size_t)(tok0 + r) * p.H + h) * dq + c);
+        else *reinterpret_cast<uint4 *>(&sm.q[r][c]) = make_uint4(0, 0, 0, 0);
     }
     const size_t img_bytes = (size_t)(p.dc / 64 + 1) * kBlk;
     // image address of (token, head) row r of group r / 32, in the block of dims col..
@@ -156,14 +173,20 @@ __global__ void __launch_bounds__(kAbsThreads) latent_absorb_kernel(const Latent
                blk_off(r % kRows + (lo ? kRows : 0), col & 63) + (col & 7) * 2;
     };
     if (cc == 0) {
-        // the queries' shared part
-        for (int idx = tid; idx < rows * kDR; idx += kAbsThreads) {
-            const int tok = tok0 + idx / kDR, c = idx % kDR;
-            const float x = __bfloat162float(p.q[((size_t)tok * p.H + h) * dq + D + c]) * p.scale_log2;
-            const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-            *reinterpret_cast<__nv_bfloat16 *>(img(tok, h, p.dc + c, false)) = hi;
-            *reinterpret_cast<__nv_bfloat16 *>(img(tok, h, p.dc + c, true)) =
-                __float2bfloat16_rn(x - __bfloat162float(hi));
+        // the queries' shared part, 8 dims a thread
+        for (int idx = tid; idx < rows * (kDR / 8); idx += kAbsThreads) {
+            const int tok = tok0 + idx / (kDR / 8), c = idx % (kDR / 8) * 8;
+            const uint4 in = *reinterpret_cast<const uint4 *>(p.q + ((size_t)tok * p.H + h) * dq + D + c);
+            const uint32_t x[4] = {in.x, in.y, in.z, in.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x0 = bf16_lo(x[e]) * p.scale_log2, x1 = bf16_hi(x[e]) * p.scale_log2;
+                hi[e] = pack_bf16x2(x0, x1);
+                lo[e] = pack_bf16x2(x0 - bf16_lo(hi[e]), x1 - bf16_hi(hi[e]));
+            }
+            *reinterpret_cast<uint4 *>(img(tok, h, p.dc + c, false)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(img(tok, h, p.dc + c, true)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
     if (h == 0 && cc == n_cols - 1) {
@@ -181,22 +204,7 @@ __global__ void __launch_bounds__(kAbsThreads) latent_absorb_kernel(const Latent
             }
         }
     }
-    if (h == p.H - 1 && cc == 0) {
-        // append: token (b, i) at position L - nq + i
-        for (int idx = tid; idx < rows * (row_w / 8); idx += kAbsThreads) {
-            const int tok = tok0 + idx / (row_w / 8), c = idx % (row_w / 8) * 8;
-            const int b = tok / p.nq, L = p.seq_lens[b];
-            if (L < p.nq || L > p.max_seq_len) continue;
-            const int pos = L - p.nq + (tok - b * p.nq);
-            const int pg = p.page_table[(size_t)b * p.max_pages + pos / kPT];
-            if (pg < 0 || pg >= p.n_pages) {
-                atomicOr(&g_err, HMD_DEVERR_PAGE);
-                continue;
-            }
-            *reinterpret_cast<uint4 *>(p.pool + ((size_t)pg * kPT + pos % kPT) * row_w + c) =
-                *reinterpret_cast<const uint4 *>(p.new_c + (size_t)tok * row_w + c);
-        }
-    }
+    cp_async_wait_all();
     __syncthreads();
     // 32 tokens x 128 latent dims: a warp takes 32 of the dims
     float acc[2][4][4] = {};
@@ -482,10 +490,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
                 if (ws.at == ws.seg_end) ws.seek(p, end);
                 const int st = s % NS;
                 const bool asks = lane < NU || (lane == NU && ws.at == ws.seg_begin);
-                const bool ready = mbar_test_if(asks, lane < NU ? full(st, lane) : bar(SM::B_QFULL),
-                                                (lane < NU ? s / NS : seg) & 1);
-                if (__all_sync(0xffffffffu, ready || !asks)) {
-                    __syncwarp();
+                if (mbar_test_warp(asks, lane < NU ? full(st, lane) : bar(SM::B_QFULL),
+                                   (lane < NU ? s / NS : seg) & 1)) {
                     tc_fence_after();
                     const uint32_t d = tmem + kTmemS + (s & 1) * 64;
                     const Desc kd = d_k.at(st * PAGE);
@@ -549,12 +555,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
             }
             for (; w.at < w.seg_end; ++w.at, ++k) {
                 const int st = k % NS, pos0 = (w.at - page0) * kPT;
-                ok = wait_or_abort_warp(lead, bar(SM::B_S + (k & 1)), (k >> 1) & 1, abort_flag);
-                // P's tile of two pages ago has been read
-                if (ok && k >= 2) ok = wait_or_abort_warp(lead, bar(SM::B_O + (k & 1)), ((k - 2) >> 1) & 1, abort_flag);
-                if (ok) ok = wait_or_abort_warp(lead, full(st, 0), (k / NS) & 1, abort_flag);  // page_ok
-                ok = !bar_softmax_or(!ok);
-                if (!ok) break;
+                // the scores (their completion implies the earlier products', so P's tile of two
+                // pages ago has been read) and, for page_ok, the page
+                ok = wait_or_abort_warp(lane < 2, lane ? full(st, 0) : bar(SM::B_S + (k & 1)),
+                                        (lane ? k / NS : k >> 1) & 1, abort_flag);
                 tc_fence_after();
                 float s[16];  // [j][e]: column 8j + c0 + e % 2, key 16 warp + lane / 4 + 8 (e / 2)
                 {
@@ -581,7 +585,9 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) grew |= s[4 * j + e] > base[2 * j + (e & 1)] + kLazy;
-                if (bar_softmax_or(grew)) {
+                if (bar_softmax_or(grew || !ok)) {
+                    ok = !bar_softmax_or(!ok);
+                    if (!ok) break;
                     // some row outgrew its base: every row's new base is the maximum so far
                     float mx[8];
 #pragma unroll
@@ -761,14 +767,13 @@ __global__ void __launch_bounds__(kExpThreads) latent_expand_kernel(const Latent
     const __nv_bfloat16 *wv = p.w_uv + h * p.w_uv_head + cc * 128;
     for (int idx = tid; idx < D * 16; idx += kExpThreads) {
         const int v = idx >> 4, c = (idx & 15) * 8;
-        *reinterpret_cast<uint4 *>(&sm.w[v][c]) =
-            *reinterpret_cast<const uint4 *>(wv + (size_t)v * p.dc + c);
+        cp_async16(smem_u32(&sm.w[v][c]), wv + (size_t)v * p.dc + c);  // lands during the merge
     }
     // merge the ranges: `wpr` warps share a token's ranges, lanes its 128 dims (4 each)
     const int P = p.cum[p.B], n_live = min(p.n_ranges, P);
     const int wpr = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8;
     uint32_t missing = 0;  // tokens of which a range gave up
-    for (int r0 = 0; r0 < kExpTok; r0 += 8 / wpr) {
+    for (int r0 = 0; r0 < rows; r0 += 8 / wpr) {
         const int r = r0 + warp / wpr, part = warp % wpr;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float M = -INFINITY, den = 0.f;
@@ -789,7 +794,7 @@ __global__ void __launch_bounds__(kExpThreads) latent_expand_kernel(const Latent
             for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
             lost = __any_sync(0xffffffffu, lost);
             if (!lost && M != -INFINITY) {
-#pragma unroll 4
+#pragma unroll 8
                 for (int i = i0 + part; i < i1; i += wpr) {
                     const size_t at = part_index(p, i, b, g) * kRows + c;
                     const float2 v = *reinterpret_cast<const float2 *>(p.part_ml + at * 2);
@@ -812,7 +817,7 @@ __global__ void __launch_bounds__(kExpThreads) latent_expand_kernel(const Latent
                 }
             __syncthreads();
         }
-        if (part == 0) {
+        if (part == 0 && r < rows) {
             const float inv = den > 0.f ? 1.f / den : 0.f;
             const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
             const uint32_t h0 = pack_bf16x2(x[0], x[1]), h1 = pack_bf16x2(x[2], x[3]);
@@ -821,11 +826,16 @@ __global__ void __launch_bounds__(kExpThreads) latent_expand_kernel(const Latent
                 make_uint2(pack_bf16x2(x[0] - bf16_lo(h0), x[1] - bf16_hi(h0)),
                            pack_bf16x2(x[2] - bf16_lo(h1), x[3] - bf16_hi(h1)));
         }
-        if (r < kExpTok && lost) missing |= 1u << r;
+        if (r < rows && lost) missing |= 1u << r;
+    }
+    for (int r = rows + warp; r < kExpTok; r += 8) {  // rows without a token
+        *reinterpret_cast<uint2 *>(&sm.hi[r][lane * 4]) = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2 *>(&sm.lo[r][lane * 4]) = make_uint2(0u, 0u);
     }
     // a warp knows the losses of the tokens it merged; the output needs all of them
     __shared__ uint32_t s_missing;
     if (tid == 0) s_missing = 0;
+    cp_async_wait_all();
     __syncthreads();
     if (lane == 0 && missing) atomicOr(&s_missing, missing);
     // out[16 tokens][D] = latent output x W_uv^T over this CTA's dims; a warp takes D / 8 columns
@@ -857,11 +867,14 @@ __global__ void __launch_bounds__(kExpThreads) latent_expand_kernel(const Latent
     for (int idx = (int)me * kExpThreads + tid; idx < rows * (D / 2); idx += n_cols * kExpThreads) {
         const int r = idx / (D / 2), v = idx % (D / 2) * 2;
         if ((s_missing >> r) & 1u) continue;  // o stays as it was
-        float x0 = 0.f, x1 = 0.f;
-        for (int c = 0; c < n_cols; ++c) {
-            x0 += ld_cluster_f32(smem_u32(&sm.out[r][v]), c);
-            x1 += ld_cluster_f32(smem_u32(&sm.out[r][v + 1]), c);
+        float y[4][2];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            y[c][0] = c < n_cols ? ld_cluster_f32(smem_u32(&sm.out[r][v]), c) : 0.f;
+            y[c][1] = c < n_cols ? ld_cluster_f32(smem_u32(&sm.out[r][v + 1]), c) : 0.f;
         }
+        const float x0 = ((y[0][0] + y[1][0]) + y[2][0]) + y[3][0];
+        const float x1 = ((y[0][1] + y[1][1]) + y[2][1]) + y[3][1];
         *reinterpret_cast<uint32_t *>(p.o + ((size_t)(tok0 + r) * p.H + h) * D + v) = pack_bf16x2(x0, x1);
     }
     cluster_sync_all();  // nobody leaves while its part is still read
@@ -917,7 +930,8 @@ cudaError_t launch_absorb(const LatentParams &p, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
     const int blocks = (p.B * p.nq + kAbsTok - 1) / kAbsTok;
-    return launch_pdl(latent_absorb_kernel<D>, dim3((unsigned)(p.dc / 128 * p.H * blocks + 1)),
+    const int n_app = (p.B * p.nq + kAbsThreads / 32 - 1) / (kAbsThreads / 32);
+    return launch_pdl(latent_absorb_kernel<D>, dim3((unsigned)(p.dc / 128 * p.H * blocks + n_app + 1)),
                       dim3(kAbsThreads), sizeof(AbsSmem<D>), s, p);
 }
 

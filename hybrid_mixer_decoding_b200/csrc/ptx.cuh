@@ -101,6 +101,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
+// 16 bytes global -> shared without passing through registers; completed by cp_async_wait_all.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Programmatic dependent launch. griddep_wait: block until the grids this launch depends on
 // have completed and their writes are visible (a no-op for a launch without such a dependency);
 // every kernel calls it before its first global-memory access. griddep_launch_dependents: allow

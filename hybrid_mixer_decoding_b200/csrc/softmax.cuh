@@ -135,13 +135,14 @@ __device__ __forceinline__ bool mbar_test_if(bool asks, uint32_t bar, uint32_t p
         : "memory");
     return ok != 0;
 }
-// The same for a whole converged warp, asked by its lane with `lead`.
+// The same for a whole converged warp, asked by its lane or lanes with `lead`, of which each may
+// name a barrier of its own: all of them have to be complete.
 __device__ __forceinline__ bool mbar_test_warp(bool lead, uint32_t bar, uint32_t parity) {
-    const bool ok = __any_sync(0xffffffffu, mbar_test_if(lead, bar, parity));
+    const bool ok = __all_sync(0xffffffffu, mbar_test_if(lead, bar, parity) || !lead);
     __syncwarp();  // what the asking lane has seen is seen by all: a vote alone orders nothing
     return ok;
 }
-// wait_or_abort for a whole converged warp: one lane waits. (128 threads that spin on a barrier keep
+// wait_or_abort for a whole converged warp: the lanes with `lead` ask. (128 threads that spin on a barrier keep
 // the shared-memory pipe busy and slow down the warp that issues the products.)
 __device__ __forceinline__ bool wait_or_abort_warp(bool lead, uint32_t bar, uint32_t parity,
                                                    volatile int *abort) {
