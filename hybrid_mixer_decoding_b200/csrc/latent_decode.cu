@@ -557,7 +557,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
                 const int st = k % NS, pos0 = (w.at - page0) * kPT;
                 // the scores (their completion implies the earlier products', so P's tile of two
                 // pages ago has been read) and, for page_ok, the page
-                ok = wait_or_abort_warp(lane < 2, lane ? full(st, 0) : bar(SM::B_S + (k & 1)),
+                ok = wait_warp(lane < 2, lane ? full(st, 0) : bar(SM::B_S + (k & 1)),
                                         (lane ? k / NS : k >> 1) & 1, abort_flag);
                 tc_fence_after();
                 float s[16];  // [j][e]: column 8j + c0 + e % 2, key 16 warp + lane / 4 + 8 (e / 2)
@@ -615,7 +615,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
 #pragma unroll
                             for (int j = 0; j < 8; ++j) s_red[0][(j >> 1) * 8 + c0 + (j & 1)] = f[j];
                         bar_softmax();
-                        ok = wait_or_abort_warp(lead, bar(SM::B_O + ((k - 1) & 1)), ((k - 1) >> 1) & 1, abort_flag);
+                        ok = wait_warp(lead, bar(SM::B_O + ((k - 1) & 1)), ((k - 1) >> 1) & 1, abort_flag);
                         ok = !bar_softmax_or(!ok);
                         if (!ok) break;
                         tc_fence_after();
@@ -672,7 +672,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
             }
             const size_t piece = part_index(p, range, b, group);
             float *ml = p.part_ml + piece * kRows * 2;
-            if (ok) ok = wait_or_abort_warp(lead, bar(SM::B_O + ((k - 1) & 1)), ((k - 1) >> 1) & 1, abort_flag);
+            if (ok) ok = wait_warp(lead, bar(SM::B_O + ((k - 1) & 1)), ((k - 1) >> 1) & 1, abort_flag);
             ok = !bar_softmax_or(!ok);
             if (!ok) {
                 // this piece and the range's later ones are marked as missing

@@ -225,17 +225,14 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         const Desc d_a(smem_desc_sw128(sb + SM::OFF_A, 16, 1024));
         const Desc d_w(smem_desc_sw128(sb + SM::OFF_W, 16, 1024));
         constexpr uint32_t ID = idesc_bf16(128, 2 * D, 0, 0);
-        auto wait = [&](int i, uint32_t parity) {
-            return wait_or_abort_warp(lead, bar(i), parity, abort_flag);
-        };
-        bool ok = wait(SM::B_A, 0);
+        auto wait = [&](int i, uint32_t parity) { wait_warp(lead, bar(i), parity, abort_flag); };
+        wait(SM::B_A, 0);
         int n = 0;
-        for (int st = 0; st < n_steps && ok; ++st) {
-            if (st >= 2) ok = wait(SM::B_READ + (st & 1), ((st >> 1) - 1) & 1);
-            for (int kc = 0; kc < n_kc && ok; ++kc, ++n) {
+        for (int st = 0; st < n_steps; ++st) {
+            if (st >= 2) wait(SM::B_READ + (st & 1), ((st >> 1) - 1) & 1);
+            for (int kc = 0; kc < n_kc; ++kc, ++n) {
                 const int w = n % SM::NW;
-                ok = wait(SM::B_WFULL + w, (n / SM::NW) & 1);
-                if (!ok) break;
+                wait(SM::B_WFULL + w, (n / SM::NW) & 1);
                 tc_fence_after();
                 const Desc a = d_a.at(kc * kBlk), wd = d_w.at(w * SM::W_STAGE);
 #pragma unroll
@@ -247,7 +244,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
             }
         }
         if (lead) {
-            if (!ok) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+            if (*abort_flag) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
             umma_commit(bar(SM::B_END));  // every product is done before TMEM goes (bounded)
             (void)mbar_wait_bounded(bar(SM::B_END), 0);
         }
@@ -259,10 +256,8 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         const bool lead = elect_one();
         bool out = false;
         for (int st = 0; st < n_steps; ++st) {
-            if (!wait_or_abort_warp(lead, bar(SM::B_ACC + (st & 1)), (st >> 1) & 1, abort_flag)) {
-                if (lane == 0) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
-                break;
-            }
+            wait_warp(lead, bar(SM::B_ACC + (st & 1)), (st >> 1) & 1, abort_flag);
+            if (*abort_flag) break;  // reported by the products' warp; the whole warp leaves below
             tc_fence_after();
             const size_t row = (((size_t)b * p.heads + ha + st) * p.s_pad + pos) * D;
 #pragma unroll 1
@@ -340,8 +335,10 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SM::OFF_BAR + 8 * SM::N_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + SM::OFF_BAR + 8 * SM::N_BARS + 4);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+    // longest query blocks of all heads first (a wave of CTAs on a few heads' blocks of all lengths,
+    // which keeps their keys in L2, ended 8% later)
     const int bh = blockIdx.x % (p.B * p.heads);
-    const int qb = p.n_qb - 1 - (int)(blockIdx.x / (p.B * p.heads));  // longest blocks first
+    const int qb = p.n_qb - 1 - (int)(blockIdx.x / (p.B * p.heads));
     const int b = bh / p.heads, hl = bh - b * p.heads, h = p.h0 + hl;
     griddep_launch_dependents();
     griddep_wait();
@@ -428,13 +425,14 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         const Desc d_v(smem_desc_sw128(sb + SM::OFF_R, kBlk, 1024));
         constexpr uint32_t ID_S = idesc_f16(128, kTile, 0, 0);
         constexpr uint32_t ID_O = idesc_f16(128, D, 0, 1), ID_O64 = idesc_f16(128, 64, 0, 1);
-        auto wait = [&](int i, uint32_t parity) {
-            return wait_or_abort_warp(lead, bar(i), parity, abort_flag);
-        };
-        auto wait_blocks = [&](int n, int count) {
-            bool ok = true;
-            for (int u = n; u < n + count && ok; ++u) ok = wait(SM::B_FULL + u % NR, (u / NR) & 1);
-            return ok;
+        // lanes 0 .. count - 1 wait for blocks n .. n + count - 1, lane `count` for P of query tile j
+        // (j < 0: for blocks only)
+        auto wait_for = [&](int n, int count, int j, int i) {
+            const int u = n + lane;
+            const bool block = lane < count;
+            wait_warp(block || (lane == count && j >= 0), block ? bar(SM::B_FULL + u % NR) : bar(SM::B_P + j),
+                      (block ? u / NR : i) & 1, abort_flag);
+            tc_fence_after();
         };
         auto free_blocks = [&](int n, int count) {
             for (int u = n; u < n + count; ++u) umma_commit_if(lead, bar(SM::B_FREE + u % NR));
@@ -469,35 +467,27 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                     umma_ts_if(lead, o + 64, pj + 8 * kk, d_v.at(kk * 2048), ID_O64, kk > 0 ? 1u : more);
             }
         };
-        bool ok = wait_blocks(0, KB);
-        if (ok) {
-            tc_fence_after();
-            issue_s(0, 0);
-            if (nt1 > 0) issue_s(1, 0);
-            free_blocks(0, KB);
-        }
-        for (int i = 0; i < n_tiles && ok; ++i) {
+        wait_for(0, KB, -1, 0);
+        issue_s(0, 0);
+        if (nt1 > 0) issue_s(1, 0);
+        free_blocks(0, KB);
+        for (int i = 0; i < n_tiles; ++i) {
 #pragma unroll 1
-            for (int j = 0; j < 2 && ok; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const int nt = j ? nt1 : nt0;
-                if (j == 0) ok = wait_blocks(i * NB + KB, VB);
-                if (ok && i < nt) ok = wait(SM::B_P + j, i & 1);
-                if (!ok) break;
-                tc_fence_after();
+                if (j == 0 || i < nt) wait_for(i * NB + KB, j == 0 ? VB : 0, i < nt ? j : -1, i);
                 if (i < nt) issue_o(j, i);
                 if (i == nt - 1) umma_commit_if(lead, bar(SM::B_O + j));
                 if (j == 1) free_blocks(i * NB + KB, VB);
                 if (i + 1 < n_tiles) {
-                    if (j == 0) ok = wait_blocks((i + 1) * NB, KB);
-                    if (!ok) break;
-                    tc_fence_after();
+                    if (j == 0) wait_for((i + 1) * NB, KB, -1, 0);
                     if (i + 1 < nt) issue_s(j, i + 1);
                     if (j == 1) free_blocks((i + 1) * NB, KB);
                 }
             }
         }
         if (lead) {
-            if (!ok) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+            if (*abort_flag) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
             umma_commit(bar(SM::B_END));  // every product is done before TMEM goes (bounded)
             (void)mbar_wait_bounded(bar(SM::B_END), 0);
         }
@@ -509,10 +499,8 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         const uint32_t s_col = lane_base + 256 * qt, o_col = s_col + 128;
         const bool lead = elect_one();
         float m_base = -INFINITY, l_run = 0.f;
-        bool ok = true;
-        for (int i = 0; i < nt && ok; ++i) {
-            ok = wait_or_abort_warp(lead, bar(SM::B_S + qt), i & 1, abort_flag);
-            if (!ok) break;
+        for (int i = 0; i < nt; ++i) {
+            wait_warp(lead, bar(SM::B_S + qt), i & 1, abort_flag);
             tc_fence_after();
             float x[kTile];
             {
@@ -596,7 +584,8 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(SM::B_P + qt));
         }
-        if (ok) ok = wait_or_abort_warp(lead, bar(SM::B_O + qt), 0, abort_flag);
+        wait_warp(lead, bar(SM::B_O + qt), 0, abort_flag);
+        const bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
         if (ok) {
             tc_fence_after();
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;

@@ -142,20 +142,20 @@ __device__ __forceinline__ bool mbar_test_warp(bool lead, uint32_t bar, uint32_t
     __syncwarp();  // what the asking lane has seen is seen by all: a vote alone orders nothing
     return ok;
 }
-// wait_or_abort for a whole converged warp: the lanes with `lead` ask. (128 threads that spin on a barrier keep
-// the shared-memory pipe busy and slow down the warp that issues the products.)
-__device__ __forceinline__ bool wait_or_abort_warp(bool lead, uint32_t bar, uint32_t parity,
-                                                   volatile int *abort) {
-    bool done = mbar_test_warp(lead, bar, parity);
-    if (!done) {
-        const unsigned long long t0 = globaltimer_ns();
-        while (!(done = mbar_test_warp(lead, bar, parity))) {
-            const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
-            if (late) *abort = 1;
-            if (__any_sync(0xffffffffu, late || *abort)) break;
-        }
+// wait_or_abort for a whole converged warp: the lanes with `asks` ask, each for a barrier of its own.
+// The warp stays converged (it asks and votes in turn): a lane that waits in a branch of its own
+// leaves the others free to reach the next product before it. A wait that gave up shows in `abort`
+// too; a caller that goes on (over what memory holds, with waits that return at once) looks at the
+// flag before it writes results.
+__device__ __forceinline__ bool wait_warp(bool asks, uint32_t bar, uint32_t parity, volatile int *abort) {
+    if (mbar_test_warp(asks, bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    while (true) {
+        if (mbar_test_warp(asks, bar, parity)) return true;
+        const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+        if (late) *abort = 1;
+        if (__any_sync(0xffffffffu, late || *abort)) return false;
     }
-    return done;
 }
 __device__ __forceinline__ void umma_commit_if(bool lead, uint32_t bar) {
     asm volatile(
