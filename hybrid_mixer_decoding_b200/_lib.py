@@ -159,24 +159,37 @@ def _contig(*ts):
             raise ValueError("tensors must be contiguous")
 
 
-def _expect(dtype, **tensors) -> None:
-    """Every given tensor is a contiguous one of `dtype` on the current device."""
-    tensors = {name: t for name, t in tensors.items() if t is not None}
-    for name, t in tensors.items():
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    for name, t in tensors.items():
-        if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} must be on the current CUDA device, not {t.device}")
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
 
 
-def _shape(t, *want, name) -> None:
-    """t has the wanted sizes (None: any)."""
-    if t is not None and (t.dim() != len(want) or
-                          any(w is not None and w != n for w, n in zip(want, t.shape))):
-        raise ValueError(f"{name} must have shape {want}, not {tuple(t.shape)}")
+def _demand(dev, *specs) -> None:
+    """Every given tensor, as (name, tensor or None, dtype, shape), is a contiguous one of that type
+    and shape on device `dev` (the current one). A small call is short: the checks that pass
+    do nothing else."""
+    away = None
+    for name, t, dtype, shape in specs:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or
+                              not t.is_contiguous() or t.get_device() != dev or dev < 0):
+            if t.dtype is not dtype:
+                raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+            away = away or f"{name} must be on the current CUDA device, not {t.device}"
+    if away:
+        raise ValueError(away)
+
+
+def _dims(t, n, name):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, not {t.dim()}")
+    return t.shape
+
+
+def _raw_stream(dev, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def delta_rule_decode(kind, q, k, v, beta, log_gate, state, o, slots=None, scale=1.0,
@@ -341,26 +354,23 @@ def attn_verify_scored(q, new_k, new_v, k_pool, v_pool, weights, page_table, seq
     """attn_verify over an FA cache that also adds every key's softmax weight to weights
     [n_slots,Hkv,w_len] fp32 (see include/hmd.h); n_q = 1 is the decode step. q,o [B,n_q,Hq,d];
     new_k,new_v [B,n_q,Hkv,d]; slots int32 [B] or None (row b)."""
-    _expect(torch.bfloat16, q=q, new_k=new_k, new_v=new_v, k_pool=k_pool, v_pool=v_pool, o=o)
-    _expect(torch.float32, weights=weights)
-    _expect(torch.int32, page_table=page_table, seq_lens=seq_lens, slots=slots)
-    _expect(workspace.dtype, workspace=workspace)
-    B, n_q, Hq, d = q.shape
-    n_pages, Hkv, PT, _ = k_pool.shape
-    _shape(o, B, n_q, Hq, d, name="o")
-    for name, t in (("new_k", new_k), ("new_v", new_v)):
-        _shape(t, B, n_q, Hkv, d, name=name)
-    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-        _shape(t, n_pages, Hkv, PT, d, name=name)
-    _shape(weights, None, Hkv, None, name="weights")
-    _shape(page_table, B, None, name="page_table")
-    _shape(seq_lens, B, name="seq_lens")
-    _shape(slots, B, name="slots")
-    st = lib().attn_verify_scored(n_q, B, Hq, Hkv, d, PT, _p(q), _p(new_k), _p(new_v), _p(k_pool),
-                                  _p(v_pool), n_pages, _p(page_table), page_table.shape[1],
-                                  _p(seq_lens), int(max_seq_len), _p(weights), weights.shape[2],
-                                  weights.shape[0], _p(slots), _p(o), _p(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream(stream))
+    B, n_q, Hq, d = _dims(q, 4, "q")
+    n_pages, Hkv, PT, _ = _dims(k_pool, 4, "k_pool")
+    n_slots, _, w_len = _dims(weights, 3, "weights")
+    max_pages = _dims(page_table, 2, "page_table")[1]
+    new, pool, dev, bf = (B, n_q, Hkv, d), (n_pages, Hkv, PT, d), _device(), torch.bfloat16
+    _demand(dev, ("q", q, bf, (B, n_q, Hq, d)), ("o", o, bf, (B, n_q, Hq, d)),
+            ("k_pool", k_pool, bf, pool), ("v_pool", v_pool, bf, pool), ("new_k", new_k, bf, new),
+            ("new_v", new_v, bf, new), ("weights", weights, torch.float32, (n_slots, Hkv, w_len)),
+            ("page_table", page_table, torch.int32, (B, max_pages)),
+            ("seq_lens", seq_lens, torch.int32, (B,)), ("slots", slots, torch.int32, (B,)),
+            ("workspace", workspace, workspace.dtype, workspace.shape))
+    st = lib().attn_verify_scored(n_q, B, Hq, Hkv, d, PT, q.data_ptr(), new_k.data_ptr(),
+                                  new_v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), n_pages,
+                                  page_table.data_ptr(), max_pages, seq_lens.data_ptr(),
+                                  int(max_seq_len), weights.data_ptr(), w_len, n_slots, _p(slots),
+                                  o.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                  _raw_stream(dev, stream))
     _check("attn_verify_scored", st)
 
 
@@ -371,25 +381,25 @@ def kv_cache_evict(budget, recent, k_pool, v_pool, page_table, seq_lens, max_seq
     [n_pages,Hkv,64,d] bf16; weights, weights_out [n_slots,Hkv,*] fp32; kept int32
     [B,Hkv,budget]; new_lens int32 [B]. dst_table may be page_table, weights_out weights and
     new_lens seq_lens (in place)."""
-    _expect(torch.bfloat16, k_pool=k_pool, v_pool=v_pool)
-    _expect(torch.float32, weights=weights, weights_out=weights_out)
-    _expect(torch.int32, page_table=page_table, seq_lens=seq_lens, dst_table=dst_table, kept=kept,
-            new_lens=new_lens, slots=slots)
-    n_pages, Hkv, PT, d = k_pool.shape
-    B = seq_lens.shape[0]
-    _shape(v_pool, n_pages, Hkv, PT, d, name="v_pool")
-    _shape(page_table, B, None, name="page_table")
-    _shape(dst_table, B, None, name="dst_table")
-    _shape(weights, None, Hkv, None, name="weights")
-    _shape(weights_out, weights.shape[0], Hkv, None, name="weights_out")
-    _shape(kept, B, Hkv, int(budget), name="kept")
-    _shape(new_lens, B, name="new_lens")
-    _shape(slots, B, name="slots")
-    st = lib().kv_cache_evict(int(budget), int(recent), B, Hkv, d, PT, _p(k_pool), _p(v_pool),
-                              n_pages, _p(page_table), page_table.shape[1], _p(seq_lens),
-                              int(max_seq_len), _p(weights), weights.shape[2], weights.shape[0],
-                              _p(slots), _p(dst_table), dst_table.shape[1], _p(weights_out),
-                              weights_out.shape[2], _p(kept), _p(new_lens), _stream(stream))
+    n_pages, Hkv, PT, d = _dims(k_pool, 4, "k_pool")
+    n_slots, _, w_len = _dims(weights, 3, "weights")
+    w_out_len = _dims(weights_out, 3, "weights_out")[2]
+    (B,), budget = _dims(seq_lens, 1, "seq_lens"), int(budget)
+    max_pages, dst_pages = _dims(page_table, 2, "page_table")[1], _dims(dst_table, 2, "dst_table")[1]
+    pool, dev, i32 = (n_pages, Hkv, PT, d), _device(), torch.int32
+    _demand(dev, ("k_pool", k_pool, torch.bfloat16, pool), ("v_pool", v_pool, torch.bfloat16, pool),
+            ("page_table", page_table, i32, (B, max_pages)), ("seq_lens", seq_lens, i32, (B,)),
+            ("weights", weights, torch.float32, (n_slots, Hkv, w_len)),
+            ("dst_table", dst_table, i32, (B, dst_pages)),
+            ("weights_out", weights_out, torch.float32, (n_slots, Hkv, w_out_len)),
+            ("kept", kept, i32, (B, Hkv, budget)), ("new_lens", new_lens, i32, (B,)),
+            ("slots", slots, i32, (B,)))
+    st = lib().kv_cache_evict(budget, int(recent), B, Hkv, d, PT, k_pool.data_ptr(),
+                              v_pool.data_ptr(), n_pages, page_table.data_ptr(), max_pages,
+                              seq_lens.data_ptr(), int(max_seq_len), weights.data_ptr(), w_len,
+                              n_slots, _p(slots), dst_table.data_ptr(), dst_pages,
+                              weights_out.data_ptr(), w_out_len, kept.data_ptr(),
+                              new_lens.data_ptr(), _raw_stream(dev, stream))
     _check("kv_cache_evict", st)
 
 
@@ -398,17 +408,21 @@ def attn_latent_decode_workspace_size(n_q, B, H, d, d_c, d_r, page_tokens, max_s
                                                        max_seq_len))
 
 
-def _latent_weights(H, d, d_c, w_uk, w_uv):
-    """Elements between heads of w_uk and w_uv [H,d,d_c]: each head's block is dense, the heads
-    may be further apart (slices of one [H,2d,d_c] projection)."""
-    for name, w in (("w_uk", w_uk), ("w_uv", w_uv)):
-        _shape(w, H, d, d_c, name=name)
-        if w.stride()[1:] != (d_c, 1):
-            raise ValueError(f"{name}: every head's [d,d_c] block must be contiguous")
-        if H > 1 and w.stride(0) < d * d_c:
-            raise ValueError(f"{name}: the heads' blocks must not overlap")
-        _expect(torch.bfloat16, **{name: w[0]})
-    return tuple(w.stride(0) if H > 1 else d * d_c for w in (w_uk, w_uv))
+def _head_stride(dev, name, w, H, d, d_c) -> int:
+    """Elements between the heads of w [H,d,d_c]: each head's block is dense, the heads may be further
+    apart (a slice of one [H,2d,d_c] projection)."""
+    if w.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, not {w.dtype}")
+    if w.shape != (H, d, d_c):
+        raise ValueError(f"{name} must have shape {(H, d, d_c)}, not {tuple(w.shape)}")
+    head, row, col = w.stride()
+    if row != d_c or col != 1:
+        raise ValueError(f"{name}: every head's [d,d_c] block must be contiguous")
+    if H > 1 and head < d * d_c:
+        raise ValueError(f"{name}: the heads' blocks must not overlap")
+    if w.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be on the current CUDA device, not {w.device}")
+    return head if H > 1 else d * d_c
 
 
 def attn_latent_decode(q, new_c, w_uk, w_uv, pool, page_table, seq_lens, max_seq_len, o, workspace,
@@ -416,24 +430,25 @@ def attn_latent_decode(q, new_c, w_uk, w_uv, pool, page_table, seq_lens, max_seq
     """Latent attention of n_q new tokens per sequence against the paged latent cache, absorbed
     form (see include/hmd.h). q [B,n_q,H,d+64]; new_c [B,n_q,d_c+64]; w_uk,w_uv [H,d,d_c]; pool
     [n_pages,64,d_c+64]; o [B,n_q,H,d]; scale None: 1 / sqrt(d + 64)."""
-    _expect(torch.bfloat16, q=q, new_c=new_c, pool=pool, o=o)
-    _expect(torch.int32, page_table=page_table, seq_lens=seq_lens)
-    _expect(workspace.dtype, workspace=workspace)
-    B, n_q, H, dq = q.shape
-    d, (n_pages, PT, row) = o.shape[-1], pool.shape
+    B, n_q, H, dq = _dims(q, 4, "q")
+    n_pages, PT, row = _dims(pool, 3, "pool")
+    d, max_pages = _dims(o, 4, "o")[3], _dims(page_table, 2, "page_table")[1]
     d_r = dq - d
     d_c = row - d_r
-    _shape(o, B, n_q, H, d, name="o")
-    _shape(new_c, B, n_q, row, name="new_c")
-    _shape(page_table, B, None, name="page_table")
-    _shape(seq_lens, B, name="seq_lens")
-    uk, uv = _latent_weights(H, d, d_c, w_uk, w_uv)
+    dev, bf = _device(), torch.bfloat16
+    _demand(dev, ("q", q, bf, (B, n_q, H, dq)), ("o", o, bf, (B, n_q, H, d)),
+            ("new_c", new_c, bf, (B, n_q, row)), ("pool", pool, bf, (n_pages, PT, row)),
+            ("page_table", page_table, torch.int32, (B, max_pages)),
+            ("seq_lens", seq_lens, torch.int32, (B,)),
+            ("workspace", workspace, workspace.dtype, workspace.shape))
     st = lib().attn_latent_decode(n_q, B, H, d, d_c, d_r, PT,
-                                  dq ** -0.5 if scale is None else float(scale), _p(q), _p(new_c),
-                                  _p(w_uk), uk, _p(w_uv), uv, _p(pool), n_pages, _p(page_table),
-                                  page_table.shape[1], _p(seq_lens), int(max_seq_len), _p(o),
-                                  _p(workspace), workspace.numel() * workspace.element_size(),
-                                  _stream(stream))
+                                  dq ** -0.5 if scale is None else float(scale), q.data_ptr(),
+                                  new_c.data_ptr(), w_uk.data_ptr(),
+                                  _head_stride(dev, "w_uk", w_uk, H, d, d_c), w_uv.data_ptr(),
+                                  _head_stride(dev, "w_uv", w_uv, H, d, d_c), pool.data_ptr(),
+                                  n_pages, page_table.data_ptr(), max_pages, seq_lens.data_ptr(),
+                                  int(max_seq_len), o.data_ptr(), workspace.data_ptr(),
+                                  workspace.nbytes, _raw_stream(dev, stream))
     _check("attn_latent_decode", st)
 
 
@@ -448,25 +463,26 @@ def attn_latent_prefill(q, c, w_uk, w_uv, pool, page_table, o, workspace, prefix
     include/hmd.h). q [B,T,H,d+64]; c [B,T,d_c+64]; w_uk,w_uv [H,d,d_c]; pool
     [n_pages,64,d_c+64]; o [B,T,H,d]; prefix_lens, prompt_lens int32 [B] or None; scale None:
     1 / sqrt(d + 64)."""
-    _expect(torch.bfloat16, q=q, c=c, pool=pool, o=o)
-    _expect(torch.int32, page_table=page_table, prefix_lens=prefix_lens, prompt_lens=prompt_lens)
-    _expect(workspace.dtype, workspace=workspace)
-    B, T, H, dq = q.shape
-    d, (n_pages, PT, row) = o.shape[-1], pool.shape
+    B, T, H, dq = _dims(q, 4, "q")
+    n_pages, PT, row = _dims(pool, 3, "pool")
+    d, max_pages = _dims(o, 4, "o")[3], _dims(page_table, 2, "page_table")[1]
     d_r = dq - d
     d_c = row - d_r
-    _shape(o, B, T, H, d, name="o")
-    _shape(c, B, T, row, name="c")
-    _shape(page_table, B, None, name="page_table")
-    _shape(prefix_lens, B, name="prefix_lens")
-    _shape(prompt_lens, B, name="prompt_lens")
-    uk, uv = _latent_weights(H, d, d_c, w_uk, w_uv)
+    dev, bf = _device(), torch.bfloat16
+    _demand(dev, ("q", q, bf, (B, T, H, dq)), ("o", o, bf, (B, T, H, d)), ("c", c, bf, (B, T, row)),
+            ("pool", pool, bf, (n_pages, PT, row)),
+            ("page_table", page_table, torch.int32, (B, max_pages)),
+            ("prefix_lens", prefix_lens, torch.int32, (B,)),
+            ("prompt_lens", prompt_lens, torch.int32, (B,)),
+            ("workspace", workspace, workspace.dtype, workspace.shape))
     st = lib().attn_latent_prefill(B, T, H, d, d_c, d_r, PT,
-                                   dq ** -0.5 if scale is None else float(scale), _p(q), _p(c),
-                                   _p(w_uk), uk, _p(w_uv), uv, _p(prefix_lens), int(max_prefix),
-                                   _p(prompt_lens), _p(pool), n_pages, _p(page_table),
-                                   page_table.shape[1], _p(o), _p(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(stream))
+                                   dq ** -0.5 if scale is None else float(scale), q.data_ptr(),
+                                   c.data_ptr(), w_uk.data_ptr(),
+                                   _head_stride(dev, "w_uk", w_uk, H, d, d_c), w_uv.data_ptr(),
+                                   _head_stride(dev, "w_uv", w_uv, H, d, d_c), _p(prefix_lens),
+                                   int(max_prefix), _p(prompt_lens), pool.data_ptr(), n_pages,
+                                   page_table.data_ptr(), max_pages, o.data_ptr(),
+                                   workspace.data_ptr(), workspace.nbytes, _raw_stream(dev, stream))
     _check("attn_latent_prefill", st)
 
 

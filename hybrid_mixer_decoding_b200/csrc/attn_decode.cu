@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(D) attn_combine_kernel(const float *ws_ml, con
 
 // Kernel 2 of the scored form: one launch, two kinds of blocks of 128 threads. The first
 // n_row_blocks merge the splits of 128 / D query rows into o, as attn_combine_kernel does; the
-// others each take one (sequence, kv-head) and kScoreKeys keys: with M_r and l_r the maximum and
+// others each take one (sequence, kv-head) and kScoreKeys keys, four per thread: with M_r and l_r the maximum and
 // sum over all splits, key j received sum_r 2^(s_rj - M_r) / l_r from the group's rows, which is
 // added to its accumulated weight (a new token's slot starts from 0). Every key has one thread
 // and its rows are added in order, so results do not depend on scheduling. A sequence whose
@@ -557,15 +557,47 @@ __global__ void __launch_bounds__(128) attn_combine_scored_kernel(const ScorePar
     }
     __syncthreads();
     if (s_missing) return;
-    const float *sc = p.ws_s + (size_t)bg * R * p.s_len;
-    float *w = p.weights + ((size_t)slot * p.Hkv + g) * p.w_len;
+    // four keys per thread, four rows' loads in flight before their sums
+    const int j0 = chunk * kScoreKeys + tid * 4;
+    if (j0 >= L) return;
+    const float *sc = p.ws_s + (size_t)bg * R * p.s_len + j0;
+    float *w = p.weights + ((size_t)slot * p.Hkv + g) * p.w_len + j0;
+    const int n_old = L - p.nq - j0, n = min(4, L - j0);  // of the four: old keys, keys
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool whole = n_old >= 4 && (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
+    if (whole) {
+        const float4 v = *reinterpret_cast<const float4 *>(w);
+        a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
+    } else {
 #pragma unroll
-    for (int u = 0; u < kScoreKeys / 128; ++u) {
-        const int j = chunk * kScoreKeys + u * 128 + tid;
-        if (j >= L) break;
-        float a = 0.f;
-        for (int r = 0; r < R; ++r) a += exp2f(sc[(size_t)r * p.s_len + j] - s_max[r]) * s_inv[r];
-        w[j] = j < L - p.nq ? w[j] + a : a;
+        for (int e = 0; e < 4; ++e)
+            if (e < n_old) a[e] = w[e];
+    }
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r0 = 0; r0 < R; r0 += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (r0 + u < R) x[u] = __ldcs(reinterpret_cast<const float4 *>(sc + (size_t)(r0 + u) * p.s_len));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (r0 + u < R) {
+                const float m = s_max[r0 + u], inv = s_inv[r0 + u];
+                sum[0] += exp2f(x[u].x - m) * inv;
+                sum[1] += exp2f(x[u].y - m) * inv;
+                sum[2] += exp2f(x[u].z - m) * inv;
+                sum[3] += exp2f(x[u].w - m) * inv;
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] += sum[e];
+    if (whole) {
+        *reinterpret_cast<float4 *>(w) = make_float4(a[0], a[1], a[2], a[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) w[e] = a[e];
     }
 }
 
@@ -602,6 +634,16 @@ bool make_pool_map(CUtensorMap *m, void *pool, int n_pages, int Hkv, int d) {
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
+}
+
+// Most pages of a key range of the scored form. One wave of ranges as long as the longest sequence
+// leaves SMs idle once the shorter sequences of a batch are done; shorter ranges are dealt out as
+// SMs come free. B = 32, Hkv = 8, sequences of 4096 to 8192: 171 us with whole sequences, 148 to
+// 157 us with 8 to 32 pages; B = 16, n_q = 4, 2048 to 4097: 69 us with 32 or 33 pages, 73 with 24,
+// 82 with 8. At most 256 ranges a sequence, as in the plain form.
+constexpr int kScoredRange = 32;
+int scored_max_range(int max_seq_len) {
+    return std::max(kScoredRange, ((max_seq_len + kPT - 1) / kPT + (int)kMaxSplits - 1) / (int)kMaxSplits);
 }
 
 // Positions per row of the scored form's stored scores: whole pages.
@@ -693,7 +735,7 @@ bool attn_decode_supported(int d, int page_tokens, int group, int nq) {
 }
 
 AttnPlan attn_decode_plan(bool swa, int window, int B, int Hq, int Hkv, int d, int page_tokens,
-                          int max_seq_len, int nq) {
+                          int max_seq_len, int nq, int max_range) {
     (void)page_tokens;
     (void)Hq;
     AttnPlan pl;
@@ -713,7 +755,7 @@ AttnPlan attn_decode_plan(bool swa, int window, int B, int Hq, int Hkv, int d, i
                      kMaxSplits}));
     const bool one_wave_fits = units * s_one <= slots && units * s_one * 4 >= slots * 3;
     long long splits = (one_wave_fits || units * s_many <= slots) ? s_one : s_many;
-    const long long pps = (tiles + splits - 1) / splits;
+    const long long pps = std::min<long long>((tiles + splits - 1) / splits, max_range);
     splits = (tiles + pps - 1) / pps;  // no empty range
     pl.n_splits = (int)splits;
     pl.pages_per_split = (int)pps;
@@ -725,13 +767,15 @@ AttnPlan attn_decode_plan(bool swa, int window, int B, int Hq, int Hkv, int d, i
 
 size_t attn_scored_ws_bytes(int nq, int B, int Hq, int Hkv, int d, int page_tokens,
                             int max_seq_len) {
-    const AttnPlan pl = attn_decode_plan(false, 0, B, Hq, Hkv, d, page_tokens, max_seq_len, nq);
+    const AttnPlan pl = attn_decode_plan(false, 0, B, Hq, Hkv, d, page_tokens, max_seq_len, nq,
+                                         scored_max_range(max_seq_len));
     return pl.ws_bytes + (size_t)B * nq * Hq * scored_len(max_seq_len) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {
     const AttnPlan plan = attn_decode_plan(a.swa, a.window, a.rows ? a.n_rows : a.B, a.Hq, a.Hkv,
-                                           a.d, a.page_tokens, a.max_seq_len, a.nq);
+                                           a.d, a.page_tokens, a.max_seq_len, a.nq,
+                                           a.weights ? scored_max_range(a.max_seq_len) : kWholeRange);
     if (a.d == 128) return launch_d<128>(a, plan, s);
     if (a.d == 64) return launch_d<64>(a, plan, s);
     return cudaErrorInvalidValue;

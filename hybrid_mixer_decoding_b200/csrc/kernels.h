@@ -174,8 +174,9 @@ struct AttnPlan {
     int n_ctas;           // grid size: one CTA per (sequence, kv-head, key range)
     size_t ws_bytes;
 };
+constexpr int kWholeRange = 1 << 30;  // no bound on the pages of a key range
 AttnPlan attn_decode_plan(bool swa, int window, int B, int Hq, int Hkv, int d, int page_tokens,
-                          int max_seq_len, int nq);
+                          int max_seq_len, int nq, int max_range = kWholeRange);
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s);
 // workspace of the scored form: the plan's partials and every row's scores
 size_t attn_scored_ws_bytes(int nq, int B, int Hq, int Hkv, int d, int page_tokens,

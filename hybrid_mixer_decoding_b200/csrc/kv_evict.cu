@@ -5,12 +5,12 @@
 // order: kept[0] < kept[1] < ..., entry kept[i] moves to position i. Attention over a set of keys
 // does not depend on their order, so the packed cache decodes as the same set of keys.
 //
-// Kernel 1 (choose), one CTA per (sequence, kv-head): the m-th largest of n weights is found
-// digit by digit (11, 11 and 10 bits of the weight's order-preserving integer, a histogram in
-// shared memory per digit). Then each of the 32 warps counts and, after one scan over the warps,
-// writes the entries of its own contiguous stretch: above the threshold, or equal to it while
-// equal ones are still wanted, lowest index first. The weights are read once, into shared
-// memory, up to kCacheKeys of them; longer sequences read them again per digit (from L2).
+// Kernel 1 (choose), one cluster of 1 to 8 CTAs per (sequence, kv-head): the m-th largest of n weights
+// is found digit by digit (11, 11 and 10 bits of the weight's order-preserving integer, a
+// histogram in shared memory per digit, added up over the cluster). Then each warp counts and,
+// after one scan over the warps and CTAs, writes the entries of its own contiguous stretch: above
+// the threshold, or equal to it while equal ones are still wanted, lowest index first. The
+// weights are read once, into shared memory, unless a CTA's share is above kCacheKeys.
 // Kernel 2 (move): rows of K and V and the weights go to their places. Into other pages, every
 // row is independent. Within the same pages, kept[i] >= i means that a destination is a source
 // of earlier rows only: one CTA owns one 64-byte column of the rows of a (sequence, kv-head) and
@@ -35,6 +35,9 @@ constexpr int kChooseThreads = 1024;
 constexpr int kWarps = kChooseThreads / 32;
 constexpr int kBins = 2048;           // 11 bits a digit
 constexpr int kCacheKeys = 49152;     // weights held in shared memory: 192 KiB
+constexpr int kMaxRanks = 8;          // CTAs of a cluster
+constexpr int kShare = 4096;          // a CTA of a cluster has at least this many entries
+constexpr int kSms = 148;
 constexpr int kMoveThreads = 256;
 constexpr int kRowsPerBlock = 64;     // rows moved by one CTA into other pages
 
@@ -62,47 +65,94 @@ __device__ __forceinline__ Row row_of(const EvictArgs &a, int b) {
     return r;
 }
 
-__global__ void __launch_bounds__(kChooseThreads, 1) evict_choose_kernel(const EvictArgs a) {
-    extern __shared__ uint32_t keys[];  // order keys of the first min(n_old, kCacheKeys) entries
-    __shared__ uint32_t hist[kBins];
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint2 ld_cluster_u2(const void *at, uint32_t rank) {
+    uint32_t remote;
+    uint2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(at)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(remote) : "memory");
+    return v;
+}
+
+// Grid (sequence, kv-head) x cluster size, clusters along x: CTA `rank` holds the entries
+// [rank * share, (rank + 1) * share) of the n_old ones.
+// CACHED: the share's order keys are held in shared memory; else they are formed again per digit.
+template <bool CACHED>
+__global__ void __launch_bounds__(kChooseThreads, 2) evict_choose_kernel(const EvictArgs a, int n_ranks) {
+    extern __shared__ uint32_t keys[];
+    __shared__ __align__(8) uint32_t hist[3][kBins];  // one per digit: a slower CTA may still read
     __shared__ uint32_t warp_gt[kWarps], warp_eq[kWarps];
-    __shared__ uint32_t s_digit, s_left;
+    __shared__ __align__(8) uint32_t s_count[2];      // this CTA's keys above and at the threshold
+    __shared__ uint32_t s_digit, s_left, s_whole;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int b = blockIdx.x / a.Hkv, g = blockIdx.x - b * a.Hkv;
+    const int rank = n_ranks > 1 ? (int)cluster_rank() : 0, bg = blockIdx.x / n_ranks;
+    const int b = bg / a.Hkv, g = bg - b * a.Hkv;
+    for (int i = tid; i < 3 * kBins; i += kChooseThreads) hist[0][i] = 0;
     griddep_launch_dependents();
     griddep_wait();  // the weights and lengths come from the steps before
     const Row r = row_of(a, b);
-    if (!r.ok && tid == 0 && g == 0) {
+    if (!r.ok && tid == 0 && g == 0 && rank == 0) {
         const int L = a.seq_lens[b];
         atomicOr(&g_err, (L < 0 || L > a.max_seq_len) ? HMD_DEVERR_SEQLEN : HMD_DEVERR_SLOT);
     }
-    int32_t *kept = a.kept + ((size_t)b * a.Hkv + g) * a.budget;
-    for (int i = r.n_keep + tid; i < a.budget; i += kChooseThreads) kept[i] = -1;
-    for (int i = r.m + tid; i < r.n_keep; i += kChooseThreads) kept[i] = r.n_old + (i - r.m);
+    int32_t *kept = a.kept + (size_t)bg * a.budget;
+    const int t_all = rank * kChooseThreads + tid, n_all = n_ranks * kChooseThreads;
+    for (int i = r.n_keep + t_all; i < a.budget; i += n_all) kept[i] = -1;
+    for (int i = r.m + t_all; i < r.n_keep; i += n_all) kept[i] = r.n_old + (i - r.m);
     if (r.m == r.n_old) {  // nothing to evict
-        for (int i = tid; i < r.m; i += kChooseThreads) kept[i] = i;
+        for (int i = t_all; i < r.m; i += n_all) kept[i] = i;
         return;
     }
     if (r.m == 0) return;  // the recent ones alone
-    const float *w = a.weights + ((size_t)r.slot * a.Hkv + g) * a.w_len;
-    const int n = r.n_old, n_cached = min(n, kCacheKeys);
-    auto key_at = [&](int i) { return i < n_cached ? keys[i] : order_key(w[i]); };
-    for (int i = tid; i < n_cached; i += kChooseThreads) keys[i] = order_key(w[i]);
+    // this CTA's entries: whole 32-entry groups
+    const int share = ((r.n_old + 31) / 32 + n_ranks - 1) / n_ranks * 32;
+    const int e0 = min(r.n_old, rank * share), n = min(r.n_old, e0 + share) - e0;
+    const float *w = a.weights + ((size_t)r.slot * a.Hkv + g) * a.w_len + e0;
+    auto key_at = [&](int i) { return CACHED ? keys[i] : order_key(w[i]); };
+    __syncthreads();  // the histograms are zero
+#pragma unroll 8
+    for (int i = tid; i < n; i += kChooseThreads) {
+        const uint32_t k = order_key(w[i]);
+        if (CACHED) keys[i] = k;
+        atomicAdd(&hist[0][k >> 21], 1u);
+    }
     // the m-th largest key: `left` of the keys that share the digits found so far are wanted
     uint32_t prefix = 0, mask = 0, left = (uint32_t)r.m;
 #pragma unroll 1
     for (int digit = 0; digit < 3; ++digit) {
         const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
         const uint32_t bits = digit == 2 ? 0x3ffu : 0x7ffu;
-        for (int i = tid; i < kBins; i += kChooseThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += kChooseThreads) {
-            const uint32_t k = key_at(i);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & bits], 1u);
+        if (digit > 0) {
+#pragma unroll 8
+            for (int i = tid; i < n; i += kChooseThreads) {
+                const uint32_t k = key_at(i);
+                if ((k & mask) == prefix) atomicAdd(&hist[digit][(k >> shift) & bits], 1u);
+            }
         }
-        __syncthreads();
+        if (n_ranks > 1) cluster_sync_all();
+        else __syncthreads();
         // counts from the largest digit down: thread t holds digits 2047 - 2t and 2046 - 2t
-        const uint32_t c0 = hist[kBins - 1 - 2 * tid], c1 = hist[kBins - 2 - 2 * tid];
+        const uint32_t *at = &hist[digit][kBins - 2 - 2 * tid];
+        uint2 v = *reinterpret_cast<const uint2 *>(at);
+        uint32_t c0 = v.y, c1 = v.x;
+        if (n_ranks > 1) {
+            uint2 x[kMaxRanks];  // all ranks' counts in flight at once
+#pragma unroll
+            for (int q = 0; q < kMaxRanks; ++q)
+                x[q] = q < n_ranks && q != rank ? ld_cluster_u2(at, q) : make_uint2(0, 0);
+#pragma unroll
+            for (int q = 0; q < kMaxRanks; ++q) {
+                c0 += x[q].y;
+                c1 += x[q].x;
+            }
+        }
         uint32_t sum = c0 + c1;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -116,19 +166,27 @@ __global__ void __launch_bounds__(kChooseThreads, 1) evict_choose_kernel(const E
         if (before < left && left <= before + c0) {
             s_digit = kBins - 1 - 2 * tid;
             s_left = left - before;
+            s_whole = left == before + c0;
         } else if (before + c0 < left && left <= before + c0 + c1) {
             s_digit = kBins - 2 - 2 * tid;
             s_left = left - before - c0;
+            s_whole = left == before + c0 + c1;
         }
         __syncthreads();
         prefix |= s_digit << shift;
         mask |= bits << shift;
         left = s_left;
+        if (s_whole) {  // every key that shares these digits is wanted: no further digit decides
+            prefix -= 1;  // not 0: less than all keys are wanted
+            left = 0;
+            break;
+        }
     }
-    // each warp's stretch of whole 32-entry groups: count, scan over the warps, write
+    // each warp's stretch of whole 32-entry groups: count, scan over the warps and CTAs, write
     const int per_warp = ((n + 31) / 32 + kWarps - 1) / kWarps * 32;
     const int i0 = min(n, warp * per_warp), i1 = min(n, i0 + per_warp);
     uint32_t n_gt = 0, n_eq = 0;
+#pragma unroll 8
     for (int i = i0 + lane; i < i1; i += 32) {
         const uint32_t k = key_at(i);
         n_gt += k > prefix;
@@ -142,10 +200,30 @@ __global__ void __launch_bounds__(kChooseThreads, 1) evict_choose_kernel(const E
     }
     __syncthreads();
     uint32_t gt = 0, eq = 0;  // keys above and at the threshold before this stretch
+    if (n_ranks > 1) {
+        if (warp == 0) {
+            const uint32_t g_all = __reduce_add_sync(0xffffffffu, warp_gt[lane]);
+            const uint32_t e_all = __reduce_add_sync(0xffffffffu, warp_eq[lane]);
+            if (lane == 0) {
+                s_count[0] = g_all;
+                s_count[1] = e_all;
+            }
+        }
+        cluster_sync_all();
+        uint2 x[kMaxRanks];
+#pragma unroll
+        for (int q = 0; q < kMaxRanks; ++q) x[q] = q < rank ? ld_cluster_u2(s_count, q) : make_uint2(0, 0);
+#pragma unroll
+        for (int q = 0; q < kMaxRanks; ++q) {
+            gt += x[q].x;
+            eq += x[q].y;
+        }
+    }
     for (int v = 0; v < warp; ++v) {
         gt += warp_gt[v];
         eq += warp_eq[v];
     }
+#pragma unroll 4
     for (int i = i0; i < i1; i += 32) {
         const uint32_t k = i + lane < i1 ? key_at(i + lane) : 0u;
         const uint32_t is_gt = __ballot_sync(0xffffffffu, i + lane < i1 && k > prefix);
@@ -153,10 +231,11 @@ __global__ void __launch_bounds__(kChooseThreads, 1) evict_choose_kernel(const E
         const uint32_t below = (1u << lane) - 1u;
         const uint32_t my_gt = gt + __popc(is_gt & below), my_eq = eq + __popc(is_eq & below);
         const bool take = ((is_gt >> lane) & 1u) || (((is_eq >> lane) & 1u) && my_eq < left);
-        if (take) kept[my_gt + min(my_eq, left)] = i + lane;
+        if (take) kept[my_gt + min(my_eq, left)] = e0 + i + lane;
         gt += __popc(is_gt);
         eq += __popc(is_eq);
     }
+    if (n_ranks > 1) cluster_sync_all();  // nobody leaves while its counts are still read
 }
 
 // Row address of position i under a table (nullptr and an error for a page outside the pool).
@@ -271,14 +350,32 @@ __global__ void __launch_bounds__(kMoveThreads) evict_pack_kernel(const EvictArg
 
 cudaError_t launch_kv_evict(const EvictArgs &a, cudaStream_t s) {
     const cudaError_t attr_err = once_per_device([] {
-        return cudaFuncSetAttribute(evict_choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(evict_choose_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kCacheKeys * 4);
     });
     if (attr_err != cudaSuccess) return attr_err;
     const int heads = a.B * a.Hkv;
-    const int smem = std::min(a.max_seq_len, kCacheKeys) * 4;
-    cudaError_t e = launch_pdl(evict_choose_kernel, dim3((unsigned)heads), dim3(kChooseThreads),
-                               (size_t)smem, s, a);
+    // Split an entry list over a cluster while every CTA keeps at least kShare entries and the
+    // clusters of all heads fit the GPU at once (two CTAs per SM).
+    int n_ranks = 1;
+    while (n_ranks < kMaxRanks && a.max_seq_len / (2 * n_ranks) >= kShare && heads * 2 * n_ranks <= 2 * kSms) n_ranks *= 2;
+    const int share = ((a.max_seq_len + 31) / 32 + n_ranks - 1) / n_ranks * 32;
+    const bool cached = share <= kCacheKeys;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(heads * n_ranks));
+    cfg.blockDim = dim3(kChooseThreads);
+    cfg.dynamicSmemBytes = cached ? (size_t)share * 4 : 0;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)n_ranks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = n_ranks > 1 ? 2 : 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, cached ? evict_choose_kernel<true> : evict_choose_kernel<false>, a, n_ranks);
     if (e != cudaSuccess) return e;
     const bool same_pages = a.dst_table == a.page_table, same_weights = a.weights_out == a.weights;
     if (!same_pages) {

@@ -65,6 +65,9 @@ struct LatentParams {
     float *part_o;   // [n_ranges + B][n_groups][32][dc], see part_index
     float *part_ml;  // [n_ranges + B][n_groups][32][2]: exponent base, sum (-1: range gave up)
     int32_t *cum;    // [B + 1] pages before each sequence
+    int4 *start;     // [n_ranges + 1]: a range's first page, its sequence, that sequence's first page
+                     // and the page after its last
+    int2 *ranges;    // [B]: a sequence's ranges [x, y)
 };
 
 // Range i < n covers the flat pages [i P / n, (i + 1) P / n), n = min(n_ranges, P), so none is
@@ -74,7 +77,7 @@ __device__ __forceinline__ int range_begin(int i, int P, int n) {
     return (int)((long long)i * P / n);
 }
 __device__ __forceinline__ int range_of(int page, int P, int n) {
-    return (int)((((long long)page + 1) * n - 1) / P);
+    return (int)((((long long)page + 1) * n - 1) / P);  // P > 0
 }
 __device__ __forceinline__ size_t part_index(const LatentParams &p, int range, int b, int group) {
     return (size_t)(range + b) * p.n_groups + group;
@@ -90,7 +93,7 @@ struct AbsSmem {
     __nv_bfloat16 w[D][WP];
 };
 
-// The last block: lengths to running page counts.
+// The last block: lengths to running page counts, the ranges' first pages and the sequences' ranges.
 __device__ void schedule_block(const LatentParams &p) {
     __shared__ int warp_sum[kAbsThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -116,6 +119,27 @@ __device__ void schedule_block(const LatentParams &p) {
         if (b < p.B) p.cum[b + 1] = base + sum;
         for (int v = 0; v < kAbsThreads / 32; ++v) base += warp_sum[v];
         __syncthreads();
+    }
+    const int P = base, n_live = min(p.n_ranges, P);
+    for (int i = tid; i <= p.n_ranges; i += kAbsThreads) {
+        int4 st = make_int4(P, 0, 0, 0);
+        if (i < n_live) {
+            // the last sequence whose pages start at or before the range's first page
+            st.x = range_begin(i, P, n_live);
+            int lo = 0, hi = p.B;  // cum[lo] <= st.x < cum[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (p.cum[mid] <= st.x) lo = mid;
+                else hi = mid;
+            }
+            st = make_int4(st.x, lo, p.cum[lo], p.cum[lo + 1]);
+        }
+        p.start[i] = st;
+    }
+    for (int b = tid; b < p.B; b += kAbsThreads) {
+        const int c0 = p.cum[b], c1 = p.cum[b + 1];
+        p.ranges[b] = c1 > c0 ? make_int2(range_of(c0, P, n_live), range_of(c1 - 1, P, n_live) + 1)
+                              : make_int2(0, 0);
     }
 }
 
@@ -318,13 +342,13 @@ __device__ __forceinline__ bool bar_softmax_or(bool pred) {
 // A CTA's walk over its flat pages: the sequence of page `at`, and that sequence's last page in
 // the range.
 struct Walk {
-    int b, at, seg_begin, seg_end;
+    int b, at, page0, seg_begin, seg_end;  // page0: the sequence's first page
     __device__ __forceinline__ void seek(const LatentParams &p, int end) {  // at == seg_end < end
         do {
             ++b;
             seg_end = uniform(p.cum[b + 1]);
         } while (seg_end <= at);  // skips sequences without pages; ends: cum[B] >= end > at
-        seg_begin = at;
+        page0 = seg_begin = at;
         seg_end = min(end, seg_end);
     }
 };
@@ -346,7 +370,6 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
     uint8_t *misc = sm + SM::OFF_MISC + 512;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
-    int *s_first = reinterpret_cast<int *>(misc + 8);                 // first sequence of the range
     volatile int *page_ok = reinterpret_cast<volatile int *>(misc + 16);  // [NS]
     float(*s_red)[kRows] = reinterpret_cast<float(*)[kRows]>(misc + 64);  // [4][32]
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -366,39 +389,24 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
     }
     griddep_launch_dependents();
     griddep_wait();  // the image, the appended rows and the schedule are kernel 1's
-    const int P = uniform(p.cum[p.B]);
-    const int n_live = min(p.n_ranges, P);
-    const int begin = range < n_live ? range_begin(range, P, n_live) : 0;
-    const int end = range < n_live ? range_begin(range + 1, P, n_live) : 0;
-    if (warp == 4 && begin < end) {
-        // the sequence of page `begin`: the last one whose pages start at or before it
-        int lo = 0, n = p.B;  // in [lo, lo + n)
-        while (n > 1) {
-            const int step = (n + 31) / 32;
-            const int b = lo + lane * step;
-            const bool le = lane * step < n && p.cum[b] <= begin;
-            const int hit = 31 - __clz((int)__ballot_sync(0xffffffffu, le));
-            n = min(step, n - hit * step);
-            lo += hit * step;
-        }
-        if (lane == 0) *s_first = lo;
-    }
+    const int4 st0 = p.start[range], st1 = p.start[range + 1];
+    const int begin = uniform(st0.x), end = uniform(st1.x), n_pages = end - begin;
+    Walk w;
+    w.b = uniform(st0.y);
+    w.at = w.seg_begin = begin;
+    w.page0 = uniform(st0.z);
+    w.seg_end = min(end, uniform(st0.w));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
-    const int n_pages = end - begin;
-    Walk w;
-    w.b = n_pages > 0 ? uniform(*s_first) : 0;
-    w.at = w.seg_begin = begin;
-    w.seg_end = n_pages > 0 ? min(end, uniform(p.cum[w.b + 1])) : begin;
 
     if (warp == 4) {
         // ================= copies: the queries of each sequence, and its pages ==============
         bool ok = true;
         int k = 0, seg = 0, issued = 0, q_issued = 0;  // issued: units, in order (lane 0)
         while (ok && w.at < end) {
-            const int b = w.b, first = w.at - p.cum[b], n = w.seg_end - w.at;
+            const int b = w.b, first = w.at - w.page0, n = w.seg_end - w.at;
             if (seg > 0) ok = wait_or_abort(bar(SM::B_QFREE), (seg - 1) & 1, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -542,7 +550,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
         bool ok = true;
         int k = 0;
         while (ok && w.at < end) {
-            const int b = w.b, L = p.seq_lens[b], page0 = p.cum[b];
+            const int b = w.b, L = p.seq_lens[b], page0 = w.page0;
             // the last position each of this thread's rows sees (-1: no such row)
             int last[8];
             float base[8], l[8];
@@ -726,16 +734,17 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
 }
 
 // ---- kernel 3 ----------------------------------------------------------------------------------
-constexpr int kExpThreads = 256;
+constexpr int kExpThreads = 512;
+constexpr int kExpWarps = kExpThreads / 32;
 constexpr int kExpTok = 16;  // tokens (b, i) per cluster
 template <int D>
 struct ExpSmem {
     static constexpr int WP = 128 + 8;  // pitch (elements) without bank conflicts
     __nv_bfloat16 w[D][WP];             // W_uv[h][v][this CTA's 128 dims]
     __nv_bfloat16 hi[kExpTok][WP], lo[kExpTok][WP];
-    float red[8][128];                  // a row's partial sums, per warp
+    float red[kExpWarps][128];          // a row's partial sums, per warp
     float out[kExpTok][D];              // this CTA's part of the output
-    float den[8];
+    float den[kExpWarps];
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -770,19 +779,17 @@ __global__ void __launch_bounds__(kExpThreads) latent_expand_kernel(const Latent
         cp_async16(smem_u32(&sm.w[v][c]), wv + (size_t)v * p.dc + c);  // lands during the merge
     }
     // merge the ranges: `wpr` warps share a token's ranges, lanes its 128 dims (4 each)
-    const int P = p.cum[p.B], n_live = min(p.n_ranges, P);
-    const int wpr = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8;
+    const int wpr = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;
     uint32_t missing = 0;  // tokens of which a range gave up
-    for (int r0 = 0; r0 < rows; r0 += 8 / wpr) {
+    for (int r0 = 0; r0 < rows; r0 += kExpWarps / wpr) {
         const int r = r0 + warp / wpr, part = warp % wpr;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float M = -INFINITY, den = 0.f;
         bool lost = false;
         if (r < rows) {
             const int tok = tok0 + r, b = tok / p.nq, row = (tok - b * p.nq) * p.H + h;
-            const int pg0 = p.cum[b], pg1 = p.cum[b + 1];
-            const int i0 = pg1 > pg0 ? range_of(pg0, P, n_live) : 0;
-            const int i1 = pg1 > pg0 ? range_of(pg1 - 1, P, n_live) + 1 : 0;
+            const int2 range = p.ranges[b];
+            const int i0 = range.x, i1 = range.y;
             const int g = row / kRows, c = row % kRows;
             for (int i = i0 + lane; i < i1; i += 32) {
                 const float2 v = *reinterpret_cast<const float2 *>(
@@ -828,7 +835,7 @@ __global__ void __launch_bounds__(kExpThreads) latent_expand_kernel(const Latent
         }
         if (r < rows && lost) missing |= 1u << r;
     }
-    for (int r = rows + warp; r < kExpTok; r += 8) {  // rows without a token
+    for (int r = rows + warp; r < kExpTok; r += kExpWarps) {  // rows without a token
         *reinterpret_cast<uint2 *>(&sm.hi[r][lane * 4]) = make_uint2(0u, 0u);
         *reinterpret_cast<uint2 *>(&sm.lo[r][lane * 4]) = make_uint2(0u, 0u);
     }
@@ -838,28 +845,23 @@ __global__ void __launch_bounds__(kExpThreads) latent_expand_kernel(const Latent
     cp_async_wait_all();
     __syncthreads();
     if (lane == 0 && missing) atomicOr(&s_missing, missing);
-    // out[16 tokens][D] = latent output x W_uv^T over this CTA's dims; a warp takes D / 8 columns
-    constexpr int NT = D / 64;  // 8-column tiles per warp
-    float acc[NT][4] = {};
+    // out[16 tokens][D] = latent output x W_uv^T over this CTA's dims; a warp takes 8 columns
+    if (warp < D / 8) {
+        float acc[4] = {};
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-        uint32_t ah[4], al[4];
-        ldmatrix_x4(smem_u32(&sm.hi[lane & 15][kk * 16 + (lane >> 4) * 8]), ah[0], ah[1], ah[2], ah[3]);
-        ldmatrix_x4(smem_u32(&sm.lo[lane & 15][kk * 16 + (lane >> 4) * 8]), al[0], al[1], al[2], al[3]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const __nv_bfloat16 *wr = &sm.w[warp * NT * 8 + n * 8 + (lane >> 2)][kk * 16 + (lane & 3) * 2];
+        for (int kk = 0; kk < 8; ++kk) {
+            uint32_t ah[4], al[4];
+            ldmatrix_x4(smem_u32(&sm.hi[lane & 15][kk * 16 + (lane >> 4) * 8]), ah[0], ah[1], ah[2], ah[3]);
+            ldmatrix_x4(smem_u32(&sm.lo[lane & 15][kk * 16 + (lane >> 4) * 8]), al[0], al[1], al[2], al[3]);
+            const __nv_bfloat16 *wr = &sm.w[warp * 8 + (lane >> 2)][kk * 16 + (lane & 3) * 2];
             const uint32_t b0 = *reinterpret_cast<const uint32_t *>(wr);
             const uint32_t b1 = *reinterpret_cast<const uint32_t *>(wr + 8);
-            mma_bf16_16816(acc[n], ah, b0, b1);
-            mma_bf16_16816(acc[n], al, b0, b1);
+            mma_bf16_16816(acc, ah, b0, b1);
+            mma_bf16_16816(acc, al, b0, b1);
         }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int v = warp * NT * 8 + n * 8 + (lane & 3) * 2;
-        *reinterpret_cast<float2 *>(&sm.out[lane >> 2][v]) = make_float2(acc[n][0], acc[n][1]);
-        *reinterpret_cast<float2 *>(&sm.out[(lane >> 2) + 8][v]) = make_float2(acc[n][2], acc[n][3]);
+        const int v = warp * 8 + (lane & 3) * 2;
+        *reinterpret_cast<float2 *>(&sm.out[lane >> 2][v]) = make_float2(acc[0], acc[1]);
+        *reinterpret_cast<float2 *>(&sm.out[(lane >> 2) + 8][v]) = make_float2(acc[2], acc[3]);
     }
     cluster_sync_all();
     // every CTA of the cluster finishes a share of the elements, adding the parts in rank order
@@ -894,7 +896,7 @@ int device_sms() {
 
 struct Plan {
     int n_groups, n_ranges;
-    size_t off_o, off_ml, off_cum, bytes;
+    size_t off_o, off_ml, off_start, off_ranges, off_cum, bytes;
 };
 Plan make_plan(int nq, int B, int H, int dc, int max_seq_len) {
     Plan pl;
@@ -905,7 +907,9 @@ Plan make_plan(int nq, int B, int H, int dc, int max_seq_len) {
     const size_t pieces = (size_t)(pl.n_ranges + B) * pl.n_groups;
     pl.off_o = (size_t)B * pl.n_groups * (dc / 64 + 1) * kBlk;
     pl.off_ml = pl.off_o + pieces * kRows * dc * sizeof(float);
-    pl.off_cum = pl.off_ml + pieces * kRows * 2 * sizeof(float);
+    pl.off_start = pl.off_ml + pieces * kRows * 2 * sizeof(float);
+    pl.off_ranges = pl.off_start + ((size_t)pl.n_ranges + 1) * sizeof(int4);
+    pl.off_cum = pl.off_ranges + (size_t)B * sizeof(int2);
     pl.bytes = pl.off_cum + (((size_t)B + 1) * sizeof(int32_t) + 15) / 16 * 16;
     return pl;
 }
@@ -992,6 +996,8 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t s) {
     p.q_img = ws;
     p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
     p.part_ml = reinterpret_cast<float *>(ws + pl.off_ml);
+    p.start = reinterpret_cast<int4 *>(ws + pl.off_start);
+    p.ranges = reinterpret_cast<int2 *>(ws + pl.off_ranges);
     p.cum = reinterpret_cast<int32_t *>(ws + pl.off_cum);
     cudaError_t e = a.d == 128 ? launch_absorb<128>(p, s) : launch_absorb<64>(p, s);
     if (e != cudaSuccess) return e;
