@@ -95,6 +95,8 @@ bool make_tmap_bthd(CUtensorMap *m, CUtensorMapDataType dt, int esize, const voi
 bool make_tmap_blocks_sw128(CUtensorMap *m, CUtensorMapDataType dt, const void *base,
                             long long heads, long long head_stride, long long rows, int cols,
                             int box_rows);
+bool make_tmap_colblocks_sw128(CUtensorMap *m, CUtensorMapDataType dt, const void *base, long long rows,
+                               int pitch, int n_blocks, int box_rows, int box_blocks);
 bool make_tmap_pool_sw128(CUtensorMap *m, void *pool, int n_pages, int heads, int d);
 
 // Input activations of the delta-rule mixers, fused into their kernels when A_log is set: the

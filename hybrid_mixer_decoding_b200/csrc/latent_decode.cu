@@ -16,18 +16,19 @@
 // lays out the schedule (running page counts of the batch).
 // Kernel 2 (attention): the batch's pages, laid end to end, are cut into equal ranges, one per
 // SM (times the row groups of 32 rows), whatever the lengths are; a CTA's range may end one
-// sequence and begin another. Per page of 64 keys, with keys and latent dims as the M of the
-// products (the few query rows as N, so nothing is padded to 128 rows):
-//     S^T [64 keys x 64] = C [64 x (d_c + 64)] [q~hi ; q~lo]^T     tcgen05, M = 64, N = 64
-//     O^T [d_c x 32]    += C^T [d_c x 64 keys] P^T                 tcgen05, M = 128, N = 32
-// both from the same shared-memory tile of C (K-major, then MN-major). Warp-specialised: warp 4
-// streams pages by TMA (units of 128 dims, each freed as soon as its product is done), warp 5
-// issues the products, warps 0-3 are the softmax. O^T accumulates at an exponent base per row
-// that moves only when the row's scores exceed it by more than 2^8 (then O^T is rescaled in
-// TMEM), so the common page needs one vote and no exchange of maxima.
-// Kernel 3 (merge and expand), one cluster per (head, 16 tokens) with a CTA per 128 latent dims:
-// joins the ranges' partial sums, multiplies by its dims' part of W_uv[h] (mma.sync, the latent
-// output as a bf16 pair) and adds up over the cluster in rank order.
+// sequence and begin another. Per page of 64 keys:
+//     S   [32 hi, 32 lo rows x 64 keys] = [q~hi ; q~lo] C^T   tcgen05, M = 128, N = 64, q~ in TMEM
+//     O^T [d_c x 32 rows] += C^T [d_c x 64 keys] P^T          tcgen05, M = 128, N = 32
+// both from the same shared-memory tile of C (K-major, then MN-major). The few rows are the N of the
+// second product, so that its accumulator fits TMEM beside the queries, and only pages are left in
+// shared memory: three of 72 KiB are in flight or in use, which is what covers HBM's latency (two, with
+// the queries in shared memory as well, reached 4.5 TB/s). Warp-specialised: warp 4 streams pages
+// by TMA (units of 128 dims, each freed as soon as its product is done), warp 5 issues the products,
+// warps 0-3 are the softmax. O^T accumulates at an exponent base per row that moves only when the
+// row's scores exceed it by more than 2^8 (then O^T is rescaled in TMEM).
+// Kernel 3 (merge and expand), one CTA per (head, 16 or 32 tokens): joins the ranges' partial sums
+// while W_uv[h] is copied to shared memory, and multiplies by it (mma.sync, the latent output as a
+// bf16 pair). Bound by latency: one pass over the partial sums, one over W_uv.
 #include <cuda.h>
 
 #include <algorithm>
@@ -64,11 +65,16 @@ struct LatentParams {
     uint8_t *q_img;  // [B][n_groups][dc / 64 + 1 blocks] of 64 rows: 32 hi, 32 lo
     float *part_o;   // [n_ranges + B][n_groups][32][dc], see part_index
     float *part_ml;  // [n_ranges + B][n_groups][32][2]: exponent base, sum (-1: range gave up)
-    int32_t *cum;    // [B + 1] pages before each sequence
+    int32_t *cum;    // [B + 1] pages before each sequence (kernel 1's own, for large batches)
     int4 *start;     // [n_ranges + 1]: a range's first page, its sequence, that sequence's first page
-                     // and the page after its last
+                     // and its length
     int2 *ranges;    // [B]: a sequence's ranges [x, y)
 };
+
+// Pages of a sequence: none for an unused row or a length that is refused.
+__device__ __forceinline__ int pages_of(const LatentParams &p, int L) {
+    return L >= p.nq && L <= p.max_seq_len ? (L + kPT - 1) / kPT : 0;
+}
 
 // Range i < n covers the flat pages [i P / n, (i + 1) P / n), n = min(n_ranges, P), so none is
 // empty. Ranges and sequences both grow along the pages, so (range + sequence) is different for
@@ -94,18 +100,23 @@ struct AbsSmem {
 };
 
 // The last block: lengths to running page counts, the ranges' first pages and the sequences' ranges.
-__device__ void schedule_block(const LatentParams &p) {
+// s_cum: room for kCumShared counts in shared memory, where the search reads them (a larger batch's
+// are read from global memory).
+constexpr int kCumShared = 4096;
+__device__ void schedule_block(const LatentParams &p, int32_t *s_cum) {
     __shared__ int warp_sum[kAbsThreads / 32];
+    const bool in_shared = p.B < kCumShared;
+    int32_t *cum = in_shared ? s_cum : p.cum;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int base = 0;
-    if (tid == 0) p.cum[0] = 0;
+    if (tid == 0) cum[0] = 0;
     for (int b0 = 0; b0 < p.B; b0 += kAbsThreads) {
         const int b = b0 + tid;
         int n = 0;
         if (b < p.B) {
             const int L = p.seq_lens[b];
-            if (L >= p.nq && L <= p.max_seq_len) n = (L + kPT - 1) / kPT;
-            else if (L != 0) atomicOr(&g_err, HMD_DEVERR_SEQLEN);
+            n = pages_of(p, L);
+            if (n == 0 && L != 0) atomicOr(&g_err, HMD_DEVERR_SEQLEN);
         }
         int sum = n;
 #pragma unroll
@@ -116,7 +127,7 @@ __device__ void schedule_block(const LatentParams &p) {
         if (lane == 31) warp_sum[warp] = sum;
         __syncthreads();
         for (int v = 0; v < warp; ++v) sum += warp_sum[v];
-        if (b < p.B) p.cum[b + 1] = base + sum;
+        if (b < p.B) cum[b + 1] = base + sum;
         for (int v = 0; v < kAbsThreads / 32; ++v) base += warp_sum[v];
         __syncthreads();
     }
@@ -129,20 +140,21 @@ __device__ void schedule_block(const LatentParams &p) {
             int lo = 0, hi = p.B;  // cum[lo] <= st.x < cum[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if (p.cum[mid] <= st.x) lo = mid;
+                if (cum[mid] <= st.x) lo = mid;
                 else hi = mid;
             }
-            st = make_int4(st.x, lo, p.cum[lo], p.cum[lo + 1]);
+            st = make_int4(st.x, lo, cum[lo], p.seq_lens[lo]);
         }
         p.start[i] = st;
     }
     for (int b = tid; b < p.B; b += kAbsThreads) {
-        const int c0 = p.cum[b], c1 = p.cum[b + 1];
+        const int c0 = cum[b], c1 = cum[b + 1];
         p.ranges[b] = c1 > c0 ? make_int2(range_of(c0, P, n_live), range_of(c1 - 1, P, n_live) + 1)
                               : make_int2(0, 0);
     }
 }
 
+static_assert(sizeof(AbsSmem<64>) >= kCumShared * sizeof(int32_t), "the schedule's counts fit");
 template <int D>
 __global__ void __launch_bounds__(kAbsThreads) latent_absorb_kernel(const LatentParams p) {
     extern __shared__ __align__(16) uint8_t abs_smem[];
@@ -152,7 +164,7 @@ __global__ void __launch_bounds__(kAbsThreads) latent_absorb_kernel(const Latent
     griddep_wait();
     const int n_tok = p.B * p.nq, dq = D + kDR, row_w = p.dc + kDR;
     if (blockIdx.x == gridDim.x - 1) {
-        schedule_block(p);
+        schedule_block(p, reinterpret_cast<int32_t *>(abs_smem));
         return;
     }
     const int n_app = (n_tok + kAbsThreads / 32 - 1) / (kAbsThreads / 32);
@@ -274,58 +286,38 @@ __global__ void __launch_bounds__(kAbsThreads) latent_absorb_kernel(const Latent
 
 // ---- kernel 2 ----------------------------------------------------------------------------------
 constexpr int kAttThreads = 192;
-// Shared memory for d_c = 128 * NP: the queries' image, page stages, P, barriers. A page is NP
-// units of 128 dims (two blocks) and one of the shared part (one block).
+// Shared memory for d_c = 128 * NP: a ring of page slots, P, barriers. A page is NP units of 128 dims
+// (two blocks) and one of the shared part (one block); a sequence's queries pass through a slot too.
 template <int NP>
 struct AttSmem {
     static constexpr uint32_t PAGE = (2 * NP + 1) * kBlk;
-    static constexpr int NS = NP >= 3 ? 2 : 4;  // page stages: what 227 KiB hold
-    static constexpr uint32_t OFF_Q = 0;
-    static constexpr uint32_t OFF_C = PAGE;
-    static constexpr uint32_t OFF_P = OFF_C + NS * PAGE;       // two tiles [32 rows][64 keys]
-    static constexpr uint32_t OFF_MISC = OFF_P + 2 * kRows * 128;
-    static constexpr uint32_t BYTES = OFF_MISC + 2048;
+    static constexpr int NS = NP >= 3 ? 3 : NP == 2 ? 5 : 6;  // slots: what 227 KiB hold
+    static constexpr uint32_t OFF_P = NS * PAGE;               // [32 rows][64 keys] bf16
+    static constexpr uint32_t OFF_HI = OFF_P + kRows * 128;    // [keys 32-63][32 rows] fp32: high scores
+    static constexpr uint32_t OFF_LO = OFF_HI + 32 * kRows * 4;  // [key pairs 0-15][32 rows]: low scores
+    static constexpr uint32_t OFF_MISC = OFF_LO + 16 * kRows * 4;
+    static constexpr uint32_t BYTES = OFF_MISC + 1024;
     static constexpr uint32_t ALLOC = BYTES > 118784 ? BYTES : 118784;  // one CTA per SM
     // barriers
     static constexpr int B_FULL = 0;                      // [NS][NP + 1] unit landed (TMA)
-    static constexpr int B_FREE = B_FULL + NS * (NP + 1);  // [NS][NP + 1] unit's products done
-    static constexpr int B_QFULL = B_FREE + NS * (NP + 1);
-    static constexpr int B_QFREE = B_QFULL + 1;
-    static constexpr int B_S = B_QFREE + 1;  // [2] scores computed
-    static constexpr int B_P = B_S + 2;      // [2] weights written (four warps)
-    static constexpr int B_O = B_P + 2;      // [2] the page's output product done
-    static constexpr int B_END = B_O + 2;    // everything issued is done (teardown)
+    static constexpr int B_FREE = B_FULL + NS * (NP + 1);  // [NS][NP + 1] unit's readers done
+    static constexpr int B_Q = B_FREE + NS * (NP + 1);     // queries in TMEM (two warps)
+    static constexpr int B_S = B_Q + 1;    // scores computed
+    static constexpr int B_SR = B_S + 1;   // scores read (two warps)
+    static constexpr int B_P = B_SR + 1;   // weights written (four warps)
+    static constexpr int B_O = B_P + 1;    // the page's output product done
+    static constexpr int B_END = B_O + 1;  // everything issued is done (teardown)
     static constexpr int N_BARS = B_END + 1;
     static_assert(N_BARS * 8 <= 512, "barriers");
 };
-static_assert(AttSmem<4>::ALLOC + 1024 <= 232448, "shared memory per CTA");
-// TMEM: scores of even and odd pages, then O^T of every unit
-constexpr uint32_t kTmemS = 0, kTmemO = 128, kTmemCols = 256;
+static_assert(AttSmem<4>::ALLOC <= 232448, "shared memory per CTA");
+// TMEM columns: scores [64 rows, then unused lanes][64 keys], O^T of every unit [128 dims][32 rows],
+// the queries as packed bf16 pairs [32 hi, 32 lo rows][(d_c + 64) / 2]
+constexpr uint32_t kTmemS = 0, kTmemO = 64, kTmemQ = 192, kTmemCols = 512;
 
-// 16 lanes x 64 columns of TMEM words: register 4j + e of thread t holds lane (base + t / 4 +
-// 8 (e / 2)), column 8j + 2 (t % 4) + e % 2.
-__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-// Four 8x8 b16 matrices to shared memory, transposed: lane l gives the address of row l % 8 of
-// matrix l / 8.
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1,
-                                                  uint32_t r2, uint32_t r3) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
-                 "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-                 : "memory");
-}
-// The softmax warps' own barrier, and the same with an OR over a predicate.
+// Barriers of the four softmax warps, of the two that read scores, and an OR over a predicate.
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void bar_scores() { asm volatile("bar.sync 2, 64;" ::: "memory"); }
 __device__ __forceinline__ bool bar_softmax_or(bool pred) {
     uint32_t r;
     asm volatile(
@@ -339,29 +331,35 @@ __device__ __forceinline__ bool bar_softmax_or(bool pred) {
     return r != 0;
 }
 
-// A CTA's walk over its flat pages: the sequence of page `at`, and that sequence's last page in
-// the range.
+// A CTA's walk over its flat pages: the sequence of page `at`, and that sequence's last page in the
+// range. The next sequence's length is read when a sequence begins: a load that something waits
+// for takes microseconds while pages fill the SM's way to L2.
 struct Walk {
     int b, at, page0, seg_begin, seg_end;  // page0: the sequence's first page
+    int L, next_L;
+    __device__ __forceinline__ void enter(const LatentParams &p, int end, int length) {
+        L = length;
+        seg_begin = at;
+        seg_end = min(end, page0 + pages_of(p, L));
+        next_L = b + 1 < p.B ? p.seq_lens[b + 1] : 0;
+    }
     __device__ __forceinline__ void seek(const LatentParams &p, int end) {  // at == seg_end < end
-        do {
-            ++b;
-            seg_end = uniform(p.cum[b + 1]);
-        } while (seg_end <= at);  // skips sequences without pages; ends: cum[B] >= end > at
-        page0 = seg_begin = at;
-        seg_end = min(end, seg_end);
+        int length = uniform(next_L);
+        ++b;
+        while (pages_of(p, length) == 0) length = uniform(p.seq_lens[++b]);  // there is one: at < end
+        page0 = at;
+        enter(p, end, length);
     }
 };
 
 template <int NP>
 __global__ void __launch_bounds__(kAttThreads, 1)
-latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams p) {
+latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant__ CUtensorMap tmr,
+                     const LatentParams p) {
     using SM = AttSmem<NP>;
     constexpr int NS = SM::NS, NU = NP + 1;
     constexpr uint32_t PAGE = SM::PAGE;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];  // no byte is left to align it by hand
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + SM::OFF_MISC;
     auto bar = [&](int i) { return bars + 8 * i; };
@@ -371,16 +369,18 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
     volatile int *page_ok = reinterpret_cast<volatile int *>(misc + 16);  // [NS]
-    float(*s_red)[kRows] = reinterpret_cast<float(*)[kRows]>(misc + 64);  // [4][32]
+    float *s_f = reinterpret_cast<float *>(misc + 64);                    // [32] rescaling factors
+    float(*s_mx)[kRows] = reinterpret_cast<float(*)[kRows]>(misc + 192);  // [2] maxima, then sums
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int group = blockIdx.x % p.n_groups, range = blockIdx.x / p.n_groups;
 
     if (tid == 0) {
         for (int i = 0; i < SM::N_BARS; ++i)
-            mbar_init(bar(i), (i == SM::B_P || i == SM::B_P + 1) ? 4 : 1);
+            mbar_init(bar(i), i == SM::B_P ? 4 : (i == SM::B_Q || i == SM::B_SR) ? 2 : 1);
         fence_barrier_init();
-        *abort_flag = 0;
+        *abort_flag = (sb & 1023u) ? 1 : 0;  // (the swizzle needs 1024; else every wait gives up)
         prefetch_tmap(&tmc);
+        prefetch_tmap(&tmr);
     }
     if (warp == 5) {
         __syncwarp();
@@ -393,130 +393,144 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
     const int begin = uniform(st0.x), end = uniform(st1.x), n_pages = end - begin;
     Walk w;
     w.b = uniform(st0.y);
-    w.at = w.seg_begin = begin;
+    w.at = begin;
     w.page0 = uniform(st0.z);
-    w.seg_end = min(end, uniform(st0.w));
+    w.enter(p, end, uniform(st0.w));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
     if (warp == 4) {
-        // ================= copies: the queries of each sequence, and its pages ==============
+        // ===== copies into the ring: each sequence's queries, then its pages (the warp converged) ===
+        const bool lead = elect_one();
         bool ok = true;
-        int k = 0, seg = 0, issued = 0, q_issued = 0;  // issued: units, in order (lane 0)
-        while (ok && w.at < end) {
-            const int b = w.b, first = w.at - w.page0, n = w.seg_end - w.at;
-            if (seg > 0) ok = wait_or_abort(bar(SM::B_QFREE), (seg - 1) & 1, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(SM::B_QFULL), PAGE);
-                ++q_issued;
-                const uint8_t *src = p.q_img + ((size_t)b * p.n_groups + group) * PAGE;
+        int k = 0, issued = 0;  // items; units, in order
+        // item k; src: the queries' image, or NULL for page pg. The item's units go out in the order in
+        // which their slots come free, as many at a time as are free (lane v asks for the v-th)
+        auto issue = [&](const uint8_t *src, int pg) {
+            const int st = k % NS;
+            const bool good = src || (pg >= 0 && pg < p.n_pages);
+            int v = 0;
+            unsigned long long t0 = 0;
+            while (v < NU) {
+                uint32_t is_free = ~0u;
+                if (k >= NS)
+                    is_free = __ballot_sync(0xffffffffu, mbar_test_if(lane < NU, free_(st, (lane + NP) % NU),
+                                                                      ((k / NS) - 1) & 1) || lane >= NU);
+                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 2 * NP + 1; ++i)
-                    bulk_load(sb + SM::OFF_Q + i * kBlk, src + (size_t)i * kBlk, kBlk, bar(SM::B_QFULL));
-            }
-            int entry = -1;
-            for (int t = 0; t < n && ok; ++t, ++k) {
-                if ((t & 31) == 0)
-                    entry = t + lane < n ? p.page_table[(size_t)b * p.max_pages + first + t + lane] : -1;
-                const int pg = __shfl_sync(0xffffffffu, entry, t & 31);
-                const int st = k % NS;
-                const bool good = pg >= 0 && pg < p.n_pages;
-                if (lane == 0) {
-                    if (!good) atomicOr(&g_err, HMD_DEVERR_PAGE);
-#pragma unroll
-                    for (int v = 0; v < NU; ++v) {
-                        const int u = v == 0 ? NP : v - 1;  // the shared part is free first
-                        if (k >= NS) ok = wait_or_abort(free_(st, u), ((k / NS) - 1) & 1, abort_flag);
-                        if (!ok) break;
-                        if (u == 0) page_ok[st] = good;  // read by whoever waits for unit 0
-                        const uint32_t bytes = u == NP ? kBlk : 2 * kBlk;
-                        mbar_arrive_expect_tx(full(st, u), good ? bytes : 0);
-                        ++issued;
-                        if (!good) continue;
-                        const uint32_t dst = sb + SM::OFF_C + st * PAGE + u * 2 * kBlk;
-                        tma_load_2d(dst, &tmc, full(st, u), u * 128, pg * kPT);
-                        if (u < NP) tma_load_2d(dst + kBlk, &tmc, full(st, u), u * 128 + 64, pg * kPT);
-                    }
+                for (int e = 0; e < NU; ++e) {
+                    const int u = e == 0 ? NP : e - 1;  // the shared part's slot is free first
+                    if (e != v || !((is_free >> e) & 1u)) continue;
+                    const uint32_t dst = sb + st * PAGE + u * 2 * kBlk, bytes = u == NP ? kBlk : 2 * kBlk;
+                    if (u == 0) page_ok[st] = good;  // read by whoever waits for unit 0
+                    __syncwarp();
+                    mbar_expect_if(lead, full(st, u), good ? bytes : 0);
+                    if (src) bulk_load_if(lead, dst, src + (size_t)u * 2 * kBlk, bytes, full(st, u));
+                    else if (u < NP) tma_load_3d_if(lead && good, dst, &tmc, full(st, u), 0, pg * kPT, u * 2);
+                    else tma_load_2d_if(lead && good, dst, &tmr, full(st, u), NP * 128, pg * kPT);
+                    ++v;
+                    ++issued;
+                    t0 = 0;
                 }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                if (v < NU) {
+                    const unsigned long long now = globaltimer_ns();
+                    if (t0 == 0) t0 = now;
+                    const bool late = now - t0 > kWaitLimitNs;
+                    if (late) *abort_flag = 1;
+                    ok = !__any_sync(0xffffffffu, late || *abort_flag);
+                    if (!ok) return;
+                }
             }
-            w.at = w.seg_end;
-            ++seg;
-            if (w.at < end) w.seek(p, end);
+            if (!good && lead) atomicOr(&g_err, HMD_DEVERR_PAGE);
+        };
+        while (ok && w.at < end) {
+            const uint8_t *q = p.q_img + ((size_t)w.b * p.n_groups + group) * PAGE;
+            issue(q, 0);
+            ++k;
+            const int32_t *table = p.page_table + (size_t)w.b * p.max_pages - w.page0;
+            int next = table[w.at];
+            for (; w.at < w.seg_end && ok; ++w.at, ++k) {
+                const int pg = uniform(next);
+                if (w.at + 1 < w.seg_end) next = table[w.at + 1];
+                issue(nullptr, pg);
+            }
+            if (ok && w.at < end) w.seek(p, end);
         }
-        if (!ok && lane == 0) {
+        if (!ok && lead) {
             // the copies in flight land (bounded) before shared memory is released
             atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
             for (int i = max(0, issued - NS * NU); i < issued; ++i) {
-                const int pk = i / NU, v = i % NU;
-                (void)mbar_wait_bounded(full(pk % NS, v == 0 ? NP : v - 1), (pk / NS) & 1);
+                const int ki = i / NU, v = i % NU;
+                (void)mbar_wait_bounded(full(ki % NS, v == 0 ? NP : v - 1), (ki / NS) & 1);
             }
-            if (q_issued > 0) (void)mbar_wait_bounded(bar(SM::B_QFULL), (q_issued - 1) & 1);
         }
+        __syncwarp();
     } else if (warp == 5) {
         // ================= products, whichever is ready first (the warp converged) ===========
         const bool lead = elect_one();
-        const Desc d_q(smem_desc_sw128(sb + SM::OFF_Q, 16, 1024));
-        const Desc d_k(smem_desc_sw128(sb + SM::OFF_C, 16, 1024));    // keys x dims
-        const Desc d_v(smem_desc_sw128(sb + SM::OFF_C, kBlk, 1024));  // dims x keys
+        const Desc d_k(smem_desc_sw128(sb, 16, 1024));    // keys x dims
+        const Desc d_v(smem_desc_sw128(sb, kBlk, 1024));  // dims x keys
         const Desc d_p(smem_desc_sw128(sb + SM::OFF_P, 16, 1024));
-        constexpr uint32_t ID_S = idesc_bf16(64, 2 * kRows, 0, 0);
+        constexpr uint32_t ID_S = idesc_bf16(128, kPT, 0, 0);
         constexpr uint32_t ID_O = idesc_bf16(128, kRows, 1, 0);
-        int s = 0, pv = 0, seg = 0;
-        Walk ws = w, wp = w;  // the sequences of the next scores and of the next output product
+        int s = 0, pv = 0, seg = 0;  // pages of which the scores, the output product are issued
+        Walk ws = w, wp = w;         // their sequences
+        int ks = 1, kp = 1;          // their items in the ring: the queries come before a sequence's pages
         bool ok = true;
         unsigned long long t0 = 0;
         while (pv < n_pages) {
             bool moved = false;
-            if (pv < s && mbar_test_warp(lead, bar(SM::B_P + (pv & 1)), (pv >> 1) & 1)) {
-                // O^T += C^T P^T, unit by unit; each unit's page slot is free after it
+            if (pv < s && mbar_test_warp(lead, bar(SM::B_P), pv & 1)) {
+                // O^T += C^T P^T, unit by unit; each unit's slot is free after it
                 tc_fence_after();
-                if (wp.at == wp.seg_end) wp.seek(p, end);
-                const int st = pv % NS;
+                const int st = kp % NS;
                 const bool fresh = __all_sync(0xffffffffu, wp.at == wp.seg_begin);
-                const Desc v = d_v.at(st * PAGE), pt = d_p.at((pv & 1) * kRows * 128);
+                const Desc v = d_v.at(st * PAGE);
 #pragma unroll
                 for (int u = 0; u < NP; ++u) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         umma_if(lead, tmem + kTmemO + u * kRows, v.at(u * 2 * kBlk + kk * 2048),
-                                pt.at(kk * 32), ID_O, (fresh && kk == 0) ? 0u : 1u);
+                                d_p.at(kk * 32), ID_O, (fresh && kk == 0) ? 0u : 1u);
                     umma_commit_if(lead, free_(st, u));
                 }
-                umma_commit_if(lead, bar(SM::B_O + (pv & 1)));
-                ++wp.at;
+                umma_commit_if(lead, bar(SM::B_O));
+                ++kp;
                 ++pv;
+                if (__all_sync(0xffffffffu, ++wp.at == wp.seg_end && wp.at < end)) {
+                    wp.seek(p, end);
+                    ++kp;
+                }
                 moved = true;
             } else if (s < n_pages && s <= pv + 1) {
-                // S^T = C [q~hi ; q~lo]^T once the page (and a new sequence's queries) landed: lane u
-                // asks for unit u. The scores before last have been read: their output product is
-                // issued. (Unit by unit as they land, the questions cost more than the products.)
-                if (ws.at == ws.seg_end) ws.seek(p, end);
-                const int st = s % NS;
-                const bool asks = lane < NU || (lane == NU && ws.at == ws.seg_begin);
-                if (mbar_test_warp(asks, lane < NU ? full(st, lane) : bar(SM::B_QFULL),
-                                   (lane < NU ? s / NS : seg) & 1)) {
+                // S = [q~hi ; q~lo] C^T once the page has landed (lane u asks for unit u), the scores
+                // before have been read and, for a new sequence, its queries are in place
+                const int st = ks % NS;
+                const bool first = ws.at == ws.seg_begin;
+                const bool asks = lane < NU || (lane == NU && s > 0) || (lane == NU + 1 && first);
+                const uint32_t b = lane < NU ? full(st, lane) : lane == NU ? bar(SM::B_SR) : bar(SM::B_Q);
+                const uint32_t parity = lane < NU ? (ks / NS) & 1 : lane == NU ? (s - 1) & 1 : seg & 1;
+                if (mbar_test_warp(asks, b, parity)) {
                     tc_fence_after();
-                    const uint32_t d = tmem + kTmemS + (s & 1) * 64;
                     const Desc kd = d_k.at(st * PAGE);
 #pragma unroll
                     for (int v = 0; v < NU; ++v) {
                         const int u = v == 0 ? NP : v - 1;  // the shared part's slot is free first
 #pragma unroll
-                        for (int kk = 0; kk < (u == NP ? 4 : 8); ++kk) {
-                            const uint32_t off = u * 2 * kBlk + (kk >> 2) * kBlk + (kk & 3) * 32;
-                            umma_if(lead, d, kd.at(off), d_q.at(off), ID_S, (v > 0 || kk > 0) ? 1u : 0u);
-                        }
+                        for (int kk = 0; kk < (u == NP ? 4 : 8); ++kk)
+                            umma_ts_if(lead, tmem + kTmemS, tmem + kTmemQ + u * 64 + kk * 8,
+                                       kd.at(u * 2 * kBlk + (kk >> 2) * kBlk + (kk & 3) * 32), ID_S,
+                                       (v > 0 || kk > 0) ? 1u : 0u);
                         if (u == NP) umma_commit_if(lead, free_(st, NP));
                     }
-                    umma_commit_if(lead, bar(SM::B_S + (s & 1)));
+                    umma_commit_if(lead, bar(SM::B_S));
+                    ++ks;
                     ++s;
-                    if (__all_sync(0xffffffffu, ++ws.at == ws.seg_end)) {
-                        umma_commit_if(lead, bar(SM::B_QFREE));
+                    if (__all_sync(0xffffffffu, ++ws.at == ws.seg_end && ws.at < end)) {
+                        ws.seek(p, end);
+                        ++ks;
                         ++seg;
                     }
                     moved = true;
@@ -544,88 +558,124 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
         __syncwarp();
     } else {
         // ================= softmax and the partial results =====================================
+        // Warp 0 receives the rows' scores of q~hi (lane = row), warp 1 those of q~lo. They swap halves
+        // and each does the softmax of 32 of the page's keys; all four warps hold O^T (lane = latent
+        // dim of a unit).
         const bool lead = elect_one();
-        const int c0 = (lane & 3) * 2;  // this thread's columns: 8j + c0, 8j + c0 + 1, j < 4
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        float *hi_x = reinterpret_cast<float *>(sm + SM::OFF_HI) + lane;        // [key - 32][row]
+        uint32_t *lo_x = reinterpret_cast<uint32_t *>(sm + SM::OFF_LO) + lane;  // [key pair][row]
         bool ok = true;
-        int k = 0;
+        int item = 0, k = 0;  // ring items, pages
         while (ok && w.at < end) {
-            const int b = w.b, L = p.seq_lens[b], page0 = w.page0;
-            // the last position each of this thread's rows sees (-1: no such row)
-            int last[8];
-            float base[8], l[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int r = group * kRows + (j >> 1) * 8 + c0 + (j & 1);
-                last[j] = r < p.nq * p.H ? L - p.nq + r / p.H : -1;
-                base[j] = -INFINITY;
-                l[j] = 0.f;
-            }
-            for (; w.at < w.seg_end; ++w.at, ++k) {
-                const int st = k % NS, pos0 = (w.at - page0) * kPT;
-                // the scores (their completion implies the earlier products', so P's tile of two
-                // pages ago has been read) and, for page_ok, the page
-                ok = wait_warp(lane < 2, lane ? full(st, 0) : bar(SM::B_S + (k & 1)),
-                                        (lane ? k / NS : k >> 1) & 1, abort_flag);
-                tc_fence_after();
-                float s[16];  // [j][e]: column 8j + c0 + e % 2, key 16 warp + lane / 4 + 8 (e / 2)
-                {
+            const int b = w.b, L = w.L, page0 = w.page0;
+            if (warp < 2) {
+                // this sequence's queries to TMEM: lane = row of the image (32 hi, then 32 lo). The
+                // scores of the sequence before are complete, so its queries are not read any more
+                const int st = item % NS;
+                ok &= wait_warp(lane < NU, full(st, min(lane, NP)), (item / NS) & 1, abort_flag);
+                const uint8_t *row = sm + st * PAGE + (warp * 32 + lane) * 128;
+#pragma unroll 1
+                for (int c = 0; c < 2 * NP + 1; ++c) {
                     uint32_t r[32];
-                    tmem_ld_16x256b_x8(tmem + kTmemS + (k & 1) * 64 + lanes, r);
-                    tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            s[4 * j + e] = __uint_as_float(r[4 * j + e]) + __uint_as_float(r[16 + 4 * j + e]);
+                    for (int e = 0; e < 8; ++e) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(row + c * kBlk + ((e ^ (lane & 7)) << 4));
+                        r[4 * e] = x.x; r[4 * e + 1] = x.y; r[4 * e + 2] = x.z; r[4 * e + 3] = x.w;
+                    }
+                    tmem_st32(tmem + kTmemQ + c * 32 + lanes, r);
                 }
-                const bool good = page_ok[st] != 0;
-                const int key0 = pos0 + warp * 16 + (lane >> 2);
+                tmem_wait_st();
+                tc_fence_before();
+                fence_proxy_async_smem();  // the slot's next filling comes after these reads
+                bar_scores();
+                if (warp == 0 && lane < NU) mbar_arrive(free_(st, lane));
+                if (lane == 0) mbar_arrive(bar(SM::B_Q));
+            }
+            ++item;
+            // the last position this row sees (-1: no such row)
+            const int r_row = group * kRows + lane;
+            const int last = r_row < p.nq * p.H ? L - p.nq + r_row / p.H : -1;
+            float base = -INFINITY, l = 0.f;
+            for (; w.at < w.seg_end; ++w.at, ++k, ++item) {
+                const int st = item % NS, pos0 = (w.at - page0) * kPT;
+                float x[32], mx = -INFINITY;
                 bool grew = false;
-                if (!good || pos0 + kPT > L - p.nq + 1 || (group + 1) * kRows > p.nq * p.H) {
+                if (warp < 2) {
+                    // the scores and, for page_ok, the page
+                    ok &= wait_warp(lane < 2, lane ? full(st, 0) : bar(SM::B_S),
+                                    (lane ? item / NS : k) & 1, abort_flag);
+                    tc_fence_after();
+                    {
+                        uint32_t r[64];
+                        tmem_ld64(tmem + kTmemS + lanes, r);
+                        tmem_wait_ld();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(SM::B_SR));
+                        if (warp == 0) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                            for (int j = 0; j < 32; ++j) {
+                                hi_x[j * kRows] = __uint_as_float(r[32 + j]);
+                                x[j] = __uint_as_float(r[j]);
+                            }
+                        } else {
+                            // a low score is below 2^-8 of its row's: bf16 keeps it to 2^-17 of that
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!good || key0 + 8 * (e >> 1) > last[2 * j + (e & 1)]) s[4 * j + e] = -INFINITY;
+                            for (int j = 0; j < 16; ++j)
+                                lo_x[j * kRows] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[32 + j]);
+                        }
+                    }
+                    bar_scores();
+                    if (warp == 0) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const uint32_t v = lo_x[j * kRows];
+                            x[2 * j] += bf16_lo(v);
+                            x[2 * j + 1] += bf16_hi(v);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] += hi_x[j * kRows];
+                    }
+                    const bool good = page_ok[st] != 0;
+                    if (!good || pos0 + kPT > L - p.nq + 1 || (group + 1) * kRows > p.nq * p.H) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!good || pos0 + 32 * warp + j > last) x[j] = -INFINITY;
+                    }
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        m4[0] = max3(m4[0], x[j], x[j + 1]);
+                        m4[1] = max3(m4[1], x[j + 2], x[j + 3]);
+                        m4[2] = max3(m4[2], x[j + 4], x[j + 5]);
+                        m4[3] = max3(m4[3], x[j + 6], x[j + 7]);
+                    }
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    grew = mx > base + kLazy;
+                    s_mx[warp][lane] = mx;
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) grew |= s[4 * j + e] > base[2 * j + (e & 1)] + kLazy;
                 if (bar_softmax_or(grew || !ok)) {
                     ok = !bar_softmax_or(!ok);
                     if (!ok) break;
-                    // some row outgrew its base: every row's new base is the maximum so far
-                    float mx[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        mx[j] = fmaxf(s[4 * (j >> 1) + (j & 1)], s[4 * (j >> 1) + (j & 1) + 2]);
-#pragma unroll
-                        for (int off = 4; off < 32; off <<= 1)
-                            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], off));
-                        if (lane < 4) s_red[warp][(j >> 1) * 8 + c0 + (j & 1)] = mx[j];
+                    if (warp < 2) {
+                        // a row that outgrew its base moves it to the maximum of both halves
+                        mx = fmaxf(mx, s_mx[warp ^ 1][lane]);
+                        float f = 1.f;
+                        if (mx > base + kLazy) {
+                            f = exp2f(base - mx);
+                            base = mx;
+                            l *= f;
+                        }
+                        if (warp == 0) s_f[lane] = f;
                     }
                     bar_softmax();
-                    float f[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int c = (j >> 1) * 8 + c0 + (j & 1);
-                        const float m = fmaxf(fmaxf(fmaxf(s_red[0][c], s_red[1][c]),
-                                                    fmaxf(s_red[2][c], s_red[3][c])), base[j]);
-                        f[j] = m == -INFINITY ? 1.f : exp2f(base[j] - m);
-                        base[j] = m;
-                        l[j] *= f[j];
-                    }
                     if (w.at > w.seg_begin) {
-                        bar_softmax();  // the maxima have been read: their place takes the factors
-                        if (warp == 0 && lane < 4)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) s_red[0][(j >> 1) * 8 + c0 + (j & 1)] = f[j];
-                        bar_softmax();
-                        ok = wait_warp(lead, bar(SM::B_O + ((k - 1) & 1)), ((k - 1) >> 1) & 1, abort_flag);
-                        ok = !bar_softmax_or(!ok);
-                        if (!ok) break;
+                        // the earlier output to the new bases, once the product into it is done
+                        ok = wait_warp(lead, bar(SM::B_O), (k - 1) & 1, abort_flag);
                         tc_fence_after();
 #pragma unroll 1
                         for (int u = 0; u < NP; ++u) {
@@ -634,53 +684,51 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
                             tmem_wait_ld();
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                r[c] = __float_as_uint(__uint_as_float(r[c]) * s_red[0][c]);
+                                r[c] = __float_as_uint(__uint_as_float(r[c]) * s_f[c]);
                             tmem_st32(tmem + kTmemO + u * kRows + lanes, r);
                         }
                         tmem_wait_st();
                     }
-                    bar_softmax();  // s_red is free again
+                    bar_softmax();  // s_f and s_mx are free again
                 }
-                uint32_t pk[8];  // [j][key half]: two columns of one key
+                if (warp < 2) {
+                    const float m = base == -INFINITY ? 0.f : base;
+                    uint32_t pk[16];
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float m0 = base[2 * j] == -INFINITY ? 0.f : base[2 * j];
-                    const float m1 = base[2 * j + 1] == -INFINITY ? 0.f : base[2 * j + 1];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float p0 = ex2_approx(s[4 * j + 2 * e] - m0);
-                        const float p1 = ex2_approx(s[4 * j + 2 * e + 1] - m1);
-                        l[2 * j] += p0;
-                        l[2 * j + 1] += p1;
-                        pk[2 * j + e] = pack_bf16x2(p0, p1);
+                    for (int j = 0; j < 16; ++j) {
+                        const float p0 = ex2_approx(x[2 * j] - m), p1 = ex2_approx(x[2 * j + 1] - m);
+                        sum[(2 * j) & 3] += p0;
+                        sum[(2 * j + 1) & 3] += p1;
+                        pk[j] = pack_bf16x2(p0, p1);
                     }
-                }
-                // P^T [32 rows][64 keys], rows of 128 bytes, 128-byte swizzle
-                const uint32_t pt = sb + SM::OFF_P + (k & 1) * kRows * 128;
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    // P [32 rows][64 keys], rows of 128 bytes, 128-byte swizzle, once the product
+                    // before has read it
+                    if (k > 0) ok &= wait_warp(lead, bar(SM::B_O), (k - 1) & 1, abort_flag);
+                    uint8_t *row = sm + SM::OFF_P + lane * 128;
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    const int row = 8 * (2 * jj + (lane >> 4)) + (lane & 7);
-                    stmatrix_x4_trans(pt + blk_off(row, (2 * warp + ((lane >> 3) & 1)) * 8), pk[4 * jj],
-                                      pk[4 * jj + 1], pk[4 * jj + 2], pk[4 * jj + 3]);
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4 *>(row + (((4 * warp + e) ^ (lane & 7)) << 4)) =
+                            make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
                 }
-                if (!good || pos0 + kPT > L) {
+                if (!page_ok[st] || pos0 + kPT > L) {
                     // rows behind the sequence (or of a page that was not copied) hold anything: as
                     // values they are zeroed before the output product reads them
-                    const int n_ok = good ? L - pos0 : 0;
+                    const int n_ok = page_ok[st] ? L - pos0 : 0;
                     for (int idx = tid; idx < (kPT - n_ok) * NP * 16; idx += 128) {
                         const int row = n_ok + idx / (NP * 16), ch = idx % (NP * 16);
-                        *reinterpret_cast<uint4 *>(sm + SM::OFF_C + st * PAGE + (ch >> 3) * kBlk +
+                        *reinterpret_cast<uint4 *>(sm + st * PAGE + (ch >> 3) * kBlk +
                                                    blk_off(row, (ch & 7) * 8)) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(SM::B_P + (k & 1)));
+                if (lane == 0) mbar_arrive(bar(SM::B_P));
             }
             const size_t piece = part_index(p, range, b, group);
-            float *ml = p.part_ml + piece * kRows * 2;
-            if (ok) ok = wait_warp(lead, bar(SM::B_O + ((k - 1) & 1)), ((k - 1) >> 1) & 1, abort_flag);
+            if (ok) ok = wait_warp(lead, bar(SM::B_O), (k - 1) & 1, abort_flag);
             ok = !bar_softmax_or(!ok);
             if (!ok) {
                 // this piece and the range's later ones are marked as missing
@@ -703,22 +751,11 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
                 for (int c = 0; c < 32; ++c) dst[(size_t)c * p.dc + u * 128] = __uint_as_float(r[c]);
             }
             tc_fence_before();
-            // sums of the keys over the lanes that share a column, then over the warps
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], off);
-                if (lane < 4) s_red[warp][(j >> 1) * 8 + c0 + (j & 1)] = l[j];
-            }
+            if (warp == 1) s_mx[1][lane] = l;
             bar_softmax();
-            if (warp == 0 && lane < 4) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = (j >> 1) * 8 + c0 + (j & 1);
-                    ml[2 * c] = base[j];
-                    ml[2 * c + 1] = (s_red[0][c] + s_red[1][c]) + (s_red[2][c] + s_red[3][c]);
-                }
-            }
+            if (warp == 0)
+                *reinterpret_cast<float2 *>(p.part_ml + (piece * kRows + lane) * 2) =
+                    make_float2(base, l + s_mx[1][lane]);
             bar_softmax();
             if (w.at < end) w.seek(p, end);
         }
@@ -736,61 +773,60 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const LatentParams
 // ---- kernel 3 ----------------------------------------------------------------------------------
 constexpr int kExpThreads = 512;
 constexpr int kExpWarps = kExpThreads / 32;
-constexpr int kExpTok = 16;  // tokens (b, i) per cluster
-template <int D>
+// Up to TOK tokens (b, i) of one head per CTA, d_c = 128 * NP latent dims.
+template <int D, int NP, int TOK>
 struct ExpSmem {
-    static constexpr int WP = 128 + 8;  // pitch (elements) without bank conflicts
-    __nv_bfloat16 w[D][WP];             // W_uv[h][v][this CTA's 128 dims]
-    __nv_bfloat16 hi[kExpTok][WP], lo[kExpTok][WP];
-    float red[kExpWarps][128];          // a row's partial sums, per warp
-    float out[kExpTok][D];              // this CTA's part of the output
+    static constexpr int WP = NP * 128 + 8;  // pitch (elements) without bank conflicts
+    __nv_bfloat16 w[D][WP];                  // W_uv[h]
+    __nv_bfloat16 hi[TOK][WP], lo[TOK][WP];  // the merged latent output as a bf16 pair
     float den[kExpWarps];
+    uint64_t bar;
+    uint32_t missing;                        // tokens of which a range gave up
+    // A token's sums, per warp that shares it: over hi and lo, which are written after them (warps
+    // share a token only where all tokens are merged at once).
+    static_assert(2 * TOK * WP * 2 >= kExpWarps * NP * 128 * 4, "the sums fit");
+    __device__ float (*red())[NP * 128] { return reinterpret_cast<float(*)[NP * 128]>(&hi[0][0]); }
 };
+static_assert(sizeof(ExpSmem<128, 4, 32>) <= 232448, "shared memory per CTA");
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
-    uint32_t remote;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
-    return v;
-}
-
-// Grid (d_c / 128, H, token blocks), clusters along x.
-template <int D>
-__global__ void __launch_bounds__(kExpThreads) latent_expand_kernel(const LatentParams p) {
+template <int D, int NP, int TOK>
+__global__ void __launch_bounds__(kExpThreads, 1) latent_expand_kernel(const LatentParams p, int tokens) {
+    using SM = ExpSmem<D, NP, TOK>;
+    constexpr int DC = NP * 128, kFlight = NP > 2 ? 3 : 4;
     extern __shared__ __align__(16) uint8_t exp_smem[];
-    ExpSmem<D> &sm = *reinterpret_cast<ExpSmem<D> *>(exp_smem);
+    SM &sm = *reinterpret_cast<SM *>(exp_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int cc = blockIdx.x, h = blockIdx.y, tok0 = blockIdx.z * kExpTok;
-    const int n_cols = p.dc / 128, rows = min(kExpTok, p.B * p.nq - tok0);
+    const int h = blockIdx.x, tok0 = blockIdx.y * tokens, rows = min(tokens, p.B * p.nq - tok0);
+    const uint32_t bar = smem_u32(&sm.bar);
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_barrier_init();
+        sm.missing = 0;
+    }
     griddep_launch_dependents();
     griddep_wait();
-    const __nv_bfloat16 *wv = p.w_uv + h * p.w_uv_head + cc * 128;
-    for (int idx = tid; idx < D * 16; idx += kExpThreads) {
-        const int v = idx >> 4, c = (idx & 15) * 8;
-        cp_async16(smem_u32(&sm.w[v][c]), wv + (size_t)v * p.dc + c);  // lands during the merge
+    __syncthreads();
+    if (warp == kExpWarps - 1) {
+        // W_uv[h] lands during the merge, a bulk copy per row
+        if (lane == 0) mbar_arrive_expect_tx(bar, D * DC * 2);
+        __syncwarp();
+        const __nv_bfloat16 *w = p.w_uv + h * p.w_uv_head;
+        for (int v = lane; v < D; v += 32) bulk_load(smem_u32(&sm.w[v][0]), w + (size_t)v * DC, DC * 2, bar);
     }
-    // merge the ranges: `wpr` warps share a token's ranges, lanes its 128 dims (4 each)
+    // merge the ranges: `wpr` warps share a token's ranges, a lane has 4 dims of every 128
     const int wpr = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;
-    uint32_t missing = 0;  // tokens of which a range gave up
     for (int r0 = 0; r0 < rows; r0 += kExpWarps / wpr) {
         const int r = r0 + warp / wpr, part = warp % wpr;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float M = -INFINITY, den = 0.f;
-        bool lost = false;
+        float4 acc[NP];
+#pragma unroll
+        for (int u = 0; u < NP; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.f;
         if (r < rows) {
             const int tok = tok0 + r, b = tok / p.nq, row = (tok - b * p.nq) * p.H + h;
             const int2 range = p.ranges[b];
-            const int i0 = range.x, i1 = range.y;
-            const int g = row / kRows, c = row % kRows;
+            const int i0 = range.x, i1 = range.y, g = row / kRows, c = row % kRows;
+            float M = -INFINITY;
+            bool lost = false;
             for (int i = i0 + lane; i < i1; i += 32) {
                 const float2 v = *reinterpret_cast<const float2 *>(
                     p.part_ml + (part_index(p, i, b, g) * kRows + c) * 2);
@@ -800,86 +836,103 @@ __global__ void __launch_bounds__(kExpThreads) latent_expand_kernel(const Latent
 #pragma unroll
             for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
             lost = __any_sync(0xffffffffu, lost);
-            if (!lost && M != -INFINITY) {
-#pragma unroll 8
-                for (int i = i0 + part; i < i1; i += wpr) {
-                    const size_t at = part_index(p, i, b, g) * kRows + c;
-                    const float2 v = *reinterpret_cast<const float2 *>(p.part_ml + at * 2);
-                    const float4 x = *reinterpret_cast<const float4 *>(p.part_o + at * p.dc + cc * 128 + lane * 4);
-                    const float f = exp2f(v.x - M);
-                    den += f * v.y;
-                    acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
+            if (lost && lane == 0) atomicOr(&sm.missing, 1u << r);
+            if (M != -INFINITY) {
+                for (int i = i0 + part; i < i1; i += kFlight * wpr) {  // kFlight ranges' loads in flight
+                    float2 v[kFlight];
+                    float4 x[kFlight][NP];
+#pragma unroll
+                    for (int e = 0; e < kFlight; ++e) {
+                        const int ie = i + e * wpr;
+                        if (ie < i1) {
+                            const size_t at = part_index(p, ie, b, g) * kRows + c;
+                            v[e] = *reinterpret_cast<const float2 *>(p.part_ml + at * 2);
+#pragma unroll
+                            for (int u = 0; u < NP; ++u)
+                                x[e][u] = *reinterpret_cast<const float4 *>(p.part_o + at * DC + u * 128 + lane * 4);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < kFlight; ++e) {
+                        if (i + e * wpr < i1) {
+                            const float f = exp2f(v[e].x - M);
+                            den += f * v[e].y;
+#pragma unroll
+                            for (int u = 0; u < NP; ++u) {
+                                acc[u].x += f * x[e][u].x; acc[u].y += f * x[e][u].y;
+                                acc[u].z += f * x[e][u].z; acc[u].w += f * x[e][u].w;
+                            }
+                        }
+                    }
                 }
             }
         }
         if (wpr > 1) {
-            *reinterpret_cast<float4 *>(&sm.red[warp][lane * 4]) = acc;
+#pragma unroll
+            for (int u = 0; u < NP; ++u) *reinterpret_cast<float4 *>(&sm.red()[warp][u * 128 + lane * 4]) = acc[u];
             if (lane == 0) sm.den[warp] = den;
             __syncthreads();
             if (part == 0)
                 for (int v = 1; v < wpr; ++v) {
-                    const float4 x = *reinterpret_cast<const float4 *>(&sm.red[warp + v][lane * 4]);
-                    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+#pragma unroll
+                    for (int u = 0; u < NP; ++u) {
+                        const float4 x = *reinterpret_cast<const float4 *>(&sm.red()[warp + v][u * 128 + lane * 4]);
+                        acc[u].x += x.x; acc[u].y += x.y; acc[u].z += x.z; acc[u].w += x.w;
+                    }
                     den += sm.den[warp + v];
                 }
             __syncthreads();
         }
         if (part == 0 && r < rows) {
             const float inv = den > 0.f ? 1.f / den : 0.f;
-            const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-            const uint32_t h0 = pack_bf16x2(x[0], x[1]), h1 = pack_bf16x2(x[2], x[3]);
-            *reinterpret_cast<uint2 *>(&sm.hi[r][lane * 4]) = make_uint2(h0, h1);
-            *reinterpret_cast<uint2 *>(&sm.lo[r][lane * 4]) =
-                make_uint2(pack_bf16x2(x[0] - bf16_lo(h0), x[1] - bf16_hi(h0)),
-                           pack_bf16x2(x[2] - bf16_lo(h1), x[3] - bf16_hi(h1)));
-        }
-        if (r < rows && lost) missing |= 1u << r;
-    }
-    for (int r = rows + warp; r < kExpTok; r += kExpWarps) {  // rows without a token
-        *reinterpret_cast<uint2 *>(&sm.hi[r][lane * 4]) = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2 *>(&sm.lo[r][lane * 4]) = make_uint2(0u, 0u);
-    }
-    // a warp knows the losses of the tokens it merged; the output needs all of them
-    __shared__ uint32_t s_missing;
-    if (tid == 0) s_missing = 0;
-    cp_async_wait_all();
-    __syncthreads();
-    if (lane == 0 && missing) atomicOr(&s_missing, missing);
-    // out[16 tokens][D] = latent output x W_uv^T over this CTA's dims; a warp takes 8 columns
-    if (warp < D / 8) {
-        float acc[4] = {};
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
+            for (int u = 0; u < NP; ++u) {
+                const float x[4] = {acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv};
+                const uint32_t h0 = pack_bf16x2(x[0], x[1]), h1 = pack_bf16x2(x[2], x[3]);
+                *reinterpret_cast<uint2 *>(&sm.hi[r][u * 128 + lane * 4]) = make_uint2(h0, h1);
+                *reinterpret_cast<uint2 *>(&sm.lo[r][u * 128 + lane * 4]) =
+                    make_uint2(pack_bf16x2(x[0] - bf16_lo(h0), x[1] - bf16_hi(h0)),
+                               pack_bf16x2(x[2] - bf16_lo(h1), x[3] - bf16_hi(h1)));
+            }
+        }
+    }
+    for (int r = rows + warp; r < TOK; r += kExpWarps) {  // rows without a token
+#pragma unroll
+        for (int u = 0; u < NP; ++u) {
+            *reinterpret_cast<uint2 *>(&sm.hi[r][u * 128 + lane * 4]) = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2 *>(&sm.lo[r][u * 128 + lane * 4]) = make_uint2(0u, 0u);
+        }
+    }
+    const bool ok = mbar_wait_bounded(bar, 0);
+    if (__syncthreads_or(!ok)) {
+        if (tid == 0) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+        return;
+    }
+    // out[TOK][D] = latent output x W_uv^T: a warp has 8 columns and 16 tokens, or (D = 64, 16 tokens)
+    // half of the warps do
+    constexpr int CT = D / 8, RT = TOK / 16;  // column and row tiles
+    for (int t = warp; t < CT * RT; t += kExpWarps) {
+        const int ct = t % CT, rt = t / CT;
+        float a0[4] = {}, a1[4] = {};
+#pragma unroll 8
+        for (int kk = 0; kk < DC / 16; ++kk) {
             uint32_t ah[4], al[4];
-            ldmatrix_x4(smem_u32(&sm.hi[lane & 15][kk * 16 + (lane >> 4) * 8]), ah[0], ah[1], ah[2], ah[3]);
-            ldmatrix_x4(smem_u32(&sm.lo[lane & 15][kk * 16 + (lane >> 4) * 8]), al[0], al[1], al[2], al[3]);
-            const __nv_bfloat16 *wr = &sm.w[warp * 8 + (lane >> 2)][kk * 16 + (lane & 3) * 2];
+            ldmatrix_x4(smem_u32(&sm.hi[rt * 16 + (lane & 15)][kk * 16 + (lane >> 4) * 8]), ah[0], ah[1], ah[2], ah[3]);
+            ldmatrix_x4(smem_u32(&sm.lo[rt * 16 + (lane & 15)][kk * 16 + (lane >> 4) * 8]), al[0], al[1], al[2], al[3]);
+            const __nv_bfloat16 *wr = &sm.w[ct * 8 + (lane >> 2)][kk * 16 + (lane & 3) * 2];
             const uint32_t b0 = *reinterpret_cast<const uint32_t *>(wr);
             const uint32_t b1 = *reinterpret_cast<const uint32_t *>(wr + 8);
-            mma_bf16_16816(acc, ah, b0, b1);
-            mma_bf16_16816(acc, al, b0, b1);
+            mma_bf16_16816(a0, ah, b0, b1);
+            mma_bf16_16816(a1, al, b0, b1);
         }
-        const int v = warp * 8 + (lane & 3) * 2;
-        *reinterpret_cast<float2 *>(&sm.out[lane >> 2][v]) = make_float2(acc[0], acc[1]);
-        *reinterpret_cast<float2 *>(&sm.out[(lane >> 2) + 8][v]) = make_float2(acc[2], acc[3]);
-    }
-    cluster_sync_all();
-    // every CTA of the cluster finishes a share of the elements, adding the parts in rank order
-    const uint32_t me = cluster_rank();
-    for (int idx = (int)me * kExpThreads + tid; idx < rows * (D / 2); idx += n_cols * kExpThreads) {
-        const int r = idx / (D / 2), v = idx % (D / 2) * 2;
-        if ((s_missing >> r) & 1u) continue;  // o stays as it was
-        float y[4][2];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            y[c][0] = c < n_cols ? ld_cluster_f32(smem_u32(&sm.out[r][v]), c) : 0.f;
-            y[c][1] = c < n_cols ? ld_cluster_f32(smem_u32(&sm.out[r][v + 1]), c) : 0.f;
+        for (int e = 0; e < 2; ++e) {
+            const int r = rt * 16 + (lane >> 2) + 8 * e;
+            if (r < rows && !((sm.missing >> r) & 1u))  // else o stays as it was
+                *reinterpret_cast<uint32_t *>(p.o + ((size_t)(tok0 + r) * p.H + h) * D + ct * 8 + (lane & 3) * 2) =
+                    pack_bf16x2(a0[2 * e] + a1[2 * e], a0[2 * e + 1] + a1[2 * e + 1]);
         }
-        const float x0 = ((y[0][0] + y[1][0]) + y[2][0]) + y[3][0];
-        const float x1 = ((y[0][1] + y[1][1]) + y[2][1]) + y[3][1];
-        *reinterpret_cast<uint32_t *>(p.o + ((size_t)(tok0 + r) * p.H + h) * D + v) = pack_bf16x2(x0, x1);
     }
-    cluster_sync_all();  // nobody leaves while its part is still read
 }
 
 // ---- host side ---------------------------------------------------------------------------------
@@ -915,15 +968,16 @@ Plan make_plan(int nq, int B, int H, int dc, int max_seq_len) {
 }
 
 template <int NP>
-cudaError_t launch_attend(const CUtensorMap &tm, const LatentParams &p, cudaStream_t s) {
-    constexpr int smem = (int)AttSmem<NP>::ALLOC + 1024;
+cudaError_t launch_attend(const CUtensorMap &tmc, const CUtensorMap &tmr, const LatentParams &p,
+                          cudaStream_t s) {
+    constexpr int smem = (int)AttSmem<NP>::ALLOC;
     const cudaError_t e = once_per_device([] {
         return cudaFuncSetAttribute(latent_attend_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)AttSmem<NP>::ALLOC + 1024);
+                                    (int)AttSmem<NP>::ALLOC);
     });
     if (e != cudaSuccess) return e;
     return launch_pdl(latent_attend_kernel<NP>, dim3((unsigned)(p.n_ranges * p.n_groups)),
-                      dim3(kAttThreads), smem, s, tm, p);
+                      dim3(kAttThreads), smem, s, tmc, tmr, p);
 }
 
 template <int D>
@@ -939,29 +993,33 @@ cudaError_t launch_absorb(const LatentParams &p, cudaStream_t s) {
                       dim3(kAbsThreads), sizeof(AbsSmem<D>), s, p);
 }
 
-template <int D>
-cudaError_t launch_expand(const LatentParams &p, cudaStream_t s) {
+template <int D, int NP, int TOK>
+cudaError_t launch_expand_t(const LatentParams &p, int tokens, cudaStream_t s) {
     const cudaError_t e = once_per_device([] {
-        return cudaFuncSetAttribute(latent_expand_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)sizeof(ExpSmem<D>));
+        return cudaFuncSetAttribute(latent_expand_kernel<D, NP, TOK>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)sizeof(ExpSmem<D, NP, TOK>));
     });
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.dc / 128), (unsigned)p.H,
-                       (unsigned)((p.B * p.nq + kExpTok - 1) / kExpTok));
-    cfg.blockDim = dim3(kExpThreads);
-    cfg.dynamicSmemBytes = sizeof(ExpSmem<D>);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)(p.dc / 128);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, latent_expand_kernel<D>, p);
+    return launch_pdl(latent_expand_kernel<D, NP, TOK>,
+                      dim3((unsigned)p.H, (unsigned)((p.B * p.nq + tokens - 1) / tokens)),
+                      dim3(kExpThreads), sizeof(ExpSmem<D, NP, TOK>), s, p, tokens);
+}
+// The fewest tokens a CTA (each reads all of W_uv[h]) with which the grid has at most one CTA per SM.
+template <int D, int NP>
+cudaError_t launch_expand_np(const LatentParams &p, cudaStream_t s) {
+    int tokens = 4;
+    while (tokens < 32 && (long long)p.H * ((p.B * p.nq + tokens - 1) / tokens) > device_sms()) tokens *= 2;
+    return tokens > 16 ? launch_expand_t<D, NP, 32>(p, tokens, s) : launch_expand_t<D, NP, 16>(p, tokens, s);
+}
+template <int D>
+cudaError_t launch_expand(const LatentParams &p, cudaStream_t s) {
+    switch (p.dc / 128) {
+        case 1: return launch_expand_np<D, 1>(p, s);
+        case 2: return launch_expand_np<D, 2>(p, s);
+        case 3: return launch_expand_np<D, 3>(p, s);
+        default: return launch_expand_np<D, 4>(p, s);
+    }
 }
 
 }  // namespace
@@ -977,8 +1035,12 @@ size_t latent_decode_ws_bytes(int nq, int B, int H, int d_c, int max_seq_len) {
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t s) {
     const Plan pl = make_plan(a.nq, a.B, a.H, a.d_c, a.max_seq_len);
-    CUtensorMap tm;
-    if (!make_tmap_pool_sw128(&tm, a.pool, a.n_pages, 1, a.d_c + kDR)) return cudaErrorInvalidValue;
+    // c in units of 128 dims, two column blocks a box, and the shared part
+    CUtensorMap tmc, tmr;
+    if (!make_tmap_colblocks_sw128(&tmc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.pool, (long long)a.n_pages * kPT,
+                                   a.d_c + kDR, a.d_c / 64, kPT, 2) ||
+        !make_tmap_pool_sw128(&tmr, a.pool, a.n_pages, 1, a.d_c + kDR))
+        return cudaErrorInvalidValue;
     LatentParams p{};
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.new_c = static_cast<const __nv_bfloat16 *>(a.new_c);
@@ -1002,10 +1064,10 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t s) {
     cudaError_t e = a.d == 128 ? launch_absorb<128>(p, s) : launch_absorb<64>(p, s);
     if (e != cudaSuccess) return e;
     switch (a.d_c / 128) {
-        case 1: e = launch_attend<1>(tm, p, s); break;
-        case 2: e = launch_attend<2>(tm, p, s); break;
-        case 3: e = launch_attend<3>(tm, p, s); break;
-        default: e = launch_attend<4>(tm, p, s); break;
+        case 1: e = launch_attend<1>(tmc, tmr, p, s); break;
+        case 2: e = launch_attend<2>(tmc, tmr, p, s); break;
+        case 3: e = launch_attend<3>(tmc, tmr, p, s); break;
+        default: e = launch_attend<4>(tmc, tmr, p, s); break;
     }
     if (e != cudaSuccess) return e;
     return a.d == 128 ? launch_expand<128>(p, s) : launch_expand<64>(p, s);

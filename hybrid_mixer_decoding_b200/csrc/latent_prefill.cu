@@ -183,41 +183,39 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
     if (warp == 4) {
-        if (lane == 0) {
-            // the tile's two pages of latent rows: blocks of 64 dims (a missing page's rows hold
-            // anything; their results are stored as zeros)
-            int pg[2];
-            uint32_t bytes = 0;
-            for (int h = 0; h < 2; ++h) {
-                pg[h] = pos0 + h * kPT < s.total ? page_of(p, b, pos0 + h * kPT) : -1;
-                if (pg[h] >= 0) bytes += n_kc * (kBlk / 2);
-            }
-            mbar_arrive_expect_tx(bar(SM::B_A), bytes);
+        const bool lead = elect_one();
+        // the tile's two pages of latent rows: blocks of 64 dims (a missing page's rows hold anything;
+        // their results are stored as zeros)
+        int pg[2];
+        uint32_t bytes = 0;
+        for (int h = 0; h < 2; ++h) {
+            pg[h] = uniform(pos0 + h * kPT < s.total ? page_of(p, b, pos0 + h * kPT) : -1);
+            if (pg[h] >= 0) bytes += n_kc * (kBlk / 2);
+        }
+        mbar_expect_if(lead, bar(SM::B_A), bytes);
+        for (int kc = 0; kc < n_kc; ++kc)
             for (int h = 0; h < 2; ++h)
-                if (pg[h] >= 0)
-                    for (int kc = 0; kc < n_kc; ++kc)
-                        tma_load_2d(sb + SM::OFF_A + kc * kBlk + h * (kBlk / 2), &tmc, bar(SM::B_A),
-                                    kc * 64, pg[h] * kPT);
-            bool ok = true;
-            int n = 0;
-            for (int st = 0; st < n_steps && ok; ++st) {
-                for (int kc = 0; kc < n_kc; ++kc, ++n) {
-                    const int w = n % SM::NW;
-                    if (n >= SM::NW) ok = wait_or_abort(bar(SM::B_WFREE + w), (n / SM::NW - 1) & 1, abort_flag);
-                    if (!ok) break;
-                    const uint32_t dst = sb + SM::OFF_W + w * SM::W_STAGE;
-                    mbar_arrive_expect_tx(bar(SM::B_WFULL + w), SM::W_STAGE);
-                    tma_load_3d(dst, &tmk, bar(SM::B_WFULL + w), kc * 64, 0, p.h0 + ha + st);
-                    tma_load_3d(dst + D * 128, &tmv, bar(SM::B_WFULL + w), kc * 64, 0, p.h0 + ha + st);
-                }
+                tma_load_2d_if(lead && pg[h] >= 0, sb + SM::OFF_A + kc * kBlk + h * (kBlk / 2), &tmc,
+                               bar(SM::B_A), kc * 64, pg[h] * kPT);
+        bool ok = true;
+        int n = 0;
+        for (int st = 0; st < n_steps && ok; ++st) {
+            for (int kc = 0; kc < n_kc; ++kc, ++n) {
+                const int w = n % SM::NW;
+                if (n >= SM::NW) ok = wait_warp(lead, bar(SM::B_WFREE + w), (n / SM::NW - 1) & 1, abort_flag);
+                if (!ok) break;
+                const uint32_t dst = sb + SM::OFF_W + w * SM::W_STAGE;
+                mbar_expect_if(lead, bar(SM::B_WFULL + w), SM::W_STAGE);
+                tma_load_3d_if(lead, dst, &tmk, bar(SM::B_WFULL + w), kc * 64, 0, p.h0 + ha + st);
+                tma_load_3d_if(lead, dst + D * 128, &tmv, bar(SM::B_WFULL + w), kc * 64, 0, p.h0 + ha + st);
             }
-            if (!ok) {
-                // the copies in flight land (bounded) before shared memory is released
-                atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
-                (void)mbar_wait_bounded(bar(SM::B_A), 0);
-                for (int i = max(0, n - SM::NW); i < n; ++i)
-                    (void)mbar_wait_bounded(bar(SM::B_WFULL + i % SM::NW), (i / SM::NW) & 1);
-            }
+        }
+        if (!ok && lead) {
+            // the copies in flight land (bounded) before shared memory is released
+            atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+            (void)mbar_wait_bounded(bar(SM::B_A), 0);
+            for (int i = max(0, n - SM::NW); i < n; ++i)
+                (void)mbar_wait_bounded(bar(SM::B_WFULL + i % SM::NW), (i / SM::NW) & 1);
         }
         __syncwarp();
     } else if (warp == 5) {
@@ -392,29 +390,30 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
     if (warp == 9) {
-        // ================= copies: block n of the stream of tiles into slot n % NR ==============
-        if (lane == 0) {
-            bool ok = true;
-            int n = 0;
-            for (int i = 0; i < n_tiles && ok; ++i) {
-#pragma unroll 1
-                for (int u = 0; u < NB; ++u, ++n) {
-                    const int slot = n % NR;
-                    if (n >= NR) ok = wait_or_abort(bar(SM::B_FREE + slot), (n / NR - 1) & 1, abort_flag);
-                    if (!ok) break;
-                    const uint32_t dst = sb + SM::OFF_R + slot * kBlk, fb = bar(SM::B_FULL + slot);
-                    mbar_arrive_expect_tx(fb, kBlk);
-                    if (u < KB - 1) tma_load_3d(dst, &tmk, fb, u * 64, i * kTile, bh);
-                    else if (u == KB - 1) tma_load_3d(dst, &tmr, fb, 0, i * kTile, b);
-                    else tma_load_3d(dst, &tmv, fb, (u - KB) * 64, i * kTile, bh);
-                }
+        // ===== copies: block n of the stream of tiles into slot n % NR (the warp converged) =========
+        const bool lead = elect_one();
+        bool ok = true;
+        int n = 0;
+        for (int i = 0; i < n_tiles && ok; ++i) {
+#pragma unroll
+            for (int u = 0; u < NB; ++u) {
+                if (!ok) break;
+                const int slot = n % NR;
+                if (n >= NR) ok = wait_warp(lead, bar(SM::B_FREE + slot), (n / NR - 1) & 1, abort_flag);
+                if (!ok) break;
+                const uint32_t dst = sb + SM::OFF_R + slot * kBlk, fb = bar(SM::B_FULL + slot);
+                mbar_expect_if(lead, fb, kBlk);
+                if (u < KB - 1) tma_load_3d_if(lead, dst, &tmk, fb, u * 64, i * kTile, bh);
+                else if (u == KB - 1) tma_load_3d_if(lead, dst, &tmr, fb, 0, i * kTile, b);
+                else tma_load_3d_if(lead, dst, &tmv, fb, (u - KB) * 64, i * kTile, bh);
+                ++n;
             }
-            if (!ok) {
-                // the copies in flight land (bounded) before shared memory is released
-                atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
-                for (int i = max(0, n - NR); i < n; ++i)
-                    (void)mbar_wait_bounded(bar(SM::B_FULL + i % NR), (i / NR) & 1);
-            }
+        }
+        if (!ok && lead) {
+            // the copies in flight land (bounded) before shared memory is released
+            atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+            for (int i = max(0, n - NR); i < n; ++i)
+                (void)mbar_wait_bounded(bar(SM::B_FULL + i % NR), (i / NR) & 1);
         }
         __syncwarp();
     } else if (warp == 8) {

@@ -157,6 +157,45 @@ __device__ __forceinline__ bool wait_warp(bool asks, uint32_t bar, uint32_t pari
         if (__any_sync(0xffffffffu, late || *abort)) return false;
     }
 }
+// The copies of a converged warp, issued by its lane with `lead` (the same holds for their operands).
+__device__ __forceinline__ void mbar_expect_if(bool lead, uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}"
+        ::"r"(bar), "r"(bytes), "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_if(bool lead, uint32_t dst, const void *tmap, uint32_t bar,
+                                               int x, int y) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];\n\t}"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_if(bool lead, uint32_t dst, const void *tmap, uint32_t bar,
+                                               int x, int y, int z) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];\n\t}"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar),
+          "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_load_if(bool lead, uint32_t dst, const void *src, uint32_t bytes,
+                                             uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}"
+        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "r"((uint32_t)lead)
+        : "memory");
+}
 __device__ __forceinline__ void umma_commit_if(bool lead, uint32_t bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"

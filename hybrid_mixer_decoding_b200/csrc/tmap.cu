@@ -98,6 +98,23 @@ bool make_tmap_blocks_sw128(CUtensorMap *m, CUtensorMapDataType dt, const void *
            CUDA_SUCCESS;
 }
 
+// Rows [rows][pitch] of 16-bit values as a 3-D tensor (64 columns, rows, column blocks of 64) read in
+// boxes of box_blocks column blocks x box_rows rows with the 128-byte swizzle: one box is
+// box_blocks tiles [box_rows][128 B] one after another.
+bool make_tmap_colblocks_sw128(CUtensorMap *m, CUtensorMapDataType dt, const void *base, long long rows,
+                               int pitch, int n_blocks, int box_rows, int box_blocks) {
+    EncodeTiledFn enc = encode();
+    if (!enc) return false;
+    const cuuint64_t gdim[3] = {64, (cuuint64_t)rows, (cuuint64_t)n_blocks};
+    const cuuint64_t gstride[2] = {(cuuint64_t)pitch * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_blocks};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, dt, 3, const_cast<void *>(base), gdim, gstride, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 // A paged pool [n_pages][heads][64][d] bf16 viewed as [n_pages*heads*64 rows][d], read in boxes
 // of 64 rows x 64 dims with the 128-byte swizzle: one box is half of one page of one head.
 bool make_tmap_pool_sw128(CUtensorMap *m, void *pool, int n_pages, int heads, int d) {

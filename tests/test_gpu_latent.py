@@ -128,6 +128,14 @@ def test_decode_batches_and_lengths(B, L):
     assert hmd.hmd_device_errors(clear=True) == 0
 
 
+def test_decode_many_tokens_per_head():
+    """More (head, 16 tokens) pairs than SMs: the merge takes 32 tokens a CTA, the last one fewer."""
+    c = Latent([1 + 3 * (b % 50) for b in range(99)], 32, 128, 512, seed=9)
+    q, new_c = c.new(1)
+    check_decode(c, q, new_c, c.decode(q, new_c))
+    assert hmd.hmd_device_errors(clear=True) == 0
+
+
 def test_decode_unused_rows_and_a_bad_length():
     c = Latent([0, 130, 0, 0, 64, 0], 16, 128, 512, seed=1, max_len=200)
     q, new_c = c.new(2)
