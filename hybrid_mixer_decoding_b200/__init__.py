@@ -6,7 +6,7 @@ include/hmd.h); this package is its ctypes binding plus the seeded input generat
 48-layer mixer-only stack driver.
 """
 from ._lib import (BF16, BatchPlan, group_sequences, mixer_decode_step_batch, DEVERR_GATE, DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_SLOT, DEVERR_TIMEOUT, F32, FA, GDN,
-                   KDA, SWA, DecodeIO, HmdError, KVCache, StateCache, attn_decode,
+                   KDA, SWA, DecodeIO, HmdError, KVCache, LatentCache, StateCache, attn_decode,
                    attn_decode_static_ws, attn_prefill, attn_prefill_ext, attn_decode_workspace_size,
                    attn_latent_decode, attn_latent_decode_workspace_size, attn_latent_prefill,
                    attn_latent_prefill_workspace_size, DEVWARN_RANGE,
@@ -20,7 +20,7 @@ from ._lib import (BF16, BatchPlan, group_sequences, mixer_decode_step_batch, DE
                    mixer_decode_step)
 
 __all__ = ["BF16", "BatchPlan", "group_sequences", "mixer_decode_step_batch", "DEVERR_GATE", "DEVERR_PAGE", "DEVERR_SEQLEN", "DEVERR_SLOT", "DEVERR_TIMEOUT", "F32", "FA",
-           "GDN", "KDA", "SWA", "DecodeIO", "HmdError", "KVCache", "StateCache", "attn_decode",
+           "GDN", "KDA", "SWA", "DecodeIO", "HmdError", "KVCache", "LatentCache", "StateCache", "attn_decode",
            "attn_decode_static_ws", "attn_decode_workspace_size", "attn_latent_decode",
            "attn_latent_decode_workspace_size", "attn_latent_prefill",
            "attn_latent_prefill_workspace_size", "DEVWARN_RANGE", "attn_prefill", "attn_prefill_ext",

@@ -71,6 +71,9 @@ _SIGS = {
     "kv_cache_evict": (_c_int, [_c_int] * 6 + [_vp, _vp, _c_int, _vp, _c_int, _vp, _c_int, _vp,
                                                _c_int, _c_int, _vp, _vp, _c_int, _vp, _c_int, _vp,
                                                _vp, _vp]),
+    "latent_cache_alloc": (_c_int, [_c_int, _vp] + [_c_int] * 5 + [_vp, ctypes.POINTER(_vp)]),
+    "latent_cache_free": (_c_int, [_vp, _vp]),
+    "latent_cache_layer": (_c_int, [_vp, _c_int, ctypes.POINTER(_vp)]),
     "attn_latent_decode_workspace_size": (_sz, [_c_int] * 8),
     "attn_latent_decode": (_c_int, [_c_int] * 7 + [_c_float, _vp, _vp, _vp, ctypes.c_int64, _vp,
                                                  ctypes.c_int64, _vp, _c_int, _vp, _c_int, _vp,
@@ -589,6 +592,31 @@ class KVCache:
     def free(self, stream=None):
         if self.handle:
             _check("kv_cache_free", lib().kv_cache_free(self.handle, _stream(stream)))
+            self.handle = None
+
+
+class LatentCache:
+    """latent_cache_alloc / _layer / _free: n_pools pools of [n_pages,page_tokens,d_c+d_r] bf16."""
+
+    def __init__(self, layer_pool, n_pools, n_pages, d_c, d_r=64, page_tokens=64, stream=None):
+        lp = (ctypes.c_int32 * len(layer_pool))(*[int(x) for x in layer_pool])
+        h = _vp()
+        _check("latent_cache_alloc", lib().latent_cache_alloc(len(layer_pool), lp, n_pools, n_pages,
+                                                              d_c, d_r, page_tokens,
+                                                              _stream(stream), ctypes.byref(h)))
+        self.handle = h.value
+        self.n_pages, self.d_c, self.d_r, self.page_tokens = n_pages, d_c, d_r, page_tokens
+
+    def layer_pool(self, layer) -> torch.Tensor:
+        """A torch view of the layer's pool (no copy)."""
+        p = _vp()
+        _check("latent_cache_layer", lib().latent_cache_layer(self.handle, layer, ctypes.byref(p)))
+        shape = (self.n_pages, self.page_tokens, self.d_c + self.d_r)
+        return _from_ptr(p.value, shape[0] * shape[1] * shape[2], torch.bfloat16).view(shape)
+
+    def free(self, stream=None):
+        if self.handle:
+            _check("latent_cache_free", lib().latent_cache_free(self.handle, _stream(stream)))
             self.handle = None
 
 

@@ -12,6 +12,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "kernels.h"
@@ -34,6 +35,12 @@ struct hmd_kv_cache {
     int n_layers, n_pools, n_pages, Hkv, d, page_tokens;
     std::vector<int32_t> layer_pool;
     std::vector<void *> k_pools, v_pools;
+};
+
+struct hmd_latent_cache {
+    int n_layers, n_pools;
+    int32_t *layer_pool;  // [n_layers]
+    void **pools;         // [n_pools]
 };
 
 namespace {
@@ -596,6 +603,61 @@ hmd_status_t kv_cache_evict(int budget, int recent, int B, int Hkv, int d, int p
 }
 
 // ---- latent attention ----------------------------------------------------------------------
+
+hmd_status_t latent_cache_alloc(int n_layers, const int32_t *layer_pool, int n_pools, int n_pages,
+                                int d_c, int d_r, int page_tokens, hmd_stream_t stream,
+                                hmd_latent_cache_t **out) {
+    if (!out || !layer_pool) return fail(HMD_ERR_ARG);
+    *out = nullptr;
+    if (n_layers < 1 || n_pools < 0 || n_pages < 1 || d_c < 1 || d_r < 1 || page_tokens < 1)
+        return fail(HMD_ERR_SHAPE);
+    for (int l = 0; l < n_layers; ++l)
+        if (layer_pool[l] < -1 || layer_pool[l] >= n_pools) return fail(HMD_ERR_ARG);
+    auto *c = new (std::nothrow) hmd_latent_cache{n_layers, 0, nullptr, nullptr};
+    if (!c) return fail(HMD_ERR_OOM);
+    c->layer_pool = new (std::nothrow) int32_t[n_layers];
+    c->pools = new (std::nothrow) void *[n_pools > 0 ? n_pools : 1];
+    const size_t bytes = (size_t)n_pages * page_tokens * ((size_t)d_c + d_r) * 2;
+    hmd_status_t st = c->layer_pool && c->pools ? HMD_OK : HMD_ERR_OOM;
+    cudaStream_t s = as_stream(stream);
+    for (; st == HMD_OK && c->n_pools < n_pools; ) {
+        void *p = nullptr;
+        if (cudaMallocAsync(&p, bytes, s) != cudaSuccess) {
+            cudaGetLastError();
+            st = HMD_ERR_OOM;
+            break;
+        }
+        c->pools[c->n_pools++] = p;
+        if (cudaMemsetAsync(p, 0, bytes, s) != cudaSuccess) st = HMD_ERR_CUDA;
+    }
+    if (st != HMD_OK) {
+        latent_cache_free(c, stream);
+        return fail(st);
+    }
+    std::copy(layer_pool, layer_pool + n_layers, c->layer_pool);
+    *out = c;
+    return HMD_OK;
+}
+
+hmd_status_t latent_cache_free(hmd_latent_cache_t *c, hmd_stream_t stream) {
+    if (!c) return fail(HMD_ERR_ARG);
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < c->n_pools; ++i) {
+        const cudaError_t f = cudaFreeAsync(c->pools[i], as_stream(stream));
+        if (f != cudaSuccess) e = f;
+    }
+    delete[] c->layer_pool;
+    delete[] c->pools;
+    delete c;
+    return from_cuda(e);
+}
+
+hmd_status_t latent_cache_layer(hmd_latent_cache_t *c, int layer, void **pool) {
+    if (!c || !pool) return fail(HMD_ERR_ARG);
+    if (layer < 0 || layer >= c->n_layers || c->layer_pool[layer] < 0) return fail(HMD_ERR_ARG);
+    *pool = c->pools[c->layer_pool[layer]];
+    return HMD_OK;
+}
 
 size_t attn_latent_decode_workspace_size(int n_q, int B, int H, int d, int d_c, int d_r,
                                          int page_tokens, int max_seq_len) {

@@ -334,7 +334,8 @@ HMD_API hmd_status_t attn_decode_static_ws(hmd_kind_t kind, int window, int B, i
  *   positions a prefill filled. Entries from L on are left as they were.
  * No two sequences of a call may share a row. To count a prompt's last queries, prefill all but
  * its last n_q tokens and run those through this call. A bad slot skips the sequence's weights
- * and sets HMD_DEVERR_SLOT; o and the append are those of attn_verify, bit for bit.
+ * and sets HMD_DEVERR_SLOT. The append is attn_verify's; o is too, bit for bit where both split
+ * the keys alike (max_seq_len up to 2048), else up to the rounding of fp32 sums in another order.
  *   workspace: at least attn_verify_scored_workspace_size(...) bytes (attn_verify's partials and
  *   4 bytes per query row and key).
  * Supported: as attn_verify.                                                                  */
@@ -388,6 +389,16 @@ HMD_API hmd_status_t kv_cache_evict(int budget, int recent, int B, int Hkv, int 
 /* that one [H][2 d][d_c] projection can hold both.                                            */
 /* Supported: d in {64, 128}; d_c in {128, 256, 384, 512}; d_r == 64; page_tokens == 64; any H.  */
 /* ------------------------------------------------------------------------------------------ */
+
+/* Latent cache: n_pools pools [n_pages][page_tokens][d_c + d_r] bf16, zero-filled; layer_pool (host,
+ * n_layers entries) maps each layer to a pool, or -1 for none (layers may share one), as in
+ * kv_cache_alloc. Memory comes from cudaMallocAsync on `stream`.                               */
+typedef struct hmd_latent_cache hmd_latent_cache_t;
+HMD_API hmd_status_t latent_cache_alloc(int n_layers, const int32_t *layer_pool, int n_pools,
+                                        int n_pages, int d_c, int d_r, int page_tokens,
+                                        hmd_stream_t stream, hmd_latent_cache_t **out);
+HMD_API hmd_status_t latent_cache_free(hmd_latent_cache_t *cache, hmd_stream_t stream);
+HMD_API hmd_status_t latent_cache_layer(hmd_latent_cache_t *cache, int layer, void **pool);
 
 /* Absorbed form, n_q new tokens per sequence (n_q = 1: the decode step): appends their rows and
  * attends as attn_verify does (token i sits at position L - n_q + i), reading the cache once for

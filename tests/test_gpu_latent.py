@@ -360,3 +360,56 @@ def test_prefill_captured_on_another_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, ref)
+
+
+def test_cache_handle_holds_the_layers_pools():
+    cache = hmd.LatentCache([0, -1, 1, 0], 2, 5, 128)
+    a, b = cache.layer_pool(0), cache.layer_pool(2)
+    assert a.shape == (5, PT, 192) and (a == 0).all() and (b == 0).all()
+    a.fill_(3.0)
+    assert torch.equal(cache.layer_pool(3), a) and (b == 0).all()
+    for layer in (-1, 1, 4):
+        with pytest.raises(hmd.HmdError, match="HMD_ERR_ARG"):
+            cache.layer_pool(layer)
+    # a decode step on the handle's pool
+    c = Latent([70], 4, 64, 128, seed=30, max_len=128)
+    cache.layer_pool(2)[:2] = c.pool
+    q, new_c = c.new(1)
+    want = c.decode(q, new_c)
+    c.pool = cache.layer_pool(2)
+    assert torch.equal(c.decode(q, new_c), want)
+    cache.free()
+
+
+def test_two_streams_with_their_own_workspaces():
+    cs = [Latent([700 + i, 300], 16, 128, 512, seed=40 + i) for i in range(2)]
+    new = [c.new(1) for c in cs]
+    ws = [c.workspace(1) for c in cs]
+    outs = [torch.empty(2, 1, 16, 128, device="cuda", dtype=BF) for _ in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(5):
+        for c, (q, n), w, o, s in zip(cs, new, ws, outs, streams):
+            hmd.attn_latent_decode(q, n, c.w_uk, c.w_uv, c.pool, c.table, c.lens, c.max_len, o, w, stream=s)
+    torch.cuda.synchronize()
+    for c, (q, n), o in zip(cs, new, outs):
+        check_decode(c, q, n, o)
+
+
+def test_offsets_beyond_32_bits():
+    """A pool whose last pages lie beyond 2^32 bytes, and beyond 2^31 elements."""
+    n_pages = 2**32 // (64 * 576 * 2) + 4000
+    if torch.cuda.mem_get_info()[0] < 2 * n_pages * 64 * 576 * 2:
+        pytest.skip("not enough free memory")
+    c = Latent([130, 70], 16, 128, 512, seed=50, max_len=192)
+    pool = torch.zeros(n_pages, PT, 576, device="cuda", dtype=BF)
+    at = torch.arange(n_pages - c.pool.shape[0], n_pages, device="cuda")
+    pool[at] = c.pool
+    c.table = at.to(torch.int32)[c.table.long()].contiguous()
+    c.pool = pool
+    q, new_c = c.new(1)
+    check_decode(c, q, new_c, c.decode(q, new_c))
+    qp, cp = c.randn(2, 40, 16, 192), c.randn(2, 40, 576)
+    c.lens_list = [152, 110]
+    check_prefill(c, qp, cp, prefill(c, qp, cp, [112, 70], [40, 40]), [112, 70], [40, 40])
+    assert hmd.hmd_device_errors(clear=True) == 0
