@@ -526,43 +526,19 @@ __global__ void __launch_bounds__(128) attn_combine_scored_kernel(const ScorePar
         if (tid == 0) atomicOr(&g_err, HMD_DEVERR_SLOT);
         return;
     }
-    if (tid == 0) s_missing = 0;
-    __syncthreads();
-    for (int r = tid >> 5; r < R; r += 4) {  // a warp per row: the row's statistics
-        const int ti = r / G, lane = tid & 31;
-        const size_t row = ((size_t)b * p.nq + ti) * p.Hq + g * G + (r - ti * G);
-        const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + row * p.n_splits;
-        float M = -INFINITY, l = 0.f;
-        bool missing = false;
-        for (int s = lane; s < p.n_splits; s += 32) {
-            const float2 v = ml[s];
-            missing |= v.y < 0.f;
-            const float m2 = fmaxf(M, v.x);
-            if (m2 != -INFINITY) l = l * exp2f(M - m2) + v.y * exp2f(v.x - m2);
-            M = m2;
-        }
-#pragma unroll
-        for (int off = 16; off; off >>= 1) {
-            const float Mo = __shfl_xor_sync(0xffffffffu, M, off);
-            const float lo = __shfl_xor_sync(0xffffffffu, l, off);
-            const float m2 = fmaxf(M, Mo);
-            if (m2 != -INFINITY) l = l * exp2f(M - m2) + lo * exp2f(Mo - m2);
-            M = m2;
-        }
-        if (__any_sync(0xffffffffu, missing) && lane == 0) s_missing = 1;
-        if (lane == 0) {
-            s_max[r] = M == -INFINITY ? 0.f : M;
-            s_inv[r] = l > 0.f ? 1.f / l : 0.f;
-        }
-    }
-    __syncthreads();
-    if (s_missing) return;
-    // four keys per thread, four rows' loads in flight before their sums
+    // four keys per thread, eight rows' loads in flight (the first eight before the statistics)
     const int j0 = chunk * kScoreKeys + tid * 4;
-    if (j0 >= L) return;
+    const int rows = j0 < L ? R : 0;
     const float *sc = p.ws_s + (size_t)bg * R * p.s_len + j0;
     float *w = p.weights + ((size_t)slot * p.Hkv + g) * p.w_len + j0;
     const int n_old = L - p.nq - j0, n = min(4, L - j0);  // of the four: old keys, keys
+    float4 x[8];
+    auto load_rows = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (r0 + u < rows) x[u] = __ldcs(reinterpret_cast<const float4 *>(sc + (size_t)(r0 + u) * p.s_len));
+    };
+    load_rows(0);
     float a[4] = {0.f, 0.f, 0.f, 0.f};
     const bool whole = n_old >= 4 && (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
     if (whole) {
@@ -573,14 +549,42 @@ __global__ void __launch_bounds__(128) attn_combine_scored_kernel(const ScorePar
         for (int e = 0; e < 4; ++e)
             if (e < n_old) a[e] = w[e];
     }
+    if (tid == 0) s_missing = 0;
+    __syncthreads();
+    {  // eight lanes per row, the 16 rows at once: the row's statistics
+        const int r = tid >> 3, sub = tid & 7, ti = r / G;
+        float M = -INFINITY, l = 0.f;
+        if (r < R) {
+            const size_t row = ((size_t)b * p.nq + ti) * p.Hq + g * G + (r - ti * G);
+            const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + row * p.n_splits;
+            for (int s = sub; s < p.n_splits; s += 8) {
+                const float2 v = ml[s];
+                if (v.y < 0.f) s_missing = 1;
+                const float m2 = fmaxf(M, v.x);
+                if (m2 != -INFINITY) l = l * exp2f(M - m2) + v.y * exp2f(v.x - m2);
+                M = m2;
+            }
+        }
+#pragma unroll
+        for (int off = 4; off; off >>= 1) {
+            const float Mo = __shfl_xor_sync(0xffffffffu, M, off);
+            const float lo = __shfl_xor_sync(0xffffffffu, l, off);
+            const float m2 = fmaxf(M, Mo);
+            if (m2 != -INFINITY) l = l * exp2f(M - m2) + lo * exp2f(Mo - m2);
+            M = m2;
+        }
+        if (sub == 0 && r < R) {
+            s_max[r] = M == -INFINITY ? 0.f : M;
+            s_inv[r] = l > 0.f ? 1.f / l : 0.f;
+        }
+    }
+    __syncthreads();
+    if (s_missing || rows == 0) return;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int r0 = 0; r0 < R; r0 += 4) {
-        float4 x[4];
+    for (int r0 = 0; r0 < R; r0 += 8) {
+        if (r0) load_rows(r0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (r0 + u < R) x[u] = __ldcs(reinterpret_cast<const float4 *>(sc + (size_t)(r0 + u) * p.s_len));
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
             if (r0 + u < R) {
                 const float m = s_max[r0 + u], inv = s_inv[r0 + u];
                 sum[0] += exp2f(x[u].x - m) * inv;

@@ -117,11 +117,19 @@ __global__ void __launch_bounds__(kChooseThreads, 2) evict_choose_kernel(const E
     const float *w = a.weights + ((size_t)r.slot * a.Hkv + g) * a.w_len + e0;
     auto key_at = [&](int i) { return CACHED ? keys[i] : order_key(w[i]); };
     __syncthreads();  // the histograms are zero
-#pragma unroll 8
-    for (int i = tid; i < n; i += kChooseThreads) {
-        const uint32_t k = order_key(w[i]);
-        if (CACHED) keys[i] = k;
-        atomicAdd(&hist[0][k >> 21], 1u);
+    for (int i0 = tid; i0 < n; i0 += 8 * kChooseThreads) {
+        float x[8];  // eight loads in flight: none waits for a histogram's atomics
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (i0 + u * kChooseThreads < n) x[u] = __ldg(w + i0 + u * kChooseThreads);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * kChooseThreads;
+            if (i >= n) break;
+            const uint32_t k = order_key(x[u]);
+            if (CACHED) keys[i] = k;
+            atomicAdd(&hist[0][k >> 21], 1u);
+        }
     }
     // the m-th largest key: `left` of the keys that share the digits found so far are wanted
     uint32_t prefix = 0, mask = 0, left = (uint32_t)r.m;
@@ -161,8 +169,8 @@ __global__ void __launch_bounds__(kChooseThreads, 2) evict_choose_kernel(const E
         }
         if (lane == 31) warp_gt[warp] = sum;
         __syncthreads();
-        uint32_t before = sum - c0 - c1;  // keys with a larger digit
-        for (int v = 0; v < warp; ++v) before += warp_gt[v];
+        // keys with a larger digit
+        const uint32_t before = sum - c0 - c1 + __reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane] : 0u);
         if (before < left && left <= before + c0) {
             s_digit = kBins - 1 - 2 * tid;
             s_left = left - before;
@@ -219,10 +227,8 @@ __global__ void __launch_bounds__(kChooseThreads, 2) evict_choose_kernel(const E
             eq += x[q].y;
         }
     }
-    for (int v = 0; v < warp; ++v) {
-        gt += warp_gt[v];
-        eq += warp_eq[v];
-    }
+    gt += __reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane] : 0u);
+    eq += __reduce_add_sync(0xffffffffu, lane < warp ? warp_eq[lane] : 0u);
 #pragma unroll 4
     for (int i = i0; i < i1; i += 32) {
         const uint32_t k = i + lane < i1 ? key_at(i + lane) : 0u;

@@ -22,6 +22,7 @@ def _scored(n_q=1, B=2, Hq=8, Hkv=2, d=128, pt=64, q=FAKE, pool=FAKE, n_pages=10
     (dict(n_slots=-1, slots=FAKE), SHAPE), (dict(max_pages=9), SHAPE), (dict(ws_bytes=16), SHAPE),
     (dict(d=96), UNSUP), (dict(n_q=5), UNSUP), (dict(pt=32, max_pages=20), UNSUP), (dict(B=0), OK)])
 def test_scored_refusals(bad, status):
+    hmd.hmd_last_error()  # clear this thread's last status
     assert _scored(**bad) == status
     assert hmd.hmd_last_error() == status
 
@@ -49,6 +50,7 @@ def _evict(budget=64, recent=8, B=2, Hkv=2, d=128, pt=64, pool=FAKE, n_pages=100
     (dict(dst=FAKE, dst_pages=9), SHAPE), (dict(w_out=FAKE, w_out_len=64), SHAPE),
     (dict(d=256), UNSUP), (dict(pt=16, max_pages=40, dst_pages=4), UNSUP), (dict(B=0), OK)])
 def test_evict_refusals(bad, status):
+    hmd.hmd_last_error()  # clear this thread's last status
     assert _evict(**bad) == status
     assert hmd.hmd_last_error() == status
 

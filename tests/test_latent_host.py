@@ -29,6 +29,7 @@ def _decode(n_q=1, B=2, H=16, d=128, d_c=512, d_r=64, pt=64, scale=0.07, q=FAKE,
     (dict(d_c=64), UNSUP), (dict(d_r=32), UNSUP), (dict(pt=32, max_pages=20), UNSUP),
     (dict(n_pages=1 << 26), UNSUP), (dict(B=0), OK)])
 def test_decode_refusals(bad, status):
+    hmd.hmd_last_error()  # clear this thread's last status
     assert _decode(**bad) == status
     assert hmd.hmd_last_error() == status
 
@@ -48,6 +49,7 @@ def _prefill(B=2, T=300, H=16, d=128, d_c=512, d_r=64, pt=64, scale=0.07, q=FAKE
     (dict(ws_bytes=100), SHAPE), (dict(d=32), UNSUP), (dict(d_c=100), UNSUP),
     (dict(T=1 << 30, max_pages=1 << 24), UNSUP), (dict(B=0), OK), (dict(T=0), OK)])
 def test_prefill_refusals(bad, status):
+    hmd.hmd_last_error()  # clear this thread's last status
     assert _prefill(**bad) == status
     assert hmd.hmd_last_error() == status
 
