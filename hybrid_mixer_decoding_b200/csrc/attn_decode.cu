@@ -94,9 +94,12 @@ struct Item {
 
 __device__ __forceinline__ Item item_info(const SplitParams &p, int i) {
     Item it;
-    it.split = i % p.n_splits;
-    it.g = (i / p.n_splits) % p.Hkv;
-    it.r = i / (p.n_splits * p.Hkv);
+    // the scored form starts every sequence's first range before any second one: a ragged batch's
+    // short and empty ranges are the last to start
+    const int units = p.ws_s ? p.B * p.Hkv : 1, unit = p.ws_s ? i % units : i / p.n_splits;
+    it.split = p.ws_s ? i / units : i % p.n_splits;
+    it.g = unit % p.Hkv;
+    it.r = unit / p.Hkv;
     it.b = p.rows ? p.rows[it.r] : it.r;
     it.L = p.seq_lens[it.b];
     it.bad_len = it.L < p.nq || it.L > p.max_seq_len;
