@@ -124,19 +124,20 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(const PrefillParams p,
 }
 
 // ---- kernel 2 ------------------------------------------------------------------------------------
-constexpr int kExpandThreads = 192;
-template <int D>
+constexpr int kExpandThreads = 320;
+constexpr int kExpAcc = 4;  // accumulators of 128 columns
 struct ExpandSmem {
-    static constexpr uint32_t W_STAGE = 2 * D * 128;  // [W_uk ; W_uv] rows x 64 latent dims
-    static constexpr int NW = 3;                      // stages: what is left beside 512 dims of C
+    static constexpr uint32_t W_STAGE = kBlk;  // a step's 128 rows of weights x 64 latent dims
+    static constexpr int NW = 6;               // stages: what is left beside 512 dims of C
     static constexpr uint32_t OFF_A = 0, OFF_W = 8 * kBlk;
     static constexpr uint32_t OFF_MISC = OFF_W + NW * W_STAGE;
     static constexpr uint32_t BYTES = OFF_MISC + 256 + 1024;
-    static constexpr uint32_t ALLOC = BYTES > 118784 ? BYTES : 118784;  // one CTA per SM
+    static constexpr uint32_t ALLOC = BYTES;   // one CTA per SM
     static constexpr int B_A = 0, B_WFULL = 1, B_WFREE = B_WFULL + NW, B_ACC = B_WFREE + NW,
-                         B_READ = B_ACC + 2, B_END = B_READ + 2, N_BARS = B_END + 1;
+                         B_READ = B_ACC + kExpAcc, B_END = B_READ + kExpAcc, N_BARS = B_END + 1;
+    static_assert(N_BARS * 8 + 8 <= 256, "barriers");
 };
-static_assert(ExpandSmem<128>::ALLOC <= 232448, "shared memory per CTA");
+static_assert(ExpandSmem::ALLOC <= 232448, "shared memory per CTA");
 
 // 32 bytes to global memory in one store
 __device__ __forceinline__ void store_32b(void *dst, const uint32_t (&v)[8]) {
@@ -149,7 +150,8 @@ template <int D>
 __global__ void __launch_bounds__(kExpandThreads, 1)
 latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant__ CUtensorMap tmk,
                  const __grid_constant__ CUtensorMap tmv, const PrefillParams p) {
-    using SM = ExpandSmem<D>;
+    using SM = ExpandSmem;
+    constexpr int STEPS = D / 64;  // steps of 128 columns a head: K and V of 64 dims at once, of 128 in turn
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -161,18 +163,20 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     const int tiles = p.s_pad / kTile, tile = blockIdx.x / p.splits;
     const int b = tile / tiles, pos0 = (tile - b * tiles) * kTile;
     const int ha = (blockIdx.x % p.splits) * p.per_split, hb = min(p.heads, ha + p.per_split);
-    const int n_kc = p.dc / 64, n_steps = hb - ha;
+    const int n_kc = p.dc / 64, n_steps = (hb - ha) * STEPS;
+    // a CTA's heads, in an order that begins elsewhere for every tile
+    auto head_of = [&](int st) { return ha + (st / STEPS + tile) % (hb - ha); };
     griddep_launch_dependents();
     griddep_wait();  // the appended rows are kernel 1's
     const Seq s = seq_of(p, b);
     if (pos0 >= s.total || n_steps <= 0) return;
     if (tid == 0) {
         for (int i = 0; i < SM::N_BARS; ++i)
-            mbar_init(bar(i), (i == SM::B_READ || i == SM::B_READ + 1) ? 4 : 1);
+            mbar_init(bar(i), i >= SM::B_READ && i < SM::B_READ + kExpAcc ? 4 : 1);
         fence_barrier_init();
         *abort_flag = 0;
     }
-    if (warp == 5) {
+    if (warp == 9) {
         __syncwarp();
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
@@ -182,7 +186,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
-    if (warp == 4) {
+    if (warp == 8) {
         const bool lead = elect_one();
         // the tile's two pages of latent rows: blocks of 64 dims (a missing page's rows hold anything;
         // their results are stored as zeros)
@@ -206,8 +210,11 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
                 if (!ok) break;
                 const uint32_t dst = sb + SM::OFF_W + w * SM::W_STAGE;
                 mbar_expect_if(lead, bar(SM::B_WFULL + w), SM::W_STAGE);
-                tma_load_3d_if(lead, dst, &tmk, bar(SM::B_WFULL + w), kc * 64, 0, p.h0 + ha + st);
-                tma_load_3d_if(lead, dst + D * 128, &tmv, bar(SM::B_WFULL + w), kc * 64, 0, p.h0 + ha + st);
+                const int h = p.h0 + head_of(st);
+                if (STEPS == 1 || st % 2 == 0)
+                    tma_load_3d_if(lead, dst, &tmk, bar(SM::B_WFULL + w), kc * 64, 0, h);
+                if (STEPS == 1 || st % 2 == 1)
+                    tma_load_3d_if(lead, dst + (STEPS == 1 ? D * 128 : 0), &tmv, bar(SM::B_WFULL + w), kc * 64, 0, h);
             }
         }
         if (!ok && lead) {
@@ -218,16 +225,17 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
                 (void)mbar_wait_bounded(bar(SM::B_WFULL + i % SM::NW), (i / SM::NW) & 1);
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == 9) {
         const bool lead = elect_one();
         const Desc d_a(smem_desc_sw128(sb + SM::OFF_A, 16, 1024));
         const Desc d_w(smem_desc_sw128(sb + SM::OFF_W, 16, 1024));
-        constexpr uint32_t ID = idesc_bf16(128, 2 * D, 0, 0);
+        constexpr uint32_t ID = idesc_bf16(128, 128, 0, 0);
         auto wait = [&](int i, uint32_t parity) { wait_warp(lead, bar(i), parity, abort_flag); };
         wait(SM::B_A, 0);
         int n = 0;
         for (int st = 0; st < n_steps; ++st) {
-            if (st >= 2) wait(SM::B_READ + (st & 1), ((st >> 1) - 1) & 1);
+            const int acc = st % kExpAcc;
+            if (st >= kExpAcc) wait(SM::B_READ + acc, (st / kExpAcc - 1) & 1);
             for (int kc = 0; kc < n_kc; ++kc, ++n) {
                 const int w = n % SM::NW;
                 wait(SM::B_WFULL + w, (n / SM::NW) & 1);
@@ -235,10 +243,10 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
                 const Desc a = d_a.at(kc * kBlk), wd = d_w.at(w * SM::W_STAGE);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_if(lead, tmem + (st & 1) * 256, a.at(kk * 32), wd.at(kk * 32), ID,
+                    umma_if(lead, tmem + acc * 128, a.at(kk * 32), wd.at(kk * 32), ID,
                             (kc > 0 || kk > 0) ? 1u : 0u);
                 umma_commit_if(lead, bar(SM::B_WFREE + w));
-                if (kc == n_kc - 1) umma_commit_if(lead, bar(SM::B_ACC + (st & 1)));
+                if (kc == n_kc - 1) umma_commit_if(lead, bar(SM::B_ACC + acc));
             }
         }
         if (lead) {
@@ -248,54 +256,74 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         }
         __syncwarp();
     } else {
-        const int pos = pos0 + warp * 32 + lane;
+        // warps 0-3 store the even steps, 4-7 the odd ones; a lane has a position (its row of TMEM)
+        const int quarter = warp & 3, pos = pos0 + quarter * 32 + lane;
         const bool live = pos < s.total && page_of(p, b, pos) >= 0;
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const bool lead = elect_one();
         bool out = false;
-        for (int st = 0; st < n_steps; ++st) {
-            wait_warp(lead, bar(SM::B_ACC + (st & 1)), (st >> 1) & 1, abort_flag);
-            if (*abort_flag) break;  // reported by the products' warp; the whole warp leaves below
+        for (int st = warp >> 2; st < n_steps; st += 2) {
+            const int acc = st % kExpAcc;
+            wait_warp(lead, bar(SM::B_ACC + acc), (st / kExpAcc) & 1, abort_flag);
+            if (uniform(*abort_flag)) break;  // reported by the products' warp; the whole warp leaves below
             tc_fence_after();
-            const size_t row = (((size_t)b * p.heads + ha + st) * p.s_pad + pos) * D;
+            const size_t row0 = (((size_t)b * p.heads + head_of(st)) * p.s_pad + pos0 + quarter * 32 + (lane & ~3)) * D;
 #pragma unroll 1
-            for (int c = 0; c < 2 * D; c += 32) {
-                uint32_t r[32];
-                tmem_ld32(tmem + (st & 1) * 256 + c + lanes, r);
-                tmem_wait_ld();
-                __half *dst = c < D ? p.k + row + c : p.v + row + (c - D);
-                float big = 0.f;
+            for (int c = 0; c < 128; c += 64) {
+                uint32_t blk[4][8];  // 64 columns as fp16: four pieces of 32 bytes
 #pragma unroll
-                for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(__uint_as_float(r[j])));
-                if (live && big > kHalfMax) {
-                    out = true;
-                    for (int j = 0; j < 32; ++j) {
-                        float x = __uint_as_float(r[j]);
-                        clip_half(x);
-                        r[j] = __float_as_uint(x);
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t r[32];
+                    tmem_ld32(tmem + acc * 128 + c + half * 32 + lanes, r);
+                    tmem_wait_ld();
+                    float big = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(__uint_as_float(r[j])));
+                    if (live && big > kHalfMax) {
+                        out = true;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            float x = __uint_as_float(r[j]);
+                            clip_half(x);
+                            r[j] = __float_as_uint(x);
+                        }
                     }
-                }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        pk[j] = live ? pack_f16x2(__uint_as_float(r[16 * h + 2 * j]),
-                                                  __uint_as_float(r[16 * h + 2 * j + 1]))
-                                     : 0u;
-                    store_32b(dst + 16 * h, pk);
+                    for (int j = 0; j < 16; ++j)
+                        blk[half * 2 + j / 8][j % 8] =
+                            live ? pack_f16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])) : 0u;
                 }
                 __syncwarp();
+                // four lanes exchange their pieces, so that a store writes whole 128-byte lines
+#pragma unroll
+                for (int bit = 1; bit < 4; bit *= 2) {
+                    const bool upper = lane & bit;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        if (t & bit) continue;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t got =
+                                __shfl_xor_sync(0xffffffffu, upper ? blk[t][j] : blk[t | bit][j], bit);
+                            if (upper) blk[t][j] = got;
+                            else blk[t | bit][j] = got;
+                        }
+                    }
+                }
+                const bool key = STEPS == 2 ? st % 2 == 0 : c == 0;
+                __half *dst = (key ? p.k : p.v) + row0 + (STEPS == 2 ? c : 0) + (lane & 3) * 16;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) store_32b(dst + t * D, blk[t]);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(SM::B_READ + (st & 1)));
+            if (lane == 0) mbar_arrive(bar(SM::B_READ + acc));
         }
         if (out) atomicOr(&g_err, HMD_DEVWARN_RANGE);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == 9) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -639,7 +667,7 @@ template <int D>
 cudaError_t launch_d(const LatentPrefillArgs &a, cudaStream_t s) {
     const cudaError_t attr_err = once_per_device([] {
         cudaError_t e = cudaFuncSetAttribute(latent_kv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)ExpandSmem<D>::ALLOC);
+                                             (int)ExpandSmem::ALLOC);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(latent_attend_prompt_kernel<D>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AttendSmem<D>::ALLOC);
@@ -700,7 +728,7 @@ cudaError_t launch_d(const LatentPrefillArgs &a, cudaStream_t s) {
                                     (long long)s_pad, D, kTile))
             return cudaErrorInvalidValue;
         e = launch_pdl(latent_kv_kernel<D>, dim3((unsigned)(tiles * p.splits)), dim3(kExpandThreads),
-                       ExpandSmem<D>::ALLOC, s, tmc, tmuk, tmuv, p);
+                       ExpandSmem::ALLOC, s, tmc, tmuk, tmuv, p);
         if (e != cudaSuccess) break;
         e = launch_pdl(latent_attend_prompt_kernel<D>, dim3((unsigned)(p.n_qb * bh)), dim3(kAttThreads),
                        AttendSmem<D>::ALLOC, s, tmk, tmv, tmr, p);
