@@ -125,17 +125,19 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(const PrefillParams p,
 
 // ---- kernel 2 ------------------------------------------------------------------------------------
 constexpr int kExpandThreads = 320;
-constexpr int kExpAcc = 4;  // accumulators of 128 columns
+constexpr int kExpAcc = 2;  // accumulators of 128 columns, behind the latent rows' 256 in TMEM
 struct ExpandSmem {
     static constexpr uint32_t W_STAGE = kBlk;  // a step's 128 rows of weights x 64 latent dims
-    static constexpr int NW = 6;               // stages: what is left beside 512 dims of C
-    static constexpr uint32_t OFF_A = 0, OFF_W = 8 * kBlk;
-    static constexpr uint32_t OFF_MISC = OFF_W + NW * W_STAGE;
-    static constexpr uint32_t BYTES = OFF_MISC + 256 + 1024;
+    // The latent rows land in blocks 0-7 and go to TMEM; then all 14 blocks are stages of weights, of
+    // which the first six have been loading meanwhile.
+    static constexpr int NW = 14, EARLY = 6;
+    static constexpr uint32_t OFF_MISC = NW * W_STAGE;
+    static constexpr uint32_t BYTES = OFF_MISC + 512 + 1024;
     static constexpr uint32_t ALLOC = BYTES;   // one CTA per SM
-    static constexpr int B_A = 0, B_WFULL = 1, B_WFREE = B_WFULL + NW, B_ACC = B_WFREE + NW,
+    static constexpr int B_A = 0, B_MOVED = 1, B_WFULL = 2, B_WFREE = B_WFULL + NW, B_ACC = B_WFREE + NW,
                          B_READ = B_ACC + kExpAcc, B_END = B_READ + kExpAcc, N_BARS = B_END + 1;
-    static_assert(N_BARS * 8 + 8 <= 256, "barriers");
+    static_assert(N_BARS * 8 + 8 <= 512, "barriers");
+    __device__ static uint32_t stage(int w) { return (w < EARLY ? w + NW - EARLY : w - EARLY) * W_STAGE; }
 };
 static_assert(ExpandSmem::ALLOC <= 232448, "shared memory per CTA");
 
@@ -172,7 +174,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     if (pos0 >= s.total || n_steps <= 0) return;
     if (tid == 0) {
         for (int i = 0; i < SM::N_BARS; ++i)
-            mbar_init(bar(i), i >= SM::B_READ && i < SM::B_READ + kExpAcc ? 4 : 1);
+            mbar_init(bar(i), i >= SM::B_READ && i < SM::B_READ + kExpAcc ? 4 : i == SM::B_MOVED ? 8 : 1);
         fence_barrier_init();
         *abort_flag = 0;
     }
@@ -199,7 +201,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         mbar_expect_if(lead, bar(SM::B_A), bytes);
         for (int kc = 0; kc < n_kc; ++kc)
             for (int h = 0; h < 2; ++h)
-                tma_load_2d_if(lead && pg[h] >= 0, sb + SM::OFF_A + kc * kBlk + h * (kBlk / 2), &tmc,
+                tma_load_2d_if(lead && pg[h] >= 0, sb + kc * kBlk + h * (kBlk / 2), &tmc,
                                bar(SM::B_A), kc * 64, pg[h] * kPT);
         bool ok = true;
         int n = 0;
@@ -207,8 +209,9 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
             for (int kc = 0; kc < n_kc; ++kc, ++n) {
                 const int w = n % SM::NW;
                 if (n >= SM::NW) ok = wait_warp(lead, bar(SM::B_WFREE + w), (n / SM::NW - 1) & 1, abort_flag);
+                else if (n == SM::EARLY) ok = wait_warp(lead, bar(SM::B_MOVED), 0, abort_flag);
                 if (!ok) break;
-                const uint32_t dst = sb + SM::OFF_W + w * SM::W_STAGE;
+                const uint32_t dst = sb + SM::stage(w);
                 mbar_expect_if(lead, bar(SM::B_WFULL + w), SM::W_STAGE);
                 const int h = p.h0 + head_of(st);
                 if (STEPS == 1 || st % 2 == 0)
@@ -227,11 +230,10 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         __syncwarp();
     } else if (warp == 9) {
         const bool lead = elect_one();
-        const Desc d_a(smem_desc_sw128(sb + SM::OFF_A, 16, 1024));
-        const Desc d_w(smem_desc_sw128(sb + SM::OFF_W, 16, 1024));
+        const Desc d_w(smem_desc_sw128(sb, 16, 1024));
         constexpr uint32_t ID = idesc_bf16(128, 128, 0, 0);
         auto wait = [&](int i, uint32_t parity) { wait_warp(lead, bar(i), parity, abort_flag); };
-        wait(SM::B_A, 0);
+        wait(SM::B_MOVED, 0);
         int n = 0;
         for (int st = 0; st < n_steps; ++st) {
             const int acc = st % kExpAcc;
@@ -240,11 +242,11 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
                 const int w = n % SM::NW;
                 wait(SM::B_WFULL + w, (n / SM::NW) & 1);
                 tc_fence_after();
-                const Desc a = d_a.at(kc * kBlk), wd = d_w.at(w * SM::W_STAGE);
+                const Desc wd = d_w.at(SM::stage(w));
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_if(lead, tmem + acc * 128, a.at(kk * 32), wd.at(kk * 32), ID,
-                            (kc > 0 || kk > 0) ? 1u : 0u);
+                    umma_ts_if(lead, tmem + 256 + acc * 128, tmem + kc * 32 + kk * 8, wd.at(kk * 32), ID,
+                               (kc > 0 || kk > 0) ? 1u : 0u);
                 umma_commit_if(lead, bar(SM::B_WFREE + w));
                 if (kc == n_kc - 1) umma_commit_if(lead, bar(SM::B_ACC + acc));
             }
@@ -262,38 +264,59 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const bool lead = elect_one();
         bool out = false;
+        // the latent rows to TMEM as the products' A operand, half of the dims per four warps
+        wait_warp(lead, bar(SM::B_A), 0, abort_flag);
+        if (!uniform(*abort_flag)) {
+            const int row = quarter * 32 + lane;
+            for (int kc = warp >> 2; kc < n_kc; kc += 2) {
+                uint32_t x[32];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4 *>(&x[4 * j]) =
+                        *reinterpret_cast<const uint4 *>(sm + kc * kBlk + row * 128 + ((j ^ (row & 7)) << 4));
+                __syncwarp();
+                tmem_st32(tmem + kc * 32 + lanes, x);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(SM::B_MOVED));
+        }
         for (int st = warp >> 2; st < n_steps; st += 2) {
             const int acc = st % kExpAcc;
             wait_warp(lead, bar(SM::B_ACC + acc), (st / kExpAcc) & 1, abort_flag);
             if (uniform(*abort_flag)) break;  // reported by the products' warp; the whole warp leaves below
             tc_fence_after();
-            const size_t row0 = (((size_t)b * p.heads + head_of(st)) * p.s_pad + pos0 + quarter * 32 + (lane & ~3)) * D;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 64) {
-                uint32_t blk[4][8];  // 64 columns as fp16: four pieces of 32 bytes
+            uint32_t blk[8][8];  // 128 columns as fp16: pieces of 32 bytes
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t r[32];
-                    tmem_ld32(tmem + acc * 128 + c + half * 32 + lanes, r);
-                    tmem_wait_ld();
-                    float big = 0.f;
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[32];
+                tmem_ld32(tmem + 256 + acc * 128 + c * 32 + lanes, r);
+                tmem_wait_ld();
+                float big = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(__uint_as_float(r[j])));
-                    if (live && big > kHalfMax) {
-                        out = true;
+                for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(__uint_as_float(r[j])));
+                if (live && big > kHalfMax) {
+                    out = true;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            float x = __uint_as_float(r[j]);
-                            clip_half(x);
-                            r[j] = __float_as_uint(x);
-                        }
+                    for (int j = 0; j < 32; ++j) {
+                        float x = __uint_as_float(r[j]);
+                        clip_half(x);
+                        r[j] = __float_as_uint(x);
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        blk[half * 2 + j / 8][j % 8] =
-                            live ? pack_f16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])) : 0u;
                 }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    blk[c * 2 + j / 8][j % 8] =
+                        live ? pack_f16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])) : 0u;
                 __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(SM::B_READ + acc));  // the accumulator is free
+            const size_t row0 = (((size_t)b * p.heads + head_of(st)) * p.s_pad + pos0 + quarter * 32 + (lane & ~3)) * D;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
                 // four lanes exchange their pieces, so that a store writes whole 128-byte lines
 #pragma unroll
                 for (int bit = 1; bit < 4; bit *= 2) {
@@ -303,21 +326,18 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
                         if (t & bit) continue;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const uint32_t got =
-                                __shfl_xor_sync(0xffffffffu, upper ? blk[t][j] : blk[t | bit][j], bit);
-                            if (upper) blk[t][j] = got;
-                            else blk[t | bit][j] = got;
+                            uint32_t &x = blk[4 * c + t][j], &y = blk[4 * c + (t | bit)][j];
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x : y, bit);
+                            if (upper) x = got;
+                            else y = got;
                         }
                     }
                 }
                 const bool key = STEPS == 2 ? st % 2 == 0 : c == 0;
-                __half *dst = (key ? p.k : p.v) + row0 + (STEPS == 2 ? c : 0) + (lane & 3) * 16;
+                __half *dst = (key ? p.k : p.v) + row0 + (STEPS == 2 ? c * 64 : 0) + (lane & 3) * 16;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) store_32b(dst + t * D, blk[t]);
+                for (int t = 0; t < 4; ++t) store_32b(dst + t * D, blk[4 * c + t]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(SM::B_READ + acc));
         }
         if (out) atomicOr(&g_err, HMD_DEVWARN_RANGE);
     }
