@@ -387,8 +387,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
-    griddep_launch_dependents();
     griddep_wait();  // the image, the appended rows and the schedule are kernel 1's
+    griddep_launch_dependents();  // not before: kernel 3 reads W_uv, which then is complete, without waiting
     const int4 st0 = p.start[range], st1 = p.start[range + 1];
     const int begin = uniform(st0.x), end = uniform(st1.x), n_pages = end - begin;
     Walk w;
@@ -798,21 +798,21 @@ __global__ void __launch_bounds__(kExpThreads, 1) latent_expand_kernel(const Lat
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x, tok0 = blockIdx.y * tokens, rows = min(tokens, p.B * p.nq - tok0);
     const uint32_t bar = smem_u32(&sm.bar);
-    if (tid == 0) {
-        mbar_init(bar, 1);
-        fence_barrier_init();
-        sm.missing = 0;
-    }
-    griddep_launch_dependents();
-    griddep_wait();
-    __syncthreads();
     if (warp == kExpWarps - 1) {
-        // W_uv[h] lands during the merge, a bulk copy per row
-        if (lane == 0) mbar_arrive_expect_tx(bar, D * DC * 2);
+        // W_uv[h] lands during kernel 2's end and the merge, a bulk copy per row
+        if (lane == 0) {
+            mbar_init(bar, 1);
+            fence_barrier_init();
+            mbar_arrive_expect_tx(bar, D * DC * 2);
+            sm.missing = 0;
+        }
         __syncwarp();
         const __nv_bfloat16 *w = p.w_uv + h * p.w_uv_head;
         for (int v = lane; v < D; v += 32) bulk_load(smem_u32(&sm.w[v][0]), w + (size_t)v * DC, DC * 2, bar);
     }
+    griddep_launch_dependents();
+    griddep_wait();
+    __syncthreads();
     // merge the ranges: `wpr` warps share a token's ranges, a lane has 4 dims of every 128
     const int wpr = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;
     for (int r0 = 0; r0 < rows; r0 += kExpWarps / wpr) {
