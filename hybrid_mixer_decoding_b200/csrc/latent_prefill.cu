@@ -93,8 +93,8 @@ __device__ __forceinline__ int page_of(const PrefillParams &p, int b, int pos) {
 
 // ---- kernel 1: a warp per position ---------------------------------------------------------------
 __global__ void __launch_bounds__(256) latent_rows_kernel(const PrefillParams p, int span) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();  // not before: the next kernel reads W without waiting
     const int lane = threadIdx.x & 31, row_w = p.dc + kDR;
     const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int b = (int)(i / span), pos = (int)(i - (long long)b * span);
@@ -168,10 +168,11 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     const int n_kc = p.dc / 64, n_steps = (hb - ha) * STEPS;
     // a CTA's heads, in an order that begins elsewhere for every tile
     auto head_of = [&](int st) { return ha + (st / STEPS + tile) % (hb - ha); };
-    griddep_launch_dependents();
-    griddep_wait();  // the appended rows are kernel 1's
     const Seq s = seq_of(p, b);
-    if (pos0 >= s.total || n_steps <= 0) return;
+    if (pos0 >= s.total || n_steps <= 0) {
+        griddep_wait();
+        return;
+    }
     if (tid == 0) {
         for (int i = 0; i < SM::N_BARS; ++i)
             mbar_init(bar(i), i >= SM::B_READ && i < SM::B_READ + kExpAcc ? 4 : i == SM::B_MOVED ? 8 : 1);
@@ -190,6 +191,28 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
 
     if (warp == 8) {
         const bool lead = elect_one();
+        const int n_all = n_steps * n_kc;
+        int n = 0, w = 0, round = 0, st = 0, kc = 0, h = p.h0 + head_of(0);  // (no division per stage)
+        auto load_w = [&] {
+            const uint32_t dst = sb + SM::stage(w);
+            mbar_expect_if(lead, bar(SM::B_WFULL + w), SM::W_STAGE);
+            if (STEPS == 1 || st % 2 == 0)
+                tma_load_3d_if(lead, dst, &tmk, bar(SM::B_WFULL + w), kc * 64, 0, h);
+            if (STEPS == 1 || st % 2 == 1)
+                tma_load_3d_if(lead, dst + (STEPS == 1 ? D * 128 : 0), &tmv, bar(SM::B_WFULL + w), kc * 64, 0, h);
+            ++n;
+            if (++w == SM::NW) {
+                w = 0;
+                ++round;
+            }
+            if (++kc == n_kc) {
+                kc = 0;
+                h = p.h0 + head_of(++st);
+            }
+        };
+        while (n < SM::EARLY && n < n_all) load_w();
+        griddep_wait();  // the appended rows are kernel 1's
+        griddep_launch_dependents();
         // the tile's two pages of latent rows: blocks of 64 dims (a missing page's rows hold anything;
         // their results are stored as zeros)
         int pg[2];
@@ -204,21 +227,11 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
                 tma_load_2d_if(lead && pg[h] >= 0, sb + kc * kBlk + h * (kBlk / 2), &tmc,
                                bar(SM::B_A), kc * 64, pg[h] * kPT);
         bool ok = true;
-        int n = 0;
-        for (int st = 0; st < n_steps && ok; ++st) {
-            for (int kc = 0; kc < n_kc; ++kc, ++n) {
-                const int w = n % SM::NW;
-                if (n >= SM::NW) ok = wait_warp(lead, bar(SM::B_WFREE + w), (n / SM::NW - 1) & 1, abort_flag);
-                else if (n == SM::EARLY) ok = wait_warp(lead, bar(SM::B_MOVED), 0, abort_flag);
-                if (!ok) break;
-                const uint32_t dst = sb + SM::stage(w);
-                mbar_expect_if(lead, bar(SM::B_WFULL + w), SM::W_STAGE);
-                const int h = p.h0 + head_of(st);
-                if (STEPS == 1 || st % 2 == 0)
-                    tma_load_3d_if(lead, dst, &tmk, bar(SM::B_WFULL + w), kc * 64, 0, h);
-                if (STEPS == 1 || st % 2 == 1)
-                    tma_load_3d_if(lead, dst + (STEPS == 1 ? D * 128 : 0), &tmv, bar(SM::B_WFULL + w), kc * 64, 0, h);
-            }
+        while (n < n_all) {
+            if (round > 0) ok = wait_warp(lead, bar(SM::B_WFREE + w), (round - 1) & 1, abort_flag);
+            else if (n == SM::EARLY) ok = wait_warp(lead, bar(SM::B_MOVED), 0, abort_flag);
+            if (!ok) break;
+            load_w();
         }
         if (!ok && lead) {
             // the copies in flight land (bounded) before shared memory is released
@@ -234,13 +247,12 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         constexpr uint32_t ID = idesc_bf16(128, 128, 0, 0);
         auto wait = [&](int i, uint32_t parity) { wait_warp(lead, bar(i), parity, abort_flag); };
         wait(SM::B_MOVED, 0);
-        int n = 0;
+        int w = 0, round = 0;
         for (int st = 0; st < n_steps; ++st) {
             const int acc = st % kExpAcc;
             if (st >= kExpAcc) wait(SM::B_READ + acc, (st / kExpAcc - 1) & 1);
-            for (int kc = 0; kc < n_kc; ++kc, ++n) {
-                const int w = n % SM::NW;
-                wait(SM::B_WFULL + w, (n / SM::NW) & 1);
+            for (int kc = 0; kc < n_kc; ++kc) {
+                wait(SM::B_WFULL + w, round & 1);
                 tc_fence_after();
                 const Desc wd = d_w.at(SM::stage(w));
 #pragma unroll
@@ -249,6 +261,10 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
                                (kc > 0 || kk > 0) ? 1u : 0u);
                 umma_commit_if(lead, bar(SM::B_WFREE + w));
                 if (kc == n_kc - 1) umma_commit_if(lead, bar(SM::B_ACC + acc));
+                if (++w == SM::NW) {
+                    w = 0;
+                    ++round;
+                }
             }
         }
         if (lead) {
@@ -259,6 +275,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         __syncwarp();
     } else {
         // warps 0-3 store the even steps, 4-7 the odd ones; a lane has a position (its row of TMEM)
+        griddep_wait();  // the workspace may still be read by the kernel before
         const int quarter = warp & 3, pos = pos0 + quarter * 32 + lane;
         const bool live = pos < s.total && page_of(p, b, pos) >= 0;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
@@ -387,10 +404,12 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     const int qb = p.n_qb - 1 - (int)(blockIdx.x / (p.B * p.heads));
     const int b = bh / p.heads, hl = bh - b * p.heads, h = p.h0 + hl;
     griddep_launch_dependents();
-    griddep_wait();
     const Seq s = seq_of(p, b);
     const int t_first = qb * 2 * kTile, t_last = min(s.n, t_first + 2 * kTile) - 1;
-    if (t_first >= s.n) return;
+    if (t_first >= s.n) {
+        griddep_wait();
+        return;
+    }
     // key tiles of each query tile: up to its last row's position (none without rows)
     const int nt0 = uniform((s.prefix + min(t_last, t_first + kTile - 1)) / kTile + 1);
     const int nt1 = uniform(t_last >= t_first + kTile ? (s.prefix + t_last) / kTile + 1 : 0);
@@ -432,6 +451,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         if (out) atomicOr(&g_err, HMD_DEVWARN_RANGE);
         fence_proxy_async_smem();  // Q is read by the tensor cores
     }
+    griddep_wait();  // keys and values are kernel 2's
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
