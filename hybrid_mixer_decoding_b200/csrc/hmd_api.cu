@@ -430,6 +430,8 @@ size_t attn_decode_workspace_size(hmd_kind_t kind, int window, int B, int Hq, in
 }  // extern "C"
 
 namespace {
+constexpr long long kMaxLen = 1LL << 30;  // positions are ints, with room to round them up
+
 // The accumulated-weight rows of attn_verify_scored.
 struct WeightRows {
     float *w;
@@ -469,6 +471,7 @@ hmd_status_t attn_run(hmd_kind_t kind, int window, int ring_pages, int n_q, int 
     if (!aligned16(q) || !aligned16(new_k) || !aligned16(new_v) || !aligned16(k_pool) ||
         !aligned16(v_pool) || !aligned16(workspace))
         return fail(HMD_ERR_ARG);
+    if (weights && max_seq_len >= kMaxLen) return fail(HMD_ERR_UNSUPPORTED);
     const hmd::AttnPlan pl = hmd::attn_decode_plan(kind == HMD_SWA, window, rows ? n_rows : B, Hq,
                                                    Hkv, d, page_tokens, max_seq_len, n_q);
     const size_t need_ws = weights ? hmd::attn_scored_ws_bytes(n_q, B, Hq, Hkv, d, page_tokens,
@@ -536,7 +539,7 @@ hmd_status_t latent_bounds(int B, long long tokens, int H, int d, int d_c, int p
     // row coordinates, flat page counts and launch grids are 32-bit; heads and token blocks are
     // grid dimensions
     const long long pages = (max_len + page_tokens - 1) / page_tokens;
-    if ((long long)n_pages * page_tokens >= (1LL << 31) || B * pages >= (1LL << 31) ||
+    if (max_len >= kMaxLen || (long long)n_pages * page_tokens >= (1LL << 31) || B * pages >= (1LL << 31) ||
         tokens * H >= (1LL << 31) || tokens >= (1LL << 19) || H > 65535)
         return HMD_ERR_UNSUPPORTED;
     return HMD_OK;
@@ -589,7 +592,8 @@ hmd_status_t kv_cache_evict(int budget, int recent, int B, int Hkv, int d, int p
         (weights_out == weights && w_out_len != w_len))
         return fail(HMD_ERR_SHAPE);
     // grids of one block per (sequence, kv-head) and 64 rows, or 16 columns
-    if ((long long)B * Hkv * std::max<long long>(keep / 64 + 1, d / 16 + 1) >= (1LL << 31))
+    if (max_seq_len >= kMaxLen ||
+        (long long)B * Hkv * std::max<long long>(keep / 64 + 1, d / 16 + 1) >= (1LL << 31))
         return fail(HMD_ERR_UNSUPPORTED);
     if (!aligned16(k_pool) || !aligned16(v_pool)) return fail(HMD_ERR_ARG);
     hmd::EvictArgs a{};
@@ -727,7 +731,7 @@ hmd_status_t attn_latent_prefill(int B, int T, int H, int d, int d_c, int d_r, i
                                           w_uk_head, w_uv_head);
     if (st != HMD_OK) return fail(st);
     // positions, tensor-map rows and grids are 32-bit
-    if (span >= (1LL << 30) || (span / 128 + 1) * B * H >= (1LL << 31) ||
+    if ((span / 128 + 1) * B * H >= (1LL << 31) ||
         span * B >= (1LL << 31))
         return fail(HMD_ERR_UNSUPPORTED);
     if (!aligned16(q) || !aligned16(c) || !aligned16(w_uk) || !aligned16(w_uv) ||

@@ -954,7 +954,7 @@ struct Plan {
 Plan make_plan(int nq, int B, int H, int dc, int max_seq_len) {
     Plan pl;
     pl.n_groups = (int)(((long long)nq * H + kRows - 1) / kRows);
-    const long long pages = (long long)B * ((max_seq_len + kPT - 1) / kPT);
+    const long long pages = (long long)B * (((long long)max_seq_len + kPT - 1) / kPT);
     // one CTA per SM: the groups of one range run side by side and share its pages through L2
     pl.n_ranges = (int)std::min<long long>(std::max(1, device_sms() / pl.n_groups), pages);
     const size_t pieces = (size_t)(pl.n_ranges + B) * pl.n_groups;

@@ -20,6 +20,7 @@ def _scored(n_q=1, B=2, Hq=8, Hkv=2, d=128, pt=64, q=FAKE, pool=FAKE, n_pages=10
     (dict(q=None), ARG), (dict(w=None), ARG), (dict(pool=FAKE + 8), ARG), (dict(ws=None), ARG),
     (dict(n_q=0), SHAPE), (dict(Hq=7), SHAPE), (dict(w_len=639), SHAPE), (dict(n_slots=1), SHAPE),
     (dict(n_slots=-1, slots=FAKE), SHAPE), (dict(max_pages=9), SHAPE), (dict(ws_bytes=16), SHAPE),
+    (dict(max_pages=1 << 24, max_seq=1 << 30, w_len=1 << 30), UNSUP),
     (dict(d=96), UNSUP), (dict(n_q=5), UNSUP), (dict(pt=32, max_pages=20), UNSUP), (dict(B=0), OK)])
 def test_scored_refusals(bad, status):
     hmd.hmd_last_error()  # clear this thread's last status
@@ -48,6 +49,7 @@ def _evict(budget=64, recent=8, B=2, Hkv=2, d=128, pt=64, pool=FAKE, n_pages=100
     (dict(recent=-1), SHAPE), (dict(max_pages=9), SHAPE), (dict(budget=65), SHAPE),
     (dict(w_len=600), SHAPE), (dict(w_out_len=63), SHAPE), (dict(n_slots=1), SHAPE),
     (dict(dst=FAKE, dst_pages=9), SHAPE), (dict(w_out=FAKE, w_out_len=64), SHAPE),
+    (dict(max_pages=1 << 24, max_seq=1 << 30, w_len=1 << 30), UNSUP),
     (dict(d=256), UNSUP), (dict(pt=16, max_pages=40, dst_pages=4), UNSUP), (dict(B=0), OK)])
 def test_evict_refusals(bad, status):
     hmd.hmd_last_error()  # clear this thread's last status

@@ -27,7 +27,8 @@ def _decode(n_q=1, B=2, H=16, d=128, d_c=512, d_r=64, pt=64, scale=0.07, q=FAKE,
     (dict(uk_head=128 * 512 - 8), SHAPE), (dict(uv_head=128 * 512 + 4), SHAPE),
     (dict(ws_bytes=1000), SHAPE), (dict(d=96, uk_head=1 << 20), UNSUP), (dict(d_c=576), UNSUP),
     (dict(d_c=64), UNSUP), (dict(d_r=32), UNSUP), (dict(pt=32, max_pages=20), UNSUP),
-    (dict(n_pages=1 << 26), UNSUP), (dict(B=0), OK)])
+    (dict(n_pages=1 << 26), UNSUP), (dict(B=1, max_pages=1 << 24, max_seq=1 << 30), UNSUP),
+    (dict(B=0), OK)])
 def test_decode_refusals(bad, status):
     hmd.hmd_last_error()  # clear this thread's last status
     assert _decode(**bad) == status
