@@ -413,3 +413,42 @@ def test_offsets_beyond_32_bits():
     c.lens_list = [152, 110]
     check_prefill(c, qp, cp, prefill(c, qp, cp, [112, 70], [40, 40]), [112, 70], [40, 40])
     assert hmd.hmd_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("H,d,d_c,T", [(12, 128, 512, 300), (5, 64, 256, 150)])
+def test_inputs_written_just_before_calls_that_share_a_workspace(H, d, d_c, T):
+    """Weights, queries and rows written by the kernel before each call, calls one after another on one
+    workspace, eager and captured: as with a synchronisation between all of them."""
+    c = Latent([T + 1] * 2, H, d, d_c, seed=60)
+    ws = torch.empty(max(hmd.attn_latent_prefill_workspace_size(2, T, H, d, d_c, DR, PT, 0),
+                         c.workspace(1).numel()), dtype=torch.uint8, device="cuda")
+    sets = [(c.randn(H, d, d_c, scale=d_c ** -0.5), c.randn(H, d, d_c, scale=d_c ** -0.5),
+             c.randn(2, T, H, d + DR), c.randn(2, T, d_c + DR), *c.new(1)) for _ in range(3)]
+    q, rows, q1, row1 = (torch.empty_like(x) for x in sets[0][2:])
+    n = 9
+    outs = [(torch.empty(2, T, H, d, device="cuda", dtype=BF), torch.empty(2, 1, H, d, device="cuda", dtype=BF))
+            for _ in range(n)]
+
+    def chain(pause):
+        for i in range(n):
+            for dst, src in zip((c.w_uk, c.w_uv, q, rows, q1, row1), sets[i % 3]):
+                dst.copy_(src)
+            pause()
+            prefill(c, q, rows, o=outs[i][0], ws=ws)
+            pause()
+            c.decode(q1, row1, ws=ws, o=outs[i][1])
+            pause()
+
+    chain(torch.cuda.synchronize)
+    want = [[o.clone() for o in pair] for pair in outs]
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        chain(lambda: None)
+    for run in (lambda: chain(lambda: None), graph.replay, graph.replay):
+        for pair in outs:
+            for o in pair:
+                o.fill_(7.0)
+        run()
+        torch.cuda.synchronize()
+        for pair, ref in zip(outs, want):
+            assert all(torch.equal(o, r) for o, r in zip(pair, ref))
