@@ -27,7 +27,11 @@
 // Kernel 2 (combine): log-sum-exp merge of the splits into bf16 o.
 // Scored form (attn_verify_scored): the split kernel also stores every row's scaled scores, and
 // kernel 2 carries further blocks that turn them into softmax weights, which need the maximum and
-// sum over all splits, and add them up per key.
+// sum over all splits, and add them up per key. (Weights cannot be added up in one pass: a row's
+// maximum and sum are known only after its last key.) B = 32, Hq = 32, Hkv = 8, d = 128, 4096 to 8192
+// keys: 148 us, of which kernel 2 is 14 (817 MB of K, V and weights, 5.5 TB/s); n_q = 4, B = 16, 2048
+// to 4097 keys: 59 us (206 MB, 3.5 TB/s: the 16 rows' scores are another 50 MB through L2, and the
+// two launches' ends weigh more).
 // The step is HBM-bound (K and V are read once: ~4 flop per byte); the design goal is to keep
 // enough page copies in flight to stream at the HBM rate.
 #include <cuda.h>
@@ -95,7 +99,8 @@ struct Item {
 __device__ __forceinline__ Item item_info(const SplitParams &p, int i) {
     Item it;
     // the scored form starts every sequence's first range before any second one: a ragged batch's
-    // short and empty ranges are the last to start
+    // short and empty ranges are the last to start (n_q = 4, B = 16, 2048 to 4097 keys: 63 us with a
+    // sequence's ranges side by side, 59 us so; B = 32, 4096 to 8192: 152 and 148 us)
     const int units = p.ws_s ? p.B * p.Hkv : 1, unit = p.ws_s ? i % units : i / p.n_splits;
     it.split = p.ws_s ? i / units : i % p.n_splits;
     it.g = unit % p.Hkv;
@@ -478,9 +483,11 @@ __global__ void __launch_bounds__(D) attn_combine_kernel(const float *ws_ml, con
 
 // Kernel 2 of the scored form: one launch, two kinds of blocks of 128 threads. The first
 // n_row_blocks merge the splits of 128 / D query rows into o, as attn_combine_kernel does; the
-// others each take one (sequence, kv-head) and kScoreKeys keys, four per thread: with M_r and l_r the maximum and
-// sum over all splits, key j received sum_r 2^(s_rj - M_r) / l_r from the group's rows, which is
-// added to its accumulated weight (a new token's slot starts from 0). Every key has one thread
+// others each take one (sequence, kv-head) and kScoreKeys keys, four per thread: with M_r and l_r the
+// maximum and sum over all splits, key j received sum_r 2^(s_rj - M_r) / l_r from the group's rows, which
+// is added to its accumulated weight (a new token's slot starts from 0). Bound by latency: the rows'
+// scores are asked for before the statistics, which all rows form at once, eight rows in flight (16
+// rows: 19 us with four in flight after one row's statistics at a time, 12.5 us so). Every key has one thread
 // and its rows are added in order, so results do not depend on scheduling. A sequence whose
 // length was refused or whose range gave up keeps its weights.
 constexpr int kScoreKeys = 512;
@@ -645,9 +652,9 @@ bool make_pool_map(CUtensorMap *m, void *pool, int n_pages, int Hkv, int d) {
 
 // Most pages of a key range of the scored form. One wave of ranges as long as the longest sequence
 // leaves SMs idle once the shorter sequences of a batch are done; shorter ranges are dealt out as
-// SMs come free. B = 32, Hkv = 8, sequences of 4096 to 8192: 171 us with whole sequences, 148 to
-// 157 us with 8 to 32 pages; B = 16, n_q = 4, 2048 to 4097: 69 us with 32 or 33 pages, 73 with 24,
-// 82 with 8. At most 256 ranges a sequence, as in the plain form.
+// SMs come free. B = 32, Hkv = 8, sequences of 4096 to 8192: 163 us with whole sequences, 148 to
+// 161 us with 32 to 8 pages; B = 16, n_q = 4, 2048 to 4097: 57 to 59 us with 24 to 33 pages, 70 with
+// 16, 76 with 8. At most 256 ranges a sequence, as in the plain form.
 constexpr int kScoredRange = 32;
 int scored_max_range(int max_seq_len) {
     return std::max(kScoredRange, ((max_seq_len + kPT - 1) / kPT + (int)kMaxSplits - 1) / (int)kMaxSplits);
