@@ -96,13 +96,14 @@ struct Item {
     bool bad_len;
 };
 
+template <bool SCORED>
 __device__ __forceinline__ Item item_info(const SplitParams &p, int i) {
     Item it;
     // the scored form starts every sequence's first range before any second one: a ragged batch's
     // short and empty ranges are the last to start (n_q = 4, B = 16, 2048 to 4097 keys: 63 us with a
     // sequence's ranges side by side, 59 us so; B = 32, 4096 to 8192: 152 and 148 us)
-    const int units = p.ws_s ? p.B * p.Hkv : 1, unit = p.ws_s ? i % units : i / p.n_splits;
-    it.split = p.ws_s ? i / units : i % p.n_splits;
+    const int units = p.B * p.Hkv, unit = SCORED ? i % units : i / p.n_splits;
+    it.split = SCORED ? i / units : i % p.n_splits;
     it.g = unit % p.Hkv;
     it.r = unit / p.Hkv;
     it.b = p.rows ? p.rows[it.r] : it.r;
@@ -178,7 +179,7 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     }
     griddep_launch_dependents();
     griddep_wait();  // q, the new token, the pools and the tables may come from the previous kernel
-    const Item it = item_info(p, blockIdx.x);
+    const Item it = item_info<SCORED>(p, blockIdx.x);
     if (tid == 0 && it.bad_len && it.split == 0) atomicOr(&g_err, HMD_DEVERR_SEQLEN);
 
     // ---- producer (warp 0, warp-uniform calls; lane 0 issues) -----------------------------
@@ -681,7 +682,7 @@ cudaError_t launch_d(const AttnDecodeArgs &a, const AttnPlan &plan, cudaStream_t
     if (!make_pool_map(&tmk, a.k_pool, a.n_pages, a.Hkv, D) ||
         !make_pool_map(&tmv, a.v_pool, a.n_pages, a.Hkv, D))
         return cudaErrorInvalidValue;
-    SplitParams p;
+    SplitParams p{};
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.new_k = static_cast<const __nv_bfloat16 *>(a.new_k);
     p.new_v = static_cast<const __nv_bfloat16 *>(a.new_v);
