@@ -375,14 +375,20 @@ constexpr int kAttThreads = kSoftmax + 64;     // + the MMA warp (8) and the TMA
 template <int D>
 struct AttendSmem {
     static constexpr int KB = D / 64 + 1, VB = D / 64, NB = KB + VB;  // blocks of a key tile
-    static constexpr int NR = 8;                                      // blocks in the ring
+    // Blocks in the ring: what is left of shared memory, and (D = 64) few enough that a wait for a
+    // tile's products cannot be overtaken by those of two tiles later.
+    static constexpr int NR = D == 128 ? 8 : 5;
     static constexpr uint32_t Q_TILE = KB * kBlk;
     static constexpr uint32_t OFF_Q = 0, OFF_R = 2 * Q_TILE;
     static constexpr uint32_t OFF_BAR = OFF_R + NR * kBlk;
     static constexpr uint32_t BYTES = OFF_BAR + 256 + 1024;
     static constexpr uint32_t ALLOC = BYTES > 118784 ? BYTES : 118784;  // one CTA per SM
-    static constexpr int B_FULL = 0, B_FREE = NR, B_S = 2 * NR, B_P = B_S + 2, B_O = B_P + 2,
-                         B_END = B_O + 2, N_BARS = B_END + 1;
+    // B_S, B_P, B_O: S_j complete, P_j written, O_j complete; B_SR: S read. Keys are free once the last
+    // query tile's S is complete, values once its O is.
+    static constexpr int B_FULL = 0, B_S = NR, B_P = B_S + 2, B_O = B_P + 2, B_SR = B_O + 2,
+                         B_END = B_SR + 1, N_BARS = B_END + 1;
+    // in TMEM: O_0, O_1, S (both query tiles' in turn), P_0, P_1
+    static constexpr uint32_t T_O = 0, T_S = 256, T_P = 384;
 };
 static_assert(AttendSmem<128>::ALLOC <= 232448, "shared memory per CTA");
 
@@ -417,13 +423,13 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     const int nt1 = uniform(t_last >= t_first + kTile ? (s.prefix + t_last) / kTile + 1 : 0);
     const int n_tiles = max(nt0, nt1);
     if (tid == 0) {
-        for (int i = 0; i < SM::N_BARS; ++i) mbar_init(bar(i), (i == SM::B_P || i == SM::B_P + 1) ? 4 : 1);
+        for (int i = 0; i < SM::N_BARS; ++i) mbar_init(bar(i), (i == SM::B_P || i == SM::B_P + 1 || i == SM::B_SR) ? 4 : 1);
         fence_barrier_init();
         *abort_flag = 0;
     }
     if (warp == 8) {
         __syncwarp();
-        tmem_alloc(smem_u32(tmem_slot), 512);  // query tile j: S_j (and P_j) at 256 j, O_j at 256 j + 128
+        tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
     // Q rows -> shared memory as fp16, one row per softmax thread
@@ -460,24 +466,38 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
     if (warp == 9) {
-        // ===== copies: block n of the stream of tiles into slot n % NR (the warp converged) =========
+        // ===== copies: the blocks of K_0, K_1, V_0, K_2, V_1, ... in the order of their use, block n into
+        // slot n % NR (the warp converged) ========================================================
         const bool lead = elect_one();
-        bool ok = true;
-        int n = 0;
-        for (int i = 0; i < n_tiles && ok; ++i) {
-#pragma unroll
-            for (int u = 0; u < NB; ++u) {
-                if (!ok) break;
-                const int slot = n % NR;
-                if (n >= NR) ok = wait_warp(lead, bar(SM::B_FREE + slot), (n / NR - 1) & 1, abort_flag);
-                if (!ok) break;
-                const uint32_t dst = sb + SM::OFF_R + slot * kBlk, fb = bar(SM::B_FULL + slot);
-                mbar_expect_if(lead, fb, kBlk);
-                if (u < KB - 1) tma_load_3d_if(lead, dst, &tmk, fb, u * 64, i * kTile, bh);
-                else if (u == KB - 1) tma_load_3d_if(lead, dst, &tmr, fb, 0, i * kTile, b);
-                else tma_load_3d_if(lead, dst, &tmv, fb, (u - KB) * 64, i * kTile, bh);
-                ++n;
+        const int last = nt1 > 0;
+        struct Place {  // block u of K_g, or of K_g and V_(g-1)
+            int g = 0, u = 0;
+            __device__ void next(int n_tiles) {
+                if (++u == (g == 0 ? KB : g < n_tiles ? NB : VB)) {
+                    u = 0;
+                    ++g;
+                }
             }
+            __device__ bool key(int n_tiles) const { return g < n_tiles && u < KB; }
+        } at, old;  // the block to load, the one whose slot it takes
+        bool ok = true;
+        int n = 0, slot = 0;
+        for (; n < n_tiles * NB; ++n) {
+            if (n >= NR) {
+                const bool key = old.key(n_tiles);
+                ok = wait_warp(lead, bar((key ? SM::B_S : SM::B_O) + last), (key ? old.g : old.g - 1) & 1, abort_flag);
+                if (!ok) break;
+                old.next(n_tiles);
+            }
+            const uint32_t dst = sb + SM::OFF_R + slot * kBlk, fb = bar(SM::B_FULL + slot);
+            mbar_expect_if(lead, fb, kBlk);
+            const bool key = at.key(n_tiles);
+            const int v = at.u - (at.g < n_tiles ? KB : 0);
+            if (key && at.u < KB - 1) tma_load_3d_if(lead, dst, &tmk, fb, at.u * 64, at.g * kTile, bh);
+            else if (key) tma_load_3d_if(lead, dst, &tmr, fb, 0, at.g * kTile, b);
+            else tma_load_3d_if(lead, dst, &tmv, fb, v * 64, (at.g - 1) * kTile, bh);
+            at.next(n_tiles);
+            if (++slot == NR) slot = 0;
         }
         if (!ok && lead) {
             // the copies in flight land (bounded) before shared memory is released
@@ -487,40 +507,44 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         }
         __syncwarp();
     } else if (warp == 8) {
-        // ================= products: O_0(i), S_0(i+1), O_1(i), S_1(i+1) (the warp converged) ===
+        // ===== products: S_0(i+1), O_0(i), S_1(i+1), O_1(i) (the warp converged). A tile's scores are
+        // complete before its softmax is done with the tile before, so both softmax groups and the tensor
+        // core always have work; one S serves both, since it is read into registers at once =======
         const bool lead = elect_one();
         const Desc d_q(smem_desc_sw128(sb + SM::OFF_Q, 16, 1024));
         const Desc d_k(smem_desc_sw128(sb + SM::OFF_R, 16, 1024));
         const Desc d_v(smem_desc_sw128(sb + SM::OFF_R, kBlk, 1024));
         constexpr uint32_t ID_S = idesc_f16(128, kTile, 0, 0);
         constexpr uint32_t ID_O = idesc_f16(128, D, 0, 1), ID_O64 = idesc_f16(128, 64, 0, 1);
-        // lanes 0 .. count - 1 wait for blocks n .. n + count - 1, lane `count` for P of query tile j
-        // (j < 0: for blocks only)
-        auto wait_for = [&](int n, int count, int j, int i) {
+        int n_s = 0;  // scores issued
+        // lanes 0 .. count - 1 wait for blocks n .. n + count - 1 of the stream, lane `count` for barrier i
+        // (i < 0: for blocks only)
+        auto wait_for = [&](int n, int count, int i, int parity) {
             const int u = n + lane;
             const bool block = lane < count;
-            wait_warp(block || (lane == count && j >= 0), block ? bar(SM::B_FULL + u % NR) : bar(SM::B_P + j),
-                      (block ? u / NR : i) & 1, abort_flag);
+            wait_warp(block || (lane == count && i >= 0), bar(block ? SM::B_FULL + u % NR : max(i, 0)),
+                      (block ? u / NR : parity) & 1, abort_flag);
             tc_fence_after();
         };
-        auto free_blocks = [&](int n, int count) {
-            for (int u = n; u < n + count; ++u) umma_commit_if(lead, bar(SM::B_FREE + u % NR));
-        };
-        auto issue_s = [&](int j, int i) {  // S_j = Q_j K_i^T
+        auto issue_s = [&](int j, int i) {  // S = Q_j K_i^T
+            const int n = i == 0 ? 0 : i * NB - VB;
+            wait_for(n, j == 0 || i >= nt0 ? KB : 0, n_s > 0 ? SM::B_SR : -1, n_s - 1);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                const Desc k = d_k.at(((uint32_t)(i * NB + kb) % NR) * kBlk);
+                const Desc k = d_k.at(((uint32_t)(n + kb) % NR) * kBlk);
                 const Desc q = d_q.at(j * SM::Q_TILE + kb * kBlk);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_if(lead, tmem + 256 * j, q.at(kk * 32), k.at(kk * 32), ID_S,
-                            (kb > 0 || kk > 0) ? 1u : 0u);
+                    umma_if(lead, tmem + SM::T_S, q.at(kk * 32), k.at(kk * 32), ID_S, (kb > 0 || kk > 0) ? 1u : 0u);
             }
             umma_commit_if(lead, bar(SM::B_S + j));
+            ++n_s;
         };
         auto issue_o = [&](int j, int i) {  // O_j (+)= P_j V_i, P_j from TMEM
-            const uint32_t slot = (uint32_t)(i * NB + KB) % NR;
-            const uint32_t o = tmem + 256 * j + 128, pj = tmem + 256 * j;
+            const int n = (i + 1) * NB - VB + (i + 1 < n_tiles ? KB : 0);
+            wait_for(n, j == 0 || i >= nt0 ? VB : 0, SM::B_P + j, i);
+            const uint32_t slot = (uint32_t)n % NR;
+            const uint32_t o = tmem + SM::T_O + 128 * j, pj = tmem + SM::T_P + 64 * j;
             const Desc v = d_v.at(slot * kBlk);
             const uint32_t more = i > 0 ? 1u : 0u;
             if (VB == 1 || slot + 1 < NR) {
@@ -535,25 +559,13 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                 for (int kk = 0; kk < kTile / 16; ++kk)
                     umma_ts_if(lead, o + 64, pj + 8 * kk, d_v.at(kk * 2048), ID_O64, kk > 0 ? 1u : more);
             }
+            umma_commit_if(lead, bar(SM::B_O + j));
         };
-        wait_for(0, KB, -1, 0);
-        issue_s(0, 0);
-        if (nt1 > 0) issue_s(1, 0);
-        free_blocks(0, KB);
-        for (int i = 0; i < n_tiles; ++i) {
-#pragma unroll 1
-            for (int j = 0; j < 2; ++j) {
-                const int nt = j ? nt1 : nt0;
-                if (j == 0 || i < nt) wait_for(i * NB + KB, j == 0 ? VB : 0, i < nt ? j : -1, i);
-                if (i < nt) issue_o(j, i);
-                if (i == nt - 1) umma_commit_if(lead, bar(SM::B_O + j));
-                if (j == 1) free_blocks(i * NB + KB, VB);
-                if (i + 1 < n_tiles) {
-                    if (j == 0) wait_for((i + 1) * NB, KB, -1, 0);
-                    if (i + 1 < nt) issue_s(j, i + 1);
-                    if (j == 1) free_blocks((i + 1) * NB, KB);
-                }
-            }
+        for (int i = -1; i < n_tiles; ++i) {
+            if (i + 1 < nt0) issue_s(0, i + 1);
+            if (i >= 0 && i < nt0) issue_o(0, i);
+            if (i + 1 < nt1) issue_s(1, i + 1);
+            if (i >= 0 && i < nt1) issue_o(1, i);
         }
         if (lead) {
             if (*abort_flag) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
@@ -565,7 +577,8 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         // ================= softmax: query tile qt, one thread per row ==========================
         const int nt = qt ? nt1 : nt0;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t s_col = lane_base + 256 * qt, o_col = s_col + 128;
+        const uint32_t s_col = lane_base + SM::T_S, p_col = lane_base + SM::T_P + 64 * qt,
+                       o_col = lane_base + SM::T_O + 128 * qt;
         const bool lead = elect_one();
         float m_base = -INFINITY, l_run = 0.f;
         for (int i = 0; i < nt; ++i) {
@@ -580,6 +593,9 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                 for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(r[j]);
                 tmem_ld64(s_col + 64, r);
                 tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(SM::B_SR));  // S may be the other query tile's now
 #pragma unroll
                 for (int j = 0; j < 64; ++j) x[64 + j] = __uint_as_float(r[j]);
             }
@@ -605,13 +621,12 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                 l_run *= f;
             }
             const float mu = (m_base == -INFINITY) ? 0.f : m_base;
-            __syncwarp();  // the row-dependent branches above rejoin before the TMEM stores
+            uint32_t pk[kTile / 32][16];  // P, two keys a word
             {
                 const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nmu2 = f2(-mu, -mu);
                 uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < kTile / 32; ++c) {
-                    uint32_t pk[16];
 #pragma unroll
                     for (int u = 0; u < 16; ++u) {
                         const uint64_t y = f2_fma(f2(x[c * 32 + 2 * u], x[c * 32 + 2 * u + 1]), sc2, nmu2);
@@ -626,17 +641,18 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                         acc[u & 1] = f2_add(acc[u & 1], e);
                         float e0, e1;
                         f2_split(e, e0, e1);
-                        pk[u] = pack_f16x2(e0, e1);
+                        pk[c][u] = pack_f16x2(e0, e1);
                     }
-                    tmem_st16(s_col + 16 * c, pk);
                 }
                 float a0, a1, b0, b1;
                 f2_split(acc[0], a0, a1);
                 f2_split(acc[1], b0, b1);
                 l_run += (a0 + a1) + (b0 + b1);
             }
-            // the row's earlier output to the new base (the product into it is done: S_j(i) was
-            // issued after O_j(i-1))
+            // the product before has read P and added to O: the row's earlier output to the new base, then P
+            if (i > 0) wait_warp(lead, bar(SM::B_O + qt), (i - 1) & 1, abort_flag);
+            tc_fence_after();
+            __syncwarp();  // the row-dependent branches above rejoin before the TMEM accesses
             if (__any_sync(0xffffffffu, move) && i > 0) {
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -648,12 +664,14 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                     tmem_st32(o_col + 32 * c, r);
                 }
             }
+#pragma unroll
+            for (int c = 0; c < kTile / 32; ++c) tmem_st16(p_col + 16 * c, pk[c]);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(SM::B_P + qt));
         }
-        wait_warp(lead, bar(SM::B_O + qt), 0, abort_flag);
+        wait_warp(lead, bar(SM::B_O + qt), (nt - 1) & 1, abort_flag);
         const bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
         if (ok) {
             tc_fence_after();
