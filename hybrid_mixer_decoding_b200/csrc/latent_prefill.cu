@@ -384,9 +384,10 @@ struct AttendSmem {
     static constexpr uint32_t BYTES = OFF_BAR + 256 + 1024;
     static constexpr uint32_t ALLOC = BYTES > 118784 ? BYTES : 118784;  // one CTA per SM
     // B_S, B_P, B_O: S_j complete, P_j written, O_j complete; B_SR: S read. Keys are free once the last
-    // query tile's S is complete, values once its O is.
-    static constexpr int B_FULL = 0, B_S = NR, B_P = B_S + 2, B_O = B_P + 2, B_SR = B_O + 2,
-                         B_END = B_SR + 1, N_BARS = B_END + 1;
+    // query tile's S is complete (all but their last block a little earlier, at B_K: a tile's values
+    // take the place of its first keys), values once its O is.
+    static constexpr int B_FULL = 0, B_S = NR, B_P = B_S + 2, B_O = B_P + 2, B_SR = B_O + 2, B_K = B_SR + 1,
+                         B_END = B_K + 1, N_BARS = B_END + 1;
     // in TMEM: O_0, O_1, S (both query tiles' in turn), P_0, P_1
     static constexpr uint32_t T_O = 0, T_S = 256, T_P = 384;
 };
@@ -465,11 +466,11 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
+    const int last = nt1 > 0;  // the last query tile
     if (warp == 9) {
         // ===== copies: the blocks of K_0, K_1, V_0, K_2, V_1, ... in the order of their use, block n into
         // slot n % NR (the warp converged) ========================================================
         const bool lead = elect_one();
-        const int last = nt1 > 0;
         struct Place {  // block u of K_g, or of K_g and V_(g-1)
             int g = 0, u = 0;
             __device__ void next(int n_tiles) {
@@ -485,7 +486,8 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         for (; n < n_tiles * NB; ++n) {
             if (n >= NR) {
                 const bool key = old.key(n_tiles);
-                ok = wait_warp(lead, bar((key ? SM::B_S : SM::B_O) + last), (key ? old.g : old.g - 1) & 1, abort_flag);
+                const int free = !key ? SM::B_O + last : old.u < KB - 1 ? SM::B_K : SM::B_S + last;
+                ok = wait_warp(lead, bar(free), (key ? old.g : old.g - 1) & 1, abort_flag);
                 if (!ok) break;
                 old.next(n_tiles);
             }
@@ -536,6 +538,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     umma_if(lead, tmem + SM::T_S, q.at(kk * 32), k.at(kk * 32), ID_S, (kb > 0 || kk > 0) ? 1u : 0u);
+                if (kb == KB - 2) umma_commit_if(lead && j == last, bar(SM::B_K));
             }
             umma_commit_if(lead, bar(SM::B_S + j));
             ++n_s;
