@@ -23,11 +23,11 @@
 // second product, so that its accumulator fits TMEM beside the queries, and only pages are left in
 // shared memory: three of 72 KiB are in flight or in use, which is what covers HBM's latency (two, with
 // the queries in shared memory as well, reached 4.5 TB/s). Warp-specialised: warp 4 streams pages
-// by TMA (units of 128 dims, each freed as soon as its product is done), warp 5 issues the products,
-// warps 0-3 are the softmax. O^T accumulates at an exponent base per row that moves only when the
+// by TMA (units of 128 dims, each freed as soon as its product is done), warps 5 and 6 issue the two
+// products, warps 0-3 are the softmax. O^T accumulates at an exponent base per row that moves only when the
 // row's scores exceed it by more than 2^8 (then O^T is rescaled in TMEM). B = 32, 32 heads, 4096 to
 // 8192 keys: 48 us, 226 MB, 4.7 TB/s (after the first pages at the rate of HBM; its start and the wait
-// for kernel 1 are 7 us). With 96 rows a sequence (three groups, B = 16, 2048 to 4097 keys) 35 us,
+// for kernel 1 are 7 us). With 96 rows a sequence (three groups, B = 16, 2048 to 4097 keys) 34 us,
 // bound by the tensor core: a page costs 36 products of 48 cycles (N = 64) and 16 of 40 for 32 rows.
 // Kernel 3 (merge and expand), one CTA per (head, 16 or 32 tokens): joins the ranges' partial sums
 // while W_uv[h] is copied to shared memory (asked for while kernel 2 ends: 69.6 -> 67.8 us for the batch
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kAbsThreads) latent_absorb_kernel(const Latent
 }
 
 // ---- kernel 2 ----------------------------------------------------------------------------------
-constexpr int kAttThreads = 192;
+constexpr int kAttThreads = 224;  // softmax (warps 0-3), copies (4), scores (5), outputs (6)
 // Shared memory for d_c = 128 * NP: a ring of page slots, P, barriers. A page is NP units of 128 dims
 // (two blocks) and one of the shared part (one block); a sequence's queries pass through a slot too.
 template <int NP>
@@ -310,8 +310,8 @@ struct AttSmem {
     static constexpr int B_SR = B_S + 1;   // scores read (two warps)
     static constexpr int B_P = B_SR + 1;   // weights written (four warps)
     static constexpr int B_O = B_P + 1;    // the page's output product done
-    static constexpr int B_END = B_O + 1;  // everything issued is done (teardown)
-    static constexpr int N_BARS = B_END + 1;
+    static constexpr int B_END = B_O + 1;  // everything issued is done (teardown), one per issuing warp
+    static constexpr int N_BARS = B_END + 2;
     static_assert(N_BARS * 8 <= 512, "barriers");
 };
 static_assert(AttSmem<4>::ALLOC <= 232448, "shared memory per CTA");
@@ -472,85 +472,41 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
         }
         __syncwarp();
     } else if (warp == 5) {
-        // ================= products, whichever is ready first (the warp converged) ===========
+        // ================= scores (the warp converged) =========================================
         const bool lead = elect_one();
-        const Desc d_k(smem_desc_sw128(sb, 16, 1024));    // keys x dims
-        const Desc d_v(smem_desc_sw128(sb, kBlk, 1024));  // dims x keys
-        const Desc d_p(smem_desc_sw128(sb + SM::OFF_P, 16, 1024));
+        const Desc d_k(smem_desc_sw128(sb, 16, 1024));  // keys x dims
         constexpr uint32_t ID_S = idesc_bf16(128, kPT, 0, 0);
-        constexpr uint32_t ID_O = idesc_bf16(128, kRows, 1, 0);
-        int s = 0, pv = 0, seg = 0;  // pages of which the scores, the output product are issued
-        Walk ws = w, wp = w;         // their sequences
-        int ks = 1, kp = 1;          // their items in the ring: the queries come before a sequence's pages
+        Walk ws = w;
+        int ks = 1, seg = 0;  // items in the ring: the queries come before a sequence's pages
         bool ok = true;
-        unsigned long long t0 = 0;
-        while (pv < n_pages) {
-            bool moved = false;
-            if (pv < s && mbar_test_warp(lead, bar(SM::B_P), pv & 1)) {
-                // O^T += C^T P^T, unit by unit; each unit's slot is free after it
-                tc_fence_after();
-                const int st = kp % NS;
-                const bool fresh = __all_sync(0xffffffffu, wp.at == wp.seg_begin);
-                const Desc v = d_v.at(st * PAGE);
+        for (int s = 0; s < n_pages; ++s) {
+            // S = [q~hi ; q~lo] C^T once the page has landed (lane u asks for unit u), the scores before
+            // have been read and, for a new sequence, its queries are in place
+            const int st = ks % NS;
+            const bool first = ws.at == ws.seg_begin;
+            const bool asks = lane < NU || (lane == NU && s > 0) || (lane == NU + 1 && first);
+            const uint32_t b = lane < NU ? full(st, lane) : lane == NU ? bar(SM::B_SR) : bar(SM::B_Q);
+            const uint32_t parity = lane < NU ? (ks / NS) & 1 : lane == NU ? (s - 1) & 1 : seg & 1;
+            ok = wait_warp(asks, b, parity, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const Desc kd = d_k.at(st * PAGE);
 #pragma unroll
-                for (int u = 0; u < NP; ++u) {
+            for (int v = 0; v < NU; ++v) {
+                const int u = v == 0 ? NP : v - 1;  // the shared part's slot is free first
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_if(lead, tmem + kTmemO + u * kRows, v.at(u * 2 * kBlk + kk * 2048),
-                                d_p.at(kk * 32), ID_O, (fresh && kk == 0) ? 0u : 1u);
-                    umma_commit_if(lead, free_(st, u));
-                }
-                umma_commit_if(lead, bar(SM::B_O));
-                ++kp;
-                ++pv;
-                if (__all_sync(0xffffffffu, ++wp.at == wp.seg_end && wp.at < end)) {
-                    wp.seek(p, end);
-                    ++kp;
-                }
-                moved = true;
-            } else if (s < n_pages && s <= pv + 1) {
-                // S = [q~hi ; q~lo] C^T once the page has landed (lane u asks for unit u), the scores
-                // before have been read and, for a new sequence, its queries are in place
-                const int st = ks % NS;
-                const bool first = ws.at == ws.seg_begin;
-                const bool asks = lane < NU || (lane == NU && s > 0) || (lane == NU + 1 && first);
-                const uint32_t b = lane < NU ? full(st, lane) : lane == NU ? bar(SM::B_SR) : bar(SM::B_Q);
-                const uint32_t parity = lane < NU ? (ks / NS) & 1 : lane == NU ? (s - 1) & 1 : seg & 1;
-                if (mbar_test_warp(asks, b, parity)) {
-                    tc_fence_after();
-                    const Desc kd = d_k.at(st * PAGE);
-#pragma unroll
-                    for (int v = 0; v < NU; ++v) {
-                        const int u = v == 0 ? NP : v - 1;  // the shared part's slot is free first
-#pragma unroll
-                        for (int kk = 0; kk < (u == NP ? 4 : 8); ++kk)
-                            umma_ts_if(lead, tmem + kTmemS, tmem + kTmemQ + u * 64 + kk * 8,
-                                       kd.at(u * 2 * kBlk + (kk >> 2) * kBlk + (kk & 3) * 32), ID_S,
-                                       (v > 0 || kk > 0) ? 1u : 0u);
-                        if (u == NP) umma_commit_if(lead, free_(st, NP));
-                    }
-                    umma_commit_if(lead, bar(SM::B_S));
-                    ++ks;
-                    ++s;
-                    if (__all_sync(0xffffffffu, ++ws.at == ws.seg_end && ws.at < end)) {
-                        ws.seek(p, end);
-                        ++ks;
-                        ++seg;
-                    }
-                    moved = true;
-                }
+                for (int kk = 0; kk < (u == NP ? 4 : 8); ++kk)
+                    umma_ts_if(lead, tmem + kTmemS, tmem + kTmemQ + u * 64 + kk * 8,
+                               kd.at(u * 2 * kBlk + (kk >> 2) * kBlk + (kk & 3) * 32), ID_S,
+                               (v > 0 || kk > 0) ? 1u : 0u);
+                if (u == NP) umma_commit_if(lead, free_(st, NP));
             }
-            if (moved) {
-                t0 = 0;
-            } else {
-                const unsigned long long now = globaltimer_ns();
-                if (t0 == 0) t0 = now;
-                const bool late = now - t0 > kWaitLimitNs;
-                if (late) *abort_flag = 1;
-                if (__any_sync(0xffffffffu, late || *abort_flag)) {
-                    ok = false;
-                    break;
-                }
+            umma_commit_if(lead, bar(SM::B_S));
+            ++ks;
+            if (__all_sync(0xffffffffu, ++ws.at == ws.seg_end && ws.at < end)) {
+                ws.seek(p, end);
+                ++ks;
+                ++seg;
             }
         }
         if (lead) {
@@ -558,6 +514,45 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
             // every product is done before TMEM and shared memory go (bounded)
             umma_commit(bar(SM::B_END));
             (void)mbar_wait_bounded(bar(SM::B_END), 0);
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ===== outputs (the warp converged), issued beside the scores: 52 products and 7 commits a page
+        // are more than one warp issues in the tensor core's time =================================
+        const bool lead = elect_one();
+        const Desc d_v(smem_desc_sw128(sb, kBlk, 1024));  // dims x keys
+        const Desc d_p(smem_desc_sw128(sb + SM::OFF_P, 16, 1024));
+        constexpr uint32_t ID_O = idesc_bf16(128, kRows, 1, 0);
+        Walk wp = w;
+        int kp = 1;
+        bool ok = true;
+        for (int pv = 0; pv < n_pages; ++pv) {
+            ok = wait_warp(lead, bar(SM::B_P), pv & 1, abort_flag);
+            if (!ok) break;
+            // O^T += C^T P^T, unit by unit; each unit's slot is free after it
+            tc_fence_after();
+            const int st = kp % NS;
+            const bool fresh = __all_sync(0xffffffffu, wp.at == wp.seg_begin);
+            const Desc v = d_v.at(st * PAGE);
+#pragma unroll
+            for (int u = 0; u < NP; ++u) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_if(lead, tmem + kTmemO + u * kRows, v.at(u * 2 * kBlk + kk * 2048),
+                            d_p.at(kk * 32), ID_O, (fresh && kk == 0) ? 0u : 1u);
+                umma_commit_if(lead, free_(st, u));
+            }
+            umma_commit_if(lead, bar(SM::B_O));
+            ++kp;
+            if (__all_sync(0xffffffffu, ++wp.at == wp.seg_end && wp.at < end)) {
+                wp.seek(p, end);
+                ++kp;
+            }
+        }
+        if (lead) {
+            if (!ok) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+            umma_commit(bar(SM::B_END + 1));
+            (void)mbar_wait_bounded(bar(SM::B_END + 1), 0);
         }
         __syncwarp();
     } else {
