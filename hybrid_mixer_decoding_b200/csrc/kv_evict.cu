@@ -38,7 +38,7 @@ constexpr int kChooseThreads = 1024;
 constexpr int kWarps = kChooseThreads / 32;
 constexpr int kBins = 2048;           // 11 bits a digit
 constexpr int kCacheKeys = 49152;     // weights held in shared memory: 192 KiB
-constexpr int kMaxRanks = 8;          // CTAs of a cluster
+constexpr int kMaxRanks = 8;          // CTAs of a cluster (of 16, few fit at once: 58 us instead of 24)
 constexpr int kShare = 4096;          // a CTA of a cluster has at least this many entries
 constexpr int kSms = 148;
 constexpr int kMoveThreads = 256;
