@@ -229,21 +229,6 @@ __global__ void __launch_bounds__(kAbsThreads) latent_absorb_kernel(const Latent
             *reinterpret_cast<uint4 *>(img(tok, h, p.dc + c, true)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
-    if (h == 0 && cc == n_cols - 1) {
-        // rows of the last group that belong to no query: zero (16-byte chunks of every block)
-        const int pad0 = p.nq * p.H, n_pad = p.n_groups * kRows - pad0, chunks = (p.dc / 64 + 1) * 8;
-        for (int r = 0; r < rows && n_pad; ++r) {
-            const int tok = tok0 + r, b = tok / p.nq;
-            if (tok != b * p.nq) continue;
-            uint8_t *base = p.q_img + ((size_t)b * p.n_groups + p.n_groups - 1) * img_bytes;
-            for (int idx = tid; idx < n_pad * 2 * chunks; idx += kAbsThreads) {
-                const int ch = idx % chunks, rr = idx / chunks;
-                const int row = kRows - n_pad + rr % n_pad + (rr >= n_pad ? kRows : 0);
-                *reinterpret_cast<uint4 *>(base + (size_t)(ch >> 3) * kBlk + blk_off(row, (ch & 7) * 8)) =
-                    make_uint4(0, 0, 0, 0);
-            }
-        }
-    }
     cp_async_wait_all();
     __syncthreads();
     // 32 tokens x 128 latent dims: a warp takes 32 of the dims
@@ -574,13 +559,17 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
                 const int st = item % NS;
                 ok &= wait_warp(lane < NU, full(st, min(lane, NP)), (item / NS) & 1, abort_flag);
                 const uint8_t *row = sm + st * PAGE + (warp * 32 + lane) * 128;
+                const bool none = group * kRows + lane >= p.nq * p.H;  // no such query: its row is not written
 #pragma unroll 1
                 for (int c = 0; c < 2 * NP + 1; ++c) {
                     uint32_t r[32];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const uint4 x = *reinterpret_cast<const uint4 *>(row + c * kBlk + ((e ^ (lane & 7)) << 4));
-                        r[4 * e] = x.x; r[4 * e + 1] = x.y; r[4 * e + 2] = x.z; r[4 * e + 3] = x.w;
+                        r[4 * e] = none ? 0u : x.x;
+                        r[4 * e + 1] = none ? 0u : x.y;
+                        r[4 * e + 2] = none ? 0u : x.z;
+                        r[4 * e + 3] = none ? 0u : x.w;
                     }
                     tmem_st32(tmem + kTmemQ + c * 32 + lanes, r);
                 }
