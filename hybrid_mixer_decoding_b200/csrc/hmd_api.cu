@@ -735,7 +735,7 @@ hmd_status_t attn_latent_prefill(int B, int T, int H, int d, int d_c, int d_r, i
         span * B >= (1LL << 31))
         return fail(HMD_ERR_UNSUPPORTED);
     if (!aligned16(q) || !aligned16(c) || !aligned16(w_uk) || !aligned16(w_uv) ||
-        !aligned16(pool) || !aligned16(workspace) || !aligned16(o))
+        !aligned16(pool) || (reinterpret_cast<uintptr_t>(workspace) & 31u) || !aligned16(o))
         return fail(HMD_ERR_ARG);
     if (ws_bytes < hmd::latent_prefill_ws_bytes(B, T, 1, d, max_prefix)) return fail(HMD_ERR_SHAPE);
     hmd::LatentPrefillArgs a{};

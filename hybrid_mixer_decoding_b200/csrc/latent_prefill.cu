@@ -149,8 +149,32 @@ struct ExpandSmem {
 };
 static_assert(ExpandSmem::ALLOC <= 232448, "shared memory per CTA");
 
-// 32 bytes to global memory in one store
-__device__ __forceinline__ void store_32b(void *dst, const uint32_t (&v)[8]) {
+// Four lanes exchange pieces of 32 bytes: lane l's piece t becomes lane t's (of the four) piece l, so that
+// with a row per lane a store of four lanes writes a whole line of 128 bytes.
+__device__ __forceinline__ void transpose4(uint32_t (&blk)[4][8], int lane) {
+#pragma unroll
+    for (int bit = 1; bit < 4; bit *= 2) {
+        const bool upper = lane & bit;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (t & bit) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t &x = blk[t][j], &y = blk[t | bit][j];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x : y, bit);
+                if (upper) x = got;
+                else y = got;
+            }
+        }
+    }
+}
+// 32 bytes to global memory, in one store if `whole` (then dst is 32-byte aligned, else 16)
+__device__ __forceinline__ void store_32b(void *dst, const uint32_t (&v)[8], bool whole = true) {
+    if (!whole) {
+        static_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        return;
+    }
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
@@ -312,7 +336,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
             wait_warp(lead, bar(SM::B_ACC + acc), (st / kExpAcc) & 1, abort_flag);
             if (uniform(*abort_flag)) break;  // reported by the products' warp; the whole warp leaves below
             tc_fence_after();
-            uint32_t blk[8][8];  // 128 columns as fp16: pieces of 32 bytes
+            uint32_t blk[2][4][8];  // 128 columns as fp16: pieces of 32 bytes
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t r[32];
@@ -332,7 +356,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
                 }
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    blk[c * 2 + j / 8][j % 8] =
+                    blk[c / 2][c % 2 * 2 + j / 8][j % 8] =
                         live ? pack_f16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])) : 0u;
                 __syncwarp();
             }
@@ -342,26 +366,11 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
             const size_t row0 = (((size_t)b * p.heads + head_of(st)) * p.s_pad + pos0 + quarter * 32 + (lane & ~3)) * D;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                // four lanes exchange their pieces, so that a store writes whole 128-byte lines
-#pragma unroll
-                for (int bit = 1; bit < 4; bit *= 2) {
-                    const bool upper = lane & bit;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        if (t & bit) continue;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            uint32_t &x = blk[4 * c + t][j], &y = blk[4 * c + (t | bit)][j];
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x : y, bit);
-                            if (upper) x = got;
-                            else y = got;
-                        }
-                    }
-                }
+                transpose4(blk[c], lane);
                 const bool key = STEPS == 2 ? st % 2 == 0 : c == 0;
                 __half *dst = (key ? p.k : p.v) + row0 + (STEPS == 2 ? c * 64 : 0) + (lane & 3) * 16;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) store_32b(dst + t * D, blk[4 * c + t]);
+                for (int t = 0; t < 4; ++t) store_32b(dst + t * D, blk[c][t]);
             }
         }
         if (out) atomicOr(&g_err, HMD_DEVWARN_RANGE);
@@ -393,7 +402,7 @@ struct AttendSmem {
     // query tile's S is complete (all but their last block a little earlier, at B_K: a tile's values
     // take the place of its first keys), values once its O is.
     static constexpr int B_FULL = 0, B_S = NR, B_P = B_S + 2, B_O = B_P + 2, B_SR = B_O + 2, B_K = B_SR + 1,
-                         B_END = B_K + 1, N_BARS = B_END + 1;
+                         B_Q = B_K + 1, B_END = B_Q + 1, N_BARS = B_END + 1;
     // in TMEM: O_0, O_1, S (both query tiles' in turn), P_0, P_1
     static constexpr uint32_t T_O = 0, T_S = 256, T_P = 384;
 };
@@ -430,7 +439,8 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     const int nt1 = uniform(t_last >= t_first + kTile ? (s.prefix + t_last) / kTile + 1 : 0);
     const int n_tiles = max(nt0, nt1);
     if (tid == 0) {
-        for (int i = 0; i < SM::N_BARS; ++i) mbar_init(bar(i), (i == SM::B_P || i == SM::B_P + 1 || i == SM::B_SR) ? 4 : 1);
+        for (int i = 0; i < SM::N_BARS; ++i)
+            mbar_init(bar(i), i == SM::B_Q ? 8 : (i == SM::B_P || i == SM::B_P + 1 || i == SM::B_SR) ? 4 : 1);
         fence_barrier_init();
         *abort_flag = 0;
     }
@@ -439,38 +449,53 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
-    // Q rows -> shared memory as fp16, one row per softmax thread
-    const int qt = (warp >> 2) & 1, row = tid & (kTile - 1);
-    const int t_row = t_first + qt * kTile + row;
-    const bool row_ok = t_row <= t_last;
-    const int pos_row = s.prefix + t_row;  // the row's position: its last key
-    if (tid < kSoftmax) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + (((size_t)b * p.T + (row_ok ? t_row : 0)) * p.H + h) * (D + kDR));
-        bool out = false;
-#pragma unroll
-        for (int c = 0; c < (D + kDR) / 8; ++c) {
-            const uint4 x = row_ok ? src[c] : make_uint4(0, 0, 0, 0);
-            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float lo = bf16_lo(in[e]), hi = bf16_hi(in[e]);
-                out |= clip_half(lo);
-                out |= clip_half(hi);
-                y[e] = pack_f16x2(lo, hi);
-            }
-            *reinterpret_cast<uint4 *>(sm + SM::OFF_Q + qt * SM::Q_TILE + (c >> 3) * kBlk + row * 128 +
-                                       (((c & 7) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-        }
-        if (out) atomicOr(&g_err, HMD_DEVWARN_RANGE);
-        fence_proxy_async_smem();  // Q is read by the tensor cores
-    }
-    griddep_wait();  // keys and values are kernel 2's
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+    const int qt = (warp >> 2) & 1, row = tid & (kTile - 1);  // of a softmax thread
+    const int t_row = t_first + qt * kTile + row;
+    const bool row_ok = t_row <= t_last;
+    const int pos_row = s.prefix + t_row;  // the row's position: its last key
+    if (tid < kSoftmax) {
+        // Q -> shared memory as fp16: consecutive threads take consecutive 16-byte chunks, eight loads in
+        // flight (with a row per thread it took 10 us of a CTA's 40)
+        constexpr int CH = (D + kDR) / 8;
+        bool out = false;
+#pragma unroll 1
+        for (int k0 = 0; k0 < CH; k0 += 8) {
+            uint4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int i = tid + kSoftmax * (k0 + k), r = i / CH, c = i - r * CH;
+                x[k] = t_first + r <= t_last
+                           ? *reinterpret_cast<const uint4 *>(
+                                 p.q + (((size_t)b * p.T + t_first + r) * p.H + h) * (D + kDR) + c * 8)
+                           : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int i = tid + kSoftmax * (k0 + k), r = i / CH, c = i - r * CH;
+                const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                uint32_t y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float lo = bf16_lo(in[e]), hi = bf16_hi(in[e]);
+                    out |= clip_half(lo);
+                    out |= clip_half(hi);
+                    y[e] = pack_f16x2(lo, hi);
+                }
+                *reinterpret_cast<uint4 *>(sm + SM::OFF_Q + (r >> 7) * SM::Q_TILE + (c >> 3) * kBlk + (r & 127) * 128 +
+                                           (((c & 7) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        }
+        static_assert(CH % 8 == 0, "whole batches of loads");
+        if (out) atomicOr(&g_err, HMD_DEVWARN_RANGE);
+        fence_proxy_async_smem();  // Q is read by the tensor cores
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(SM::B_Q));
+    }
+    griddep_wait();  // keys and values are kernel 2's
 
     const int last = nt1 > 0;  // the last query tile
     if (warp == 9) {
@@ -570,6 +595,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
             }
             umma_commit_if(lead, bar(SM::B_O + j));
         };
+        wait_warp(lead, bar(SM::B_Q), 0, abort_flag);
         for (int i = -1; i < n_tiles; ++i) {
             if (i + 1 < nt0) issue_s(0, i + 1);
             if (i >= 0 && i < nt0) issue_o(0, i);
@@ -685,23 +711,27 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         if (ok) {
             tc_fence_after();
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-            uint4 *dst = reinterpret_cast<uint4 *>(p.o + (((size_t)b * p.T + t_row) * p.H + h) * D);
+            const int t0 = t_first + qt * kTile + (row & ~3);
+            const bool whole = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
+            __nv_bfloat16 *dst = p.o + (((size_t)b * p.T + t0) * p.H + h) * D + (lane & 3) * 16;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                __syncwarp();  // converged for the TMEM load after the row-dependent stores
-                uint32_t r[32];
-                tmem_ld32(o_col + 32 * c, r);
-                tmem_wait_ld();
-                if (row_ok) {
+            for (int c = 0; c < D / 64; ++c) {
+                __syncwarp();  // converged for the TMEM loads after the row-dependent stores
+                uint32_t blk[4][8];
 #pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        const float *v = reinterpret_cast<const float *>(r + 8 * q4);
-                        dst[c * 4 + q4] = make_uint4(pack_bf16x2(v[0] * inv, v[1] * inv),
-                                                     pack_bf16x2(v[2] * inv, v[3] * inv),
-                                                     pack_bf16x2(v[4] * inv, v[5] * inv),
-                                                     pack_bf16x2(v[6] * inv, v[7] * inv));
-                    }
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t r[32];
+                    tmem_ld32(o_col + 64 * c + 32 * half, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        blk[half * 2 + j / 8][j % 8] = pack_bf16x2(__uint_as_float(r[2 * j]) * inv,
+                                                                   __uint_as_float(r[2 * j + 1]) * inv);
                 }
+                transpose4(blk, lane);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (t0 + t <= t_last) store_32b(dst + (size_t)t * p.H * D + 64 * c, blk[t], whole);
             }
         } else if (lane == 0) {
             atomicOr(&g_err, HMD_DEVERR_TIMEOUT);

@@ -452,3 +452,19 @@ def test_inputs_written_just_before_calls_that_share_a_workspace(H, d, d_c, T):
         torch.cuda.synchronize()
         for pair, ref in zip(outs, want):
             assert all(torch.equal(o, r) for o, r in zip(pair, ref))
+
+
+@pytest.mark.parametrize("d,d_c", [(128, 512), (64, 128)])
+def test_prefill_outputs_on_16_byte_boundaries(d, d_c):
+    """o, q and the rows at addresses that are multiples of 16 bytes, not of 32."""
+    c = Latent([150, 70], 3, d, d_c, seed=70)
+
+    def shifted(x):
+        y = torch.empty(x.numel() + 8, device="cuda", dtype=BF)[8:].view(x.shape)
+        assert y.data_ptr() % 32 == 16
+        return y.copy_(x)
+
+    q, new_c = shifted(c.randn(2, 150, 3, d + DR)), shifted(c.randn(2, 150, d_c + DR))
+    o = shifted(torch.full((2, 150, 3, d), 9.0, device="cuda", dtype=BF))
+    check_prefill(c, q, new_c, prefill(c, q, new_c, prompt=[150, 70], o=o), [0, 0], [150, 70])
+    assert hmd.hmd_device_errors(clear=True) == 0

@@ -45,6 +45,7 @@ def _prefill(B=2, T=300, H=16, d=128, d_c=512, d_r=64, pt=64, scale=0.07, q=FAKE
 
 @pytest.mark.parametrize("bad,status", [
     (dict(q=None), ARG), (dict(pool=None), ARG), (dict(ws=FAKE + 8), ARG), (dict(o=FAKE + 8), ARG),
+    (dict(ws=FAKE + 16), ARG),
     (dict(scale=-1.0), ARG), (dict(max_prefix=-1), SHAPE), (dict(max_pages=4), SHAPE),
     (dict(prefix=FAKE, max_prefix=21), SHAPE), (dict(uk_head=0), SHAPE),
     (dict(ws_bytes=100), SHAPE), (dict(d=32), UNSUP), (dict(d_c=100), UNSUP),
