@@ -458,38 +458,34 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     const bool row_ok = t_row <= t_last;
     const int pos_row = s.prefix + t_row;  // the row's position: its last key
     if (tid < kSoftmax) {
-        // Q -> shared memory as fp16: consecutive threads take consecutive 16-byte chunks, eight loads in
+        // Q -> shared memory as fp16: consecutive threads take consecutive 16-byte chunks, all loads in
         // flight (with a row per thread it took 10 us of a CTA's 40)
         constexpr int CH = (D + kDR) / 8;
         bool out = false;
-#pragma unroll 1
-        for (int k0 = 0; k0 < CH; k0 += 8) {
-            uint4 x[8];
+        uint4 x[CH];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int i = tid + kSoftmax * (k0 + k), r = i / CH, c = i - r * CH;
-                x[k] = t_first + r <= t_last
-                           ? *reinterpret_cast<const uint4 *>(
-                                 p.q + (((size_t)b * p.T + t_first + r) * p.H + h) * (D + kDR) + c * 8)
-                           : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int i = tid + kSoftmax * (k0 + k), r = i / CH, c = i - r * CH;
-                const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                uint32_t y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float lo = bf16_lo(in[e]), hi = bf16_hi(in[e]);
-                    out |= clip_half(lo);
-                    out |= clip_half(hi);
-                    y[e] = pack_f16x2(lo, hi);
-                }
-                *reinterpret_cast<uint4 *>(sm + SM::OFF_Q + (r >> 7) * SM::Q_TILE + (c >> 3) * kBlk + (r & 127) * 128 +
-                                           (((c & 7) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
+        for (int k = 0; k < CH; ++k) {
+            const int i = tid + kSoftmax * k, r = i / CH, c = i - r * CH;
+            x[k] = t_first + r <= t_last
+                       ? *reinterpret_cast<const uint4 *>(
+                             p.q + (((size_t)b * p.T + t_first + r) * p.H + h) * (D + kDR) + c * 8)
+                       : make_uint4(0, 0, 0, 0);
         }
-        static_assert(CH % 8 == 0, "whole batches of loads");
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int i = tid + kSoftmax * k, r = i / CH, c = i - r * CH;
+            const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float lo = bf16_lo(in[e]), hi = bf16_hi(in[e]);
+                out |= clip_half(lo);
+                out |= clip_half(hi);
+                y[e] = pack_f16x2(lo, hi);
+            }
+            *reinterpret_cast<uint4 *>(sm + SM::OFF_Q + (r >> 7) * SM::Q_TILE + (c >> 3) * kBlk + (r & 127) * 128 +
+                                       (((c & 7) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
         if (out) atomicOr(&g_err, HMD_DEVWARN_RANGE);
         fence_proxy_async_smem();  // Q is read by the tensor cores
         __syncwarp();
