@@ -25,8 +25,8 @@
 // its own P: a tile's scores are complete before the softmax of the tile before is done (with S and P
 // of a group in one place a key tile took 3400 cycles, softmax and products of a group in turn; now
 // 2900). d = 128: the products of a key tile alone take 2560, and with the copies they move 340 KB through
-// shared memory, 2660 cycles of its 128 bytes. B = 2, T = 4096, 32 heads: 413 us in all (1.0 PFLOP/s), 470
-// in a row under the power limit; B = 3, 1000 after 2801: 237 us.
+// shared memory, 2660 cycles of its 128 bytes. B = 2, T = 4096, 32 heads: 397 us in all (1.04 PFLOP/s), 460
+// in a row under the power limit; B = 3, 1000 after 2801: 234 us. A CTA's start and end are about 12000 cycles.
 // If the workspace holds fewer heads than H, kernels 2 and 3 run once per group of heads.
 #include <cuda.h>
 #include <cuda_fp16.h>

@@ -426,7 +426,9 @@ HMD_API hmd_status_t attn_latent_decode(int n_q, int B, int H, int d, int d_c, i
                                         void *workspace, size_t ws_bytes, hmd_stream_t stream);
 
 /* Expanded form, for prompts: T new tokens per sequence after prefix_lens[b] cached positions.
- * Appends their rows and attends causally: token t sits at position prefix_lens[b] + t.
+ * Appends their rows and attends causally: token t sits at position prefix_lens[b] + t. Every key and
+ * value is formed once, the prefix's too: for a few new tokens after a long prefix the absorbed form
+ * (n_q = T) does less.
  *   q [B][T][H][d + d_r]; c [B][T][d_c + d_r]; o [B][T][H][d], all bf16.
  *   prefix_lens: device int32 [B], any values in [0, max_prefix]; NULL: no prefix.
  *   prompt_lens: device int32 [B] in [0, T], the sequence's new tokens; the rows of q, c and o
