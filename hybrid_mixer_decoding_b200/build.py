@@ -23,7 +23,7 @@ SOURCES = ["hmd_api.cu", "delta_decode.cu", "attn_decode.cu", "delta_prefill.cu"
            "attn_decode_static.cu", "delta_prefill_tc.cu", "attn_prefill_tc.cu",
            "tmap.cu", "kv_evict.cu", "latent_decode.cu",
            "latent_prefill.cu"]
-HEADERS = ["ptx.cuh", "softmax.cuh", "kernels.h"]
+HEADERS = ["ptx.cuh", "softmax.cuh", "kernels.h", "latent_ring.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                 "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

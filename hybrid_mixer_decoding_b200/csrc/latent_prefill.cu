@@ -34,6 +34,7 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "latent_ring.h"
 #include "ptx.cuh"
 #include "softmax.cuh"
 #include "../../include/hmd.h"
@@ -389,10 +390,7 @@ constexpr int kSoftmax = 256;                  // softmax threads: two groups of
 constexpr int kAttThreads = kSoftmax + 64;     // + the MMA warp (8) and the TMA warp (9)
 template <int D>
 struct AttendSmem {
-    static constexpr int KB = D / 64 + 1, VB = D / 64, NB = KB + VB;  // blocks of a key tile
-    // Blocks in the ring: what is left of shared memory, and (D = 64) few enough that a wait for a
-    // tile's products cannot be overtaken by those of two tiles later.
-    static constexpr int NR = D == 128 ? 8 : 5;
+    static constexpr int KB = RingShape<D>::KB, VB = RingShape<D>::VB, NR = RingShape<D>::NR;
     static constexpr uint32_t Q_TILE = KB * kBlk;
     static constexpr uint32_t OFF_Q = 0, OFF_R = 2 * Q_TILE;
     static constexpr uint32_t OFF_BAR = OFF_R + NR * kBlk;
@@ -400,9 +398,14 @@ struct AttendSmem {
     static constexpr uint32_t ALLOC = BYTES > 118784 ? BYTES : 118784;  // one CTA per SM
     // B_S, B_P, B_O: S_j complete, P_j written, O_j complete; B_SR: S read. Keys are free once the last
     // query tile's S is complete (all but their last block a little earlier, at B_K: a tile's values
-    // take the place of its first keys), values once its O is.
-    static constexpr int B_FULL = 0, B_S = NR, B_P = B_S + 2, B_O = B_P + 2, B_SR = B_O + 2, B_K = B_SR + 1,
-                         B_Q = B_K + 1, B_END = B_Q + 1, N_BARS = B_END + 1;
+    // take the place of its first keys), values once its O is. B_S, B_O and B_K are kRingPhases each,
+    // for the key tiles in turn.
+    static constexpr int B_FULL = 0, B_S = NR, B_O = B_S + 2 * kRingPhases, B_K = B_O + 2 * kRingPhases,
+                         B_P = B_K + kRingPhases, B_SR = B_P + 2, B_Q = B_SR + 1, B_END = B_Q + 1,
+                         N_BARS = B_END + 1;
+    static_assert(N_BARS * 8 + 8 <= 256, "barriers");
+    __device__ static int s(int j, int i) { return B_S + j * kRingPhases + ring_barrier(i); }
+    __device__ static int o(int j, int i) { return B_O + j * kRingPhases + ring_barrier(i); }
     // in TMEM: O_0, O_1, S (both query tiles' in turn), P_0, P_1
     static constexpr uint32_t T_O = 0, T_S = 256, T_P = 384;
 };
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                             const __grid_constant__ CUtensorMap tmr, const PrefillParams p) {
     using SM = AttendSmem<D>;
-    constexpr int KB = SM::KB, VB = SM::VB, NB = SM::NB, NR = SM::NR;
+    constexpr int KB = SM::KB, VB = SM::VB, NR = SM::NR, NB = KB + VB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -498,33 +501,26 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         // ===== copies: the blocks of K_0, K_1, V_0, K_2, V_1, ... in the order of their use, block n into
         // slot n % NR (the warp converged) ========================================================
         const bool lead = elect_one();
-        struct Place {  // block u of K_g, or of K_g and V_(g-1)
-            int g = 0, u = 0;
-            __device__ void next(int n_tiles) {
-                if (++u == (g == 0 ? KB : g < n_tiles ? NB : VB)) {
-                    u = 0;
-                    ++g;
-                }
-            }
-            __device__ bool key(int n_tiles) const { return g < n_tiles && u < KB; }
-        } at, old;  // the block to load, the one whose slot it takes
+        RingPlace<D> at, old;  // the block to load, the one whose slot it takes
         bool ok = true;
         int n = 0, slot = 0;
         for (; n < n_tiles * NB; ++n) {
             if (n >= NR) {
-                const bool key = old.key(n_tiles);
-                const int free = !key ? SM::B_O + last : old.u < KB - 1 ? SM::B_K : SM::B_S + last;
-                ok = wait_warp(lead, bar(free), (key ? old.g : old.g - 1) & 1, abort_flag);
+                const int i = old.tile(n_tiles);
+                const RingFree by = old.freed_by(n_tiles);
+                const int free = by == kFreeOutput ? SM::o(last, i) : by == kFreeKeys ? SM::B_K + ring_barrier(i)
+                                                                                      : SM::s(last, i);
+                ok = wait_warp(lead, bar(free), ring_parity(i), abort_flag);
                 if (!ok) break;
                 old.next(n_tiles);
             }
             const uint32_t dst = sb + SM::OFF_R + slot * kBlk, fb = bar(SM::B_FULL + slot);
             mbar_expect_if(lead, fb, kBlk);
             const bool key = at.key(n_tiles);
-            const int v = at.u - (at.g < n_tiles ? KB : 0);
-            if (key && at.u < KB - 1) tma_load_3d_if(lead, dst, &tmk, fb, at.u * 64, at.g * kTile, bh);
-            else if (key) tma_load_3d_if(lead, dst, &tmr, fb, 0, at.g * kTile, b);
-            else tma_load_3d_if(lead, dst, &tmv, fb, v * 64, (at.g - 1) * kTile, bh);
+            const int u = at.block(n_tiles), row0 = at.tile(n_tiles) * kTile;
+            if (key && u < KB - 1) tma_load_3d_if(lead, dst, &tmk, fb, u * 64, row0, bh);
+            else if (key) tma_load_3d_if(lead, dst, &tmr, fb, 0, row0, b);
+            else tma_load_3d_if(lead, dst, &tmv, fb, u * 64, row0, bh);
             at.next(n_tiles);
             if (++slot == NR) slot = 0;
         }
@@ -556,7 +552,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
             tc_fence_after();
         };
         auto issue_s = [&](int j, int i) {  // S = Q_j K_i^T
-            const int n = i == 0 ? 0 : i * NB - VB;
+            const int n = ring_key<D>(i);
             wait_for(n, j == 0 || i >= nt0 ? KB : 0, n_s > 0 ? SM::B_SR : -1, n_s - 1);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
@@ -565,13 +561,13 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     umma_if(lead, tmem + SM::T_S, q.at(kk * 32), k.at(kk * 32), ID_S, (kb > 0 || kk > 0) ? 1u : 0u);
-                if (kb == KB - 2) umma_commit_if(lead && j == last, bar(SM::B_K));
+                if (kb == KB - 2) umma_commit_if(lead && j == last, bar(SM::B_K + ring_barrier(i)));
             }
-            umma_commit_if(lead, bar(SM::B_S + j));
+            umma_commit_if(lead, bar(SM::s(j, i)));
             ++n_s;
         };
         auto issue_o = [&](int j, int i) {  // O_j (+)= P_j V_i, P_j from TMEM
-            const int n = (i + 1) * NB - VB + (i + 1 < n_tiles ? KB : 0);
+            const int n = ring_value<D>(i, n_tiles);
             wait_for(n, j == 0 || i >= nt0 ? VB : 0, SM::B_P + j, i);
             const uint32_t slot = (uint32_t)n % NR;
             const uint32_t o = tmem + SM::T_O + 128 * j, pj = tmem + SM::T_P + 64 * j;
@@ -589,7 +585,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                 for (int kk = 0; kk < kTile / 16; ++kk)
                     umma_ts_if(lead, o + 64, pj + 8 * kk, d_v.at(kk * 2048), ID_O64, kk > 0 ? 1u : more);
             }
-            umma_commit_if(lead, bar(SM::B_O + j));
+            umma_commit_if(lead, bar(SM::o(j, i)));
         };
         wait_warp(lead, bar(SM::B_Q), 0, abort_flag);
         for (int i = -1; i < n_tiles; ++i) {
@@ -613,7 +609,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         const bool lead = elect_one();
         float m_base = -INFINITY, l_run = 0.f;
         for (int i = 0; i < nt; ++i) {
-            wait_warp(lead, bar(SM::B_S + qt), i & 1, abort_flag);
+            wait_warp(lead, bar(SM::s(qt, i)), ring_parity(i), abort_flag);
             tc_fence_after();
             float x[kTile];
             {
@@ -681,7 +677,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                 l_run += (a0 + a1) + (b0 + b1);
             }
             // the product before has read P and added to O: the row's earlier output to the new base, then P
-            if (i > 0) wait_warp(lead, bar(SM::B_O + qt), (i - 1) & 1, abort_flag);
+            if (i > 0) wait_warp(lead, bar(SM::o(qt, i - 1)), ring_parity(i - 1), abort_flag);
             tc_fence_after();
             __syncwarp();  // the row-dependent branches above rejoin before the TMEM accesses
             if (__any_sync(0xffffffffu, move) && i > 0) {
@@ -702,7 +698,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(SM::B_P + qt));
         }
-        wait_warp(lead, bar(SM::B_O + qt), (nt - 1) & 1, abort_flag);
+        wait_warp(lead, bar(SM::o(qt, nt - 1)), ring_parity(nt - 1), abort_flag);
         const bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
         if (ok) {
             tc_fence_after();
