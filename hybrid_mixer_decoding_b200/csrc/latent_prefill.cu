@@ -9,7 +9,14 @@
 // The intermediate keys, values, queries and softmax weights are fp16, not bf16: rounding keys,
 // values and weights to bf16 would each add the error of the bf16 output itself (2^-8); fp16's 2^-11
 // adds nothing visible. Its range is 65504: larger keys, values or queries are clipped and reported
-// (HMD_DEVWARN_RANGE).
+// (HMD_DEVWARN_RANGE). Downwards it ends at 2^-14, so the values of a head in a tile of 128 positions are
+// stored times 2^e, e = 0, 20, 40 or 60, with which the largest of them is at 2^-5 or above (or as near as
+// e = 60 brings it): values are held to 2^-11, or to 2^-20 of the largest. Most often e is 0
+// everywhere, or the same; where it is not, the softmax lowers a tile's exponents by e and adds its weights
+// times 2^e to the row's sum, so that tiles of any sizes add up (a loop of its own: in the common one this
+// took 2 to 4% of the kernel). e goes with the values, in the last bits of three of them (those to 2^-10). Keys and queries need no such factor:
+// what they lose below 2^-14, at most 2^-25, moves a score by 2^-25 scale sum |q| (or |k|), which is 4e-7
+// for 192 dims of size 1 and 0.03 at the end of fp16's range.
 //
 // Kernel 1 (rows): appends the new rows to the cache and converts every position's shared part
 // k_r to fp16. Kernel 2 (expand): one CTA per (128 positions, a share of the heads):
@@ -32,6 +39,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "latent_ring.h"
@@ -50,6 +58,11 @@ constexpr int kTile = 128;           // positions per key tile, queries per quer
 constexpr uint32_t kBlk = kTile * 128;  // one [128 rows][128 B] block, 128-byte swizzle
 constexpr float kHalfMax = 65504.f;
 constexpr float kLazy = 8.f;         // log2 headroom before a row's exponent base moves
+// A head's values in a tile are stored times 2^e, e = kMaxExp - kExpStep * code, the code in the last bits of
+// its first kExpBits values. The largest e leaves a row's sum, which has every weight times 2^e, far from
+// fp32's ends: 2^75 a key, and the 2^-125 at which the softmax clamps a masked key's weight is 2^-65.
+constexpr int kMaxExp = 60, kExpStep = 20, kExpBits = 3;
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // Instruction descriptor of kind::f16 with fp16 A/B and fp32 D: the bf16 one with both type fields 0.
 constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
@@ -58,6 +71,13 @@ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+// The fp16 nearest to x whose last bit is `bit`.
+__device__ __forceinline__ uint32_t half_with_last_bit(float x, uint32_t bit) {
+    const __half n = __float2half_rn(x);
+    const uint32_t h = __half_as_ushort(n);
+    if ((h & 1u) == bit) return h;
+    return (h & 0x7fffu) == 0 || fabsf(x) > fabsf(__half2float(n)) ? h + 1 : h - 1;
 }
 // Clips to fp16's range; true if anything was outside it.
 __device__ __forceinline__ bool clip_half(float &x) {
@@ -145,7 +165,8 @@ struct ExpandSmem {
     static constexpr uint32_t ALLOC = BYTES;   // one CTA per SM
     static constexpr int B_A = 0, B_MOVED = 1, B_WFULL = 2, B_WFREE = B_WFULL + NW, B_ACC = B_WFREE + NW,
                          B_READ = B_ACC + kExpAcc, B_END = B_READ + kExpAcc, N_BARS = B_END + 1;
-    static_assert(N_BARS * 8 + 8 <= 512, "barriers");
+    static constexpr uint32_t OFF_MAX = OFF_MISC + 448;  // [two sets of warps][two steps][four warps]
+    static_assert(N_BARS * 8 + 8 <= 448, "barriers");
     __device__ static uint32_t stage(int w) { return (w < EARLY ? w + NW - EARLY : w - EARLY) * W_STAGE; }
 };
 static_assert(ExpandSmem::ALLOC <= 232448, "shared memory per CTA");
@@ -168,6 +189,19 @@ __device__ __forceinline__ void transpose4(uint32_t (&blk)[4][8], int lane) {
             }
         }
     }
+}
+// A barrier of the four warps that store the same steps (set 0 or 1), and an OR over a predicate of theirs.
+__device__ __forceinline__ bool bar_set_or(int set, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred), "r"(1 + set)
+        : "memory");
+    return r != 0;
 }
 // 32 bytes to global memory, in one store if `whole` (then dst is 32-byte aligned, else 16)
 __device__ __forceinline__ void store_32b(void *dst, const uint32_t (&v)[8], bool whole = true) {
@@ -334,36 +368,70 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         }
         for (int st = warp >> 2; st < n_steps; st += 2) {
             const int acc = st % kExpAcc;
-            wait_warp(lead, bar(SM::B_ACC + acc), (st / kExpAcc) & 1, abort_flag);
-            if (uniform(*abort_flag)) break;  // reported by the products' warp; the whole warp leaves below
+            const bool ready = wait_warp(lead, bar(SM::B_ACC + acc), (st / kExpAcc) & 1, abort_flag);
+            const bool values = STEPS == 1 || st % 2 == 1;  // the same in all steps of a set of warps
+            if (!ready && !values) break;  // reported by the products' warp
             tc_fence_after();
-            uint32_t blk[2][4][8];  // 128 columns as fp16: pieces of 32 bytes
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t r[32];
-                tmem_ld32(tmem + 256 + acc * 128 + c * 32 + lanes, r);
-                tmem_wait_ld();
-                float big = 0.f;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(__uint_as_float(r[j])));
-                if (live && big > kHalfMax) {
-                    out = true;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float x = __uint_as_float(r[j]);
-                        clip_half(x);
-                        r[j] = __float_as_uint(x);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    blk[c / 2][c % 2 * 2 + j / 8][j % 8] =
-                        live ? pack_f16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])) : 0u;
-                __syncwarp();
-            }
+            uint32_t r[2][64];  // 128 columns
+            tmem_ld64(tmem + 256 + acc * 128 + lanes, r[0]);
+            tmem_ld64(tmem + 256 + acc * 128 + 64 + lanes, r[1]);
+            tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(SM::B_READ + acc));  // the accumulator is free
+            float big[2] = {0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) big[c] = fmaxf(big[c], fabsf(__uint_as_float(r[c][j])));
+                if (!live) big[c] = 0.f;
+            }
+            int e = 0;
+            if (values) {
+                // the values' power of two, from the tile's largest one
+                volatile uint32_t *s_max = reinterpret_cast<volatile uint32_t *>(sm + SM::OFF_MAX) +
+                                           (warp >> 2) * 8 + (st >> 1 & 1) * 4;
+                const float mine = STEPS == 1 ? big[1] : fmaxf(big[0], big[1]);
+                const uint32_t top_w = __reduce_max_sync(0xffffffffu, __float_as_uint(mine));
+                if (lane == 0) s_max[quarter] = top_w;
+                if (bar_set_or(warp >> 2, !ready)) break;  // reported by the products' warp; all four leave
+                const uint32_t top = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+                e = min(kMaxExp, max(0, 127 + 14 - (int)(top >> 23)) / kExpStep * kExpStep);
+                const float f = pow2(e);
+#pragma unroll
+                for (int c = STEPS == 1 ? 1 : 0; c < 2; ++c) {
+                    big[c] *= f;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) r[c][j] = __float_as_uint(__uint_as_float(r[c][j]) * f);
+                }
+            }
+            uint32_t blk[2][4][8];  // as fp16: pieces of 32 bytes
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (big[c] > kHalfMax) {
+                    out = true;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) {
+                        float x = __uint_as_float(r[c][j]);
+                        clip_half(x);
+                        r[c][j] = __float_as_uint(x);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    blk[c][j / 8][j % 8] =
+                        live ? pack_f16x2(__uint_as_float(r[c][2 * j]), __uint_as_float(r[c][2 * j + 1])) : 0u;
+                if (c == (STEPS == 1 ? 1 : 0) && values && quarter == 0 && lane == 0) {
+                    const uint32_t code = (kMaxExp - e) / kExpStep;
+                    uint32_t h[kExpBits];
+#pragma unroll
+                    for (int j = 0; j < kExpBits; ++j)
+                        h[j] = half_with_last_bit(live ? __uint_as_float(r[c][j]) : 0.f, code >> j & 1u);
+                    blk[c][0][0] = h[0] | h[1] << 16;
+                    blk[c][0][1] = h[2] | (blk[c][0][1] & 0xffff0000u);
+                }
+                __syncwarp();
+            }
             const size_t row0 = (((size_t)b * p.heads + head_of(st)) * p.s_pad + pos0 + quarter * 32 + (lane & ~3)) * D;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -608,101 +676,131 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                        o_col = lane_base + SM::T_O + 128 * qt;
         const bool lead = elect_one();
         float m_base = -INFINITY, l_run = 0.f;
-        for (int i = 0; i < nt; ++i) {
-            wait_warp(lead, bar(SM::s(qt, i)), ring_parity(i), abort_flag);
-            tc_fence_after();
-            float x[kTile];
-            {
-                uint32_t r[64];
-                tmem_ld64(s_col, r);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(r[j]);
-                tmem_ld64(s_col + 64, r);
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(SM::B_SR));  // S may be the other query tile's now
-#pragma unroll
-                for (int j = 0; j < 64; ++j) x[64 + j] = __uint_as_float(r[j]);
-            }
-            const int j0 = i * kTile;
-            if (!(row_ok && j0 + kTile - 1 <= pos_row)) {
-#pragma unroll
-                for (int j = 0; j < kTile; ++j) x[j] = (row_ok && j0 + j <= pos_row) ? x[j] : -INFINITY;
-            }
-            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // short chains
-#pragma unroll
-            for (int j = 0; j < kTile; j += 8) {
-                mx4[0] = max3(mx4[0], x[j], x[j + 1]);
-                mx4[1] = max3(mx4[1], x[j + 2], x[j + 3]);
-                mx4[2] = max3(mx4[2], x[j + 4], x[j + 5]);
-                mx4[3] = max3(mx4[3], x[j + 6], x[j + 7]);
-            }
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
-            const bool move = mx > m_base + kLazy;
-            float f = 1.f;  // factor of the row's earlier output and sum
-            if (move) {
-                f = exp2f(m_base - mx);  // 0 while the row had no key (m_base = -inf)
-                m_base = mx;
-                l_run *= f;
-            }
-            const float mu = (m_base == -INFINITY) ? 0.f : m_base;
-            uint32_t pk[kTile / 32][16];  // P, two keys a word
-            {
-                const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nmu2 = f2(-mu, -mu);
-                uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-                for (int c = 0; c < kTile / 32; ++c) {
-#pragma unroll
-                    for (int u = 0; u < 16; ++u) {
-                        const uint64_t y = f2_fma(f2(x[c * 32 + 2 * u], x[c * 32 + 2 * u + 1]), sc2, nmu2);
-                        uint64_t e;
-                        if ((u & 3) == 3) {
-                            e = exp2_fma_x2(y);
-                        } else {
-                            float a0, a1;
-                            f2_split(y, a0, a1);
-                            e = f2(ex2_approx(a0), ex2_approx(a1));
-                        }
-                        acc[u & 1] = f2_add(acc[u & 1], e);
-                        float e0, e1;
-                        f2_split(e, e0, e1);
-                        pk[c][u] = pack_f16x2(e0, e1);
-                    }
+        // The values of the tile at hand are times 2^e: exponents are lower by e and the sum is times 2^-e, so
+        // that nothing is to be done while e stays. `mixed`: it does not, and its bits are read a tile
+        // ahead, a lane each.
+        const __half *v0 = p.v + (size_t)bh * p.s_pad * D;
+        auto e_of = [](uint32_t code) { return kMaxExp - kExpStep * (int)code; };
+        uint32_t c_min = ~0u, c_max = 0;
+#pragma unroll 4
+        for (int i = lane; i < nt; i += 32) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(v0 + (size_t)i * kTile * D);
+            const uint32_t code = (v.x & 1u) | (v.x >> 15 & 2u) | (v.y & 1u) << 2;
+            c_min = min(c_min, code);
+            c_max = max(c_max, code);
+        }
+        c_min = __reduce_min_sync(0xffffffffu, c_min);
+        c_max = __reduce_max_sync(0xffffffffu, c_max);
+        int e = e_of(c_min);
+        auto attend = [&](auto mixed) {
+            const unsigned short *e_at = reinterpret_cast<const unsigned short *>(v0) + (lane & 3);
+            uint32_t e_bit = 0;
+            if constexpr (decltype(mixed)::value) e_bit = *e_at;
+            for (int i = 0; i < nt; ++i) {
+                if constexpr (decltype(mixed)::value) {
+                    const int e_i = e_of(__ballot_sync(0xffffffffu, e_bit & 1u) & ((1u << kExpBits) - 1));
+                    if (i + 1 < nt) e_bit = e_at[(size_t)(i + 1) * kTile * D];
+                    m_base += (float)(e_i - e);
+                    l_run *= pow2(e - e_i);
+                    e = e_i;
                 }
-                float a0, a1, b0, b1;
-                f2_split(acc[0], a0, a1);
-                f2_split(acc[1], b0, b1);
-                l_run += (a0 + a1) + (b0 + b1);
-            }
-            // the product before has read P and added to O: the row's earlier output to the new base, then P
-            if (i > 0) wait_warp(lead, bar(SM::o(qt, i - 1)), ring_parity(i - 1), abort_flag);
-            tc_fence_after();
-            __syncwarp();  // the row-dependent branches above rejoin before the TMEM accesses
-            if (__any_sync(0xffffffffu, move) && i > 0) {
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t r[32];
-                    tmem_ld32(o_col + 32 * c, r);
+                wait_warp(lead, bar(SM::s(qt, i)), ring_parity(i), abort_flag);
+                tc_fence_after();
+                float x[kTile];
+                {
+                    uint32_t r[64];
+                    tmem_ld64(s_col, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
-                    tmem_st32(o_col + 32 * c, r);
-                }
-            }
+                    for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(r[j]);
+                    tmem_ld64(s_col + 64, r);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(SM::B_SR));  // S may be the other query tile's now
 #pragma unroll
-            for (int c = 0; c < kTile / 32; ++c) tmem_st16(p_col + 16 * c, pk[c]);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(SM::B_P + qt));
-        }
+                    for (int j = 0; j < 64; ++j) x[64 + j] = __uint_as_float(r[j]);
+                }
+                const int j0 = i * kTile;
+                if (!(row_ok && j0 + kTile - 1 <= pos_row)) {
+#pragma unroll
+                    for (int j = 0; j < kTile; ++j) x[j] = (row_ok && j0 + j <= pos_row) ? x[j] : -INFINITY;
+                }
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // short chains
+#pragma unroll
+                for (int j = 0; j < kTile; j += 8) {
+                    mx4[0] = max3(mx4[0], x[j], x[j + 1]);
+                    mx4[1] = max3(mx4[1], x[j + 2], x[j + 3]);
+                    mx4[2] = max3(mx4[2], x[j + 4], x[j + 5]);
+                    mx4[3] = max3(mx4[3], x[j + 6], x[j + 7]);
+                }
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+                const bool move = mx > m_base + kLazy;
+                float f = 1.f;  // factor of the row's earlier output and sum
+                if (move) {
+                    f = exp2f(m_base - mx);  // 0 while the row had no key (m_base = -inf)
+                    m_base = mx;
+                    l_run *= f;
+                }
+                const float mu = (m_base == -INFINITY) ? 0.f : m_base;
+                uint32_t pk[kTile / 32][16];  // P, two keys a word
+                {
+                    const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nmu2 = f2(-mu, -mu);
+                    uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < kTile / 32; ++c) {
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) {
+                            const uint64_t y = f2_fma(f2(x[c * 32 + 2 * u], x[c * 32 + 2 * u + 1]), sc2, nmu2);
+                            uint64_t e;
+                            if ((u & 3) == 3) {
+                                e = exp2_fma_x2(y);
+                            } else {
+                                float a0, a1;
+                                f2_split(y, a0, a1);
+                                e = f2(ex2_approx(a0), ex2_approx(a1));
+                            }
+                            acc[u & 1] = f2_add(acc[u & 1], e);
+                            float e0, e1;
+                            f2_split(e, e0, e1);
+                            pk[c][u] = pack_f16x2(e0, e1);
+                        }
+                    }
+                    float a0, a1, b0, b1;
+                    f2_split(acc[0], a0, a1);
+                    f2_split(acc[1], b0, b1);
+                    l_run += (a0 + a1) + (b0 + b1);
+                }
+                // the product before has read P and added to O: the row's earlier output to the new base, then P
+                if (i > 0) wait_warp(lead, bar(SM::o(qt, i - 1)), ring_parity(i - 1), abort_flag);
+                tc_fence_after();
+                __syncwarp();  // the row-dependent branches above rejoin before the TMEM accesses
+                if (__any_sync(0xffffffffu, move) && i > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(o_col + 32 * c, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+                        tmem_st32(o_col + 32 * c, r);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < kTile / 32; ++c) tmem_st16(p_col + 16 * c, pk[c]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(SM::B_P + qt));
+            }
+        };
+        if (c_min == c_max) attend(std::false_type());
+        else attend(std::true_type());
         wait_warp(lead, bar(SM::o(qt, nt - 1)), ring_parity(nt - 1), abort_flag);
         const bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
         if (ok) {
             tc_fence_after();
-            const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+            const float inv = l_run > 0.f ? pow2(-e) / l_run : 0.f;
             const int t0 = t_first + qt * kTile + (row & ~3);
             const bool whole = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
             __nv_bfloat16 *dst = p.o + (((size_t)b * p.T + t0) * p.H + h) * D + (lane & 3) * 16;

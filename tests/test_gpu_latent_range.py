@@ -1,0 +1,84 @@
+"""attn_latent_prefill on values far from one, against the definition in 64 bits.
+
+Tolerance: o is rounded once to bf16 (2^-8 of the value). Keys, values, queries and weights are fp16
+times a power of two (half a step, 2^-11 of each; three values of a tile 2^-10): a score moves by at
+most 3 * 2^-11 of its terms, weights by as much, by 2^-11 themselves and by the exponential's 2^-13. The
+part of a score that comes from the shared rows is exact here (small integers and powers of two).
+"""
+import pytest
+import torch
+
+import hybrid_mixer_decoding_b200 as hmd
+from test_gpu_latent import DR, Latent, prefill
+
+pytestmark = pytest.mark.gpu
+
+
+class Split(Latent):
+    """The first half of the latent dims makes the keys, the second half the values, so that either can
+    have any size at any position; the shared part of the rows and queries is zero."""
+
+    def __init__(self, L, H, d, d_c, seed, T=None, q_scale=0.05):
+        super().__init__([L], H, d, d_c, seed)
+        self.w_uk[..., d_c // 2:] = 0
+        self.w_uv[..., :d_c // 2] = 0
+        T = T or L
+        self.q, self.c = self.randn(1, T, H, d + DR, scale=q_scale), self.randn(1, T, d_c + DR)
+        self.q[..., d:], self.c[..., d_c:] = 0, 0
+
+    def check(self, o, scale, first=0, extra=0.0):
+        n, d, d_c = self.q.shape[1], self.d, self.d_c
+        C = self.rows(0, first + n).double()
+        K = torch.einsum("jc,hnc->hjn", C[:, :d_c], self.w_uk.double())
+        V = torch.einsum("jc,hvc->hjv", C[:, :d_c], self.w_uv.double())
+        qn, qr = self.q[0].double().transpose(0, 1).split([d, DR], -1)
+        hidden = torch.arange(first + n, device="cuda")[None] > first + torch.arange(n, device="cuda")[:, None]
+        x = (qn @ K.transpose(1, 2) + qr @ C[:, d_c:].T) * scale
+        p = torch.softmax(x.masked_fill(hidden, -torch.inf), -1)
+        ref, pv = (p @ V).transpose(0, 1), (p @ V.abs()).transpose(0, 1)
+        terms = (qn.abs() @ K.abs().transpose(1, 2)).amax() * scale
+        assert terms < 2
+        tol = 2.0 ** -8 * ref.abs() + (2 * 3 * 2.0 ** -11 * terms + 2 * 2.0 ** -11 + 2.0 ** -13) * pv + extra
+        err = (o[0].double() - ref).abs()
+        assert (err <= tol).all(), (err / tol).max().item()
+        assert hmd.hmd_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("d,d_c", [(128, 512), (64, 256)])
+@pytest.mark.parametrize("e", [0, 16, 20, 24, 40, 64])
+def test_values_of_any_size(d, d_c, e):
+    c = Split(300, 3, d, d_c, seed=e)
+    c.w_uv *= 2.0 ** -e
+    c.check(prefill(c, c.q, c.c, scale=0.125), 0.125)
+
+
+@pytest.mark.parametrize("d,d_c", [(128, 512), (64, 256)])
+@pytest.mark.parametrize("gap", [0, 20, 120])
+def test_values_whose_size_changes_along_the_sequence(d, d_c, gap):
+    """Every second 128 positions hold values 2^-30 of the others' size, and scores that are `gap` / 4
+    higher: the small ones count for nothing, for as much, or for all."""
+    c = Split(700, 2, d, d_c, seed=gap)
+    small = torch.arange(700, device="cuda") // 128 % 2 == 1
+    c.c[0, small, d_c // 2:d_c] *= 2.0 ** -30
+    c.c[0, small, d_c] = gap
+    c.q[..., d] = 1
+    c.check(prefill(c, c.q, c.c, scale=0.25), 0.25)
+
+
+def test_zero_values_beside_small_ones():
+    c = Split(300, 2, 64, 128, seed=3)
+    c.c[0, :128, 64:128] = 0
+    c.c[0, 128:, 64:128] *= 2.0 ** -40
+    o = prefill(c, c.q, c.c, scale=0.125)
+    assert (o[0, :128] == 0).all()
+    c.check(o, 0.125)
+
+
+def test_values_beyond_fp16_are_clipped_and_reported():
+    c = Split(200, 2, 64, 128, seed=9)
+    c.w_uv *= 2.0 ** 18
+    o = prefill(c, c.q, c.c, scale=0.125)
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVWARN_RANGE
+    assert o.isfinite().all() and o.abs().max() <= 65536
+    c.w_uv *= 2.0 ** -18
+    c.check(prefill(c, c.q, c.c, scale=0.125), 0.125)
