@@ -57,7 +57,10 @@ constexpr int kDR = 64;              // the rows' part shared as it is by every 
 constexpr int kTile = 128;           // positions per key tile, queries per query tile
 constexpr uint32_t kBlk = kTile * 128;  // one [128 rows][128 B] block, 128-byte swizzle
 constexpr float kHalfMax = 65504.f;
-constexpr float kLazy = 8.f;         // log2 headroom before a row's exponent base moves
+// A row's weights are held relative to a base that moves when the largest is above 2^kTop, then to
+// 2^kFresh: fp16 holds a weight to 2^-11 down to 2^-23 of the row's largest, and to 2^-34 of that below. (With
+// the largest at 1, 100,000 keys of 2^-25.5 each were in the row's sum and not in its output.)
+constexpr float kTop = 15.f, kFresh = 9.f;
 // A head's values in a tile are stored times 2^e, e = kMaxExp - kExpStep * code, the code in the last bits of
 // its first kExpBits values. The largest e leaves a row's sum, which has every weight times 2^e, far from
 // fp32's ends: 2^75 a key, and the 2^-125 at which the softmax clamps a masked key's weight is 2^-65.
@@ -735,11 +738,12 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                     mx4[3] = max3(mx4[3], x[j + 6], x[j + 7]);
                 }
                 const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
-                const bool move = mx > m_base + kLazy;
+                const bool move = mx > m_base + kTop;
                 float f = 1.f;  // factor of the row's earlier output and sum
                 if (move) {
-                    f = exp2f(m_base - mx);  // 0 while the row had no key (m_base = -inf)
-                    m_base = mx;
+                    const float to = mx - kFresh;
+                    f = exp2f(m_base - to);  // 0 while the row had no key (m_base = -inf)
+                    m_base = to;
                     l_run *= f;
                 }
                 const float mu = (m_base == -INFINITY) ? 0.f : m_base;

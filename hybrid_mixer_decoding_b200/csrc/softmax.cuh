@@ -30,7 +30,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// 2^x for two lanes on the FMA pipe, for x <= 8: 2^x = 2^n 2^f with n = x rounded to the
+// 2^x for two lanes on the FMA pipe, for x <= 15: 2^x = 2^n 2^f with n = x rounded to the
 // nearest integer (adding 1.5 * 2^23 rounds it into the low mantissa bits) and f = x - n in
 // [-1/2, 1/2], 2^f by a cubic fitted to it on that interval (iteratively reweighted least
 // squares at Chebyshev nodes; largest relative error 7.5e-5, below the rounding of P to bf16 or fp16).

@@ -1,4 +1,4 @@
-"""attn_latent_prefill on values far from one, against the definition in 64 bits.
+"""attn_latent_prefill on values and weights far from one, against the definition in 64 bits.
 
 Tolerance: o is rounded once to bf16 (2^-8 of the value). Keys, values, queries and weights are fp16
 times a power of two (half a step, 2^-11 of each; three values of a tile 2^-10): a score moves by at
@@ -72,6 +72,29 @@ def test_zero_values_beside_small_ones():
     o = prefill(c, c.q, c.c, scale=0.125)
     assert (o[0, :128] == 0).all()
     c.check(o, 0.125)
+
+
+@pytest.mark.parametrize("d,d_c", [(128, 256), (64, 128)])
+def test_many_keys_of_little_weight(d, d_c):
+    """One key takes nearly all of the weight and has no value; 100,000 others, 2^-25.5 of its weight
+    each, make the output. Weights are held to 2^-34 of a row's largest."""
+    L, T = 100_000, 3
+    c = Split(L + T, 1, d, d_c, seed=5, T=T)
+    c.pool.zero_()
+    t = c.table[0].long()
+    pos = torch.arange(L, device="cuda")
+    rows = c.randn(L, d_c + DR)
+    rows[:, :d_c // 2], rows[:, d_c:] = 0, 0
+    rows[0, :d_c], rows[0, d_c] = 0, 17.625   # 25.4 bits above the others
+    rows[:, d_c // 2:d_c] = rows[:, d_c // 2:d_c].abs()
+    c.pool[t[pos // 64], pos % 64] = rows
+    c.w_uv.abs_()
+    c.q[..., d], c.q[..., :d] = 1, 0
+    c.c[..., :d_c // 2] = 0
+    c.c[..., d_c // 2:d_c].abs_()
+    V = torch.einsum("jc,vc->jv", rows[:, :d_c].double(), c.w_uv[0].double())
+    o = prefill(c, c.q, c.c, prefix=[L], prompt=[T], scale=1.0)
+    c.check(o, 1.0, first=L, extra=2.0 ** -34 * V.abs().sum(0))
 
 
 def test_values_beyond_fp16_are_clipped_and_reported():
