@@ -15,8 +15,9 @@
 // everywhere, or the same; where it is not, the softmax lowers a tile's exponents by e and adds its weights
 // times 2^e to the row's sum, so that tiles of any sizes add up (a loop of its own: in the common one this
 // took 2 to 4% of the kernel). e goes with the values, in the last bits of three of them (those to 2^-10). Keys and queries need no such factor:
-// what they lose below 2^-14, at most 2^-25, moves a score by 2^-25 scale sum |q| (or |k|), which is 4e-7
-// for 192 dims of size 1 and 0.03 at the end of fp16's range.
+// what they lose below 2^-14, at most 2^-25, moves a score by 2^-25 scale sum |q| (or |k|), with the usual
+// scale 4e-7 for 192 dims of size 1 and 0.03 at the end of fp16's range. So that this holds for any scale, the
+// power of two in one of 2 or more goes to the queries.
 //
 // Kernel 1 (rows): appends the new rows to the cache and converts every position's shared part
 // k_r to fp16. Kernel 2 (expand): one CTA per (128 positions, a share of the heads):
@@ -39,6 +40,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kernels.h"
@@ -98,7 +100,7 @@ struct PrefillParams {
     int h0, heads;          // this launch's heads h0 .. h0 + heads - 1
     int splits, per_split;  // kernel 2: shares of the heads
     int n_qb;               // kernel 3: query blocks of 256
-    float scale_log2;
+    float scale_log2, q_scale;  // scale * log2(e) without the power of two that the queries take
     __half *kr;             // [B][s_pad][64]
     __half *k, *v;          // [B][heads][s_pad][d]
 };
@@ -552,7 +554,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
             uint32_t y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float lo = bf16_lo(in[e]), hi = bf16_hi(in[e]);
+                float lo = bf16_lo(in[e]) * p.q_scale, hi = bf16_hi(in[e]) * p.q_scale;
                 out |= clip_half(lo);
                 out |= clip_half(hi);
                 y[e] = pack_f16x2(lo, hi);
@@ -879,7 +881,8 @@ cudaError_t launch_d(const LatentPrefillArgs &a, cudaStream_t s) {
     const size_t s_pad = padded(a.T, p.max_prefix);
     p.s_pad = (int)s_pad;
     p.n_qb = (a.T + 2 * kTile - 1) / (2 * kTile);
-    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.q_scale = a.scale >= 2.f ? exp2f((float)std::ilogb(a.scale)) : 1.f;
+    p.scale_log2 = a.scale / p.q_scale * 1.4426950408889634f;
     // the workspace: k_r of every position, then K and V of as many heads as fit
     const size_t kr_bytes = (size_t)a.B * s_pad * kDR * 2, head_bytes = (size_t)a.B * s_pad * D * 2 * 2;
     const int fit = (int)std::min<size_t>((size_t)a.H, (a.ws_bytes - kr_bytes) / head_bytes);

@@ -441,10 +441,11 @@ HMD_API hmd_status_t attn_latent_decode(int n_q, int B, int H, int d, int d_c, i
  *   heads run in groups (same results, bit for bit). Not in use by another call while this one
  *   runs. Allocates nothing.
  * Keys, values, queries and softmax weights are rounded to fp16 (2^-11, less than the bf16
- * output's rounding); a key, value or query beyond 65504 is clipped and sets HMD_DEVWARN_RANGE.
- * A head's values at 128 positions have a common power of two, so small ones are held to 2^-11, or
- * to 2^-20 of the largest of them, wherever that is 2^-66 or more; weights are held to 2^-11, or to
- * 2^-34 of the row's largest.
+ * output's rounding); a key, value or query beyond 65504 is clipped and sets HMD_DEVWARN_RANGE
+ * (queries are taken times the power of two in `scale`, where that is 2 or more). A head's values
+ * at 128 positions have a common power of two, so small ones are held to 2^-11, or to 2^-20 of the
+ * largest of them, wherever that is 2^-66 or more; weights are held to 2^-11, or to 2^-34 of the
+ * row's largest.
  * q, c, the weights, pool and o 16-byte aligned, workspace 32-byte aligned.                     */
 HMD_API size_t attn_latent_prefill_workspace_size(int B, int T, int H, int d, int d_c, int d_r,
                                                   int page_tokens, int max_prefix);

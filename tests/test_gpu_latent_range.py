@@ -1,4 +1,4 @@
-"""attn_latent_prefill on values and weights far from one, against the definition in 64 bits.
+"""attn_latent_prefill on values, weights and scales far from one, against the definition in 64 bits.
 
 Tolerance: o is rounded once to bf16 (2^-8 of the value). Keys, values, queries and weights are fp16
 times a power of two (half a step, 2^-11 of each; three values of a tile 2^-10): a score moves by at
@@ -95,6 +95,20 @@ def test_many_keys_of_little_weight(d, d_c):
     V = torch.einsum("jc,vc->jv", rows[:, :d_c].double(), c.w_uv[0].double())
     o = prefill(c, c.q, c.c, prefix=[L], prompt=[T], scale=1.0)
     c.check(o, 1.0, first=L, extra=2.0 ** -34 * V.abs().sum(0))
+
+
+@pytest.mark.parametrize("e", [-6, 6, 20])
+def test_scales_of_any_size(e):
+    """Queries 2^-e of the usual size with a scale of 2^e: the same scores."""
+    c = Split(300, 2, 128, 512, seed=30 + e)
+    c.q *= 2.0 ** -e
+    c.check(prefill(c, c.q, c.c, scale=0.125 * 2.0 ** e), 0.125 * 2.0 ** e)
+
+
+@pytest.mark.parametrize("scale", [1.0, 1.999, 2.0, 3.0, 40.0])
+def test_scales_on_both_sides_of_two(scale):
+    c = Split(300, 2, 64, 128, seed=40, q_scale=0.01 / scale)
+    c.check(prefill(c, c.q, c.c, scale=scale), scale)
 
 
 def test_values_beyond_fp16_are_clipped_and_reported():
