@@ -730,10 +730,11 @@ def hmd_version() -> str:
 
 
 TEST_DELTA_DECODE, TEST_ATTN_SPLIT = 0, 1
+TEST_LATENT_ATTEND, TEST_LATENT_KV, TEST_LATENT_PROMPT = 2, 3, 4
 
 
 def hmd_test_arm_copy_skip(kernel: int, cta: int, wait_ns: int) -> None:
     """Arm a one-shot missing copy in CTA `cta` of this thread's next launch of `kernel`
-    (TEST_DELTA_DECODE or TEST_ATTN_SPLIT), with every bounded wait of that launch limited to
+    (one of the TEST_ numbers above), with every bounded wait of that launch limited to
     wait_ns: the failure-detection tests' way to make a wait run out without an invalid access."""
     _check("hmd_test_arm_copy_skip", lib().hmd_test_arm_copy_skip(kernel, cta, wait_ns))

@@ -55,7 +55,7 @@ hmd_status_t fail(hmd_status_t s) {
 hmd_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? HMD_OK : fail(HMD_ERR_CUDA); }
 
 // armed fault injections of this host thread (hmd_test_arm_copy_skip), one per test kernel
-thread_local hmd::CopySkip t_skip[2];
+thread_local hmd::CopySkip t_skip[HMD_TEST_LATENT_PROMPT + 1];
 
 cudaStream_t as_stream(hmd_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
@@ -90,8 +90,8 @@ CopySkip take_copy_skip(int kernel) {
 extern "C" {
 
 hmd_status_t hmd_test_arm_copy_skip(hmd_test_kernel_t kernel, int cta, uint64_t wait_ns) {
-    if ((kernel != HMD_TEST_DELTA_DECODE && kernel != HMD_TEST_ATTN_SPLIT) || cta < -1 ||
-        wait_ns < 1000 || wait_ns > 2000000000ull)
+    if (kernel < HMD_TEST_DELTA_DECODE || kernel > HMD_TEST_LATENT_PROMPT || cta < -1 || wait_ns < 1000 ||
+        wait_ns > 2000000000ull)
         return fail(HMD_ERR_ARG);
     if (cta == -1) {  // disarm
         t_skip[kernel] = hmd::CopySkip{};
@@ -699,6 +699,7 @@ hmd_status_t attn_latent_decode(int n_q, int B, int H, int d, int d_c, int d_r, 
     a.w_uk_head = w_uk_head; a.w_uv_head = w_uv_head;
     a.pool = pool; a.n_pages = n_pages; a.page_table = page_table; a.max_pages = max_pages;
     a.seq_lens = seq_lens; a.max_seq_len = max_seq_len; a.o = o; a.workspace = workspace;
+    a.skip = hmd::take_copy_skip(HMD_TEST_LATENT_ATTEND);
     return from_cuda(hmd::launch_latent_decode(a, as_stream(stream)));
 }
 
@@ -745,6 +746,8 @@ hmd_status_t attn_latent_prefill(int B, int T, int H, int d, int d_c, int d_r, i
     a.prefix_lens = prefix_lens; a.max_prefix = max_prefix; a.prompt_lens = prompt_lens;
     a.pool = pool; a.n_pages = n_pages; a.page_table = page_table; a.max_pages = max_pages;
     a.o = o; a.workspace = workspace; a.ws_bytes = ws_bytes;
+    a.skip_kv = hmd::take_copy_skip(HMD_TEST_LATENT_KV);
+    a.skip_prompt = hmd::take_copy_skip(HMD_TEST_LATENT_PROMPT);
     return from_cuda(hmd::launch_latent_prefill(a, as_stream(stream)));
 }
 

@@ -57,8 +57,8 @@ auto once_per_device(F f) -> decltype(f()) {
 hmd_status_t record_status(hmd_status_t s);
 
 // One-shot fault injection for the failure-detection tests (hmd_test_arm_copy_skip): the next
-// launch of `kernel` on this host thread has CTA `cta` arm its first copy barrier without
-// issuing the copy, and every bounded wait in it gives up after wait_ns.
+// launch of `kernel` on this host thread has CTA `cta` arm its first copy barrier for bytes that
+// no copy brings, and every bounded wait in it gives up after wait_ns.
 struct CopySkip {
     int cta = -1;                              // -1: nothing armed
     unsigned long long wait_ns = 2000000000ull;  // the normal 2 s limit
@@ -222,6 +222,7 @@ struct LatentDecodeArgs {
     int max_seq_len;
     void *o;
     void *workspace;
+    CopySkip skip;  // fault injection (tests only); inactive by default
 };
 bool latent_supported(int d, int d_c, int d_r, int page_tokens);
 size_t latent_decode_ws_bytes(int nq, int B, int H, int d_c, int max_seq_len);
@@ -243,6 +244,7 @@ struct LatentPrefillArgs {
     void *o;
     void *workspace;
     size_t ws_bytes;
+    CopySkip skip_kv, skip_prompt;  // fault injection (tests only); inactive by default
 };
 // bytes for `heads` heads at once (the call runs in groups of as many heads as fit)
 size_t latent_prefill_ws_bytes(int B, int T, int heads, int d, int max_prefix);

@@ -73,6 +73,8 @@ struct LatentParams {
     int4 *start;     // [n_ranges + 1]: a range's first page, its sequence, that sequence's first page
                      // and its length
     int2 *ranges;    // [B]: a sequence's ranges [x, y)
+    int skip_cta;    // of kernel 2: see CopySkip
+    unsigned long long wait_ns;
 };
 
 // Pages of a sequence: none for an unused row or a length that is refused.
@@ -366,6 +368,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
     if (tid == 0) {
         for (int i = 0; i < SM::N_BARS; ++i)
             mbar_init(bar(i), i == SM::B_P ? 4 : (i == SM::B_Q || i == SM::B_SR) ? 2 : 1);
+        // a test may have the first unit wait for bytes that no copy brings
+        if ((int)blockIdx.x == p.skip_cta) mbar_expect_tx(full(0, 0), 16);
         fence_barrier_init();
         *abort_flag = (sb & 1023u) ? 1 : 0;  // (the swizzle needs 1024; else every wait gives up)
         prefetch_tmap(&tmc);
@@ -390,6 +394,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
 
+    int n_issued = 0;  // of warp 4: units of the ring
     if (warp == 4) {
         // ===== copies into the ring: each sequence's queries, then its pages (the warp converged) ===
         const bool lead = elect_one();
@@ -426,7 +431,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
                 if (v < NU) {
                     const unsigned long long now = globaltimer_ns();
                     if (t0 == 0) t0 = now;
-                    const bool late = now - t0 > kWaitLimitNs;
+                    const bool late = now - t0 > p.wait_ns;
                     if (late) *abort_flag = 1;
                     ok = !__any_sync(0xffffffffu, late || *abort_flag);
                     if (!ok) return;
@@ -447,14 +452,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
             }
             if (ok && w.at < end) w.seek(p, end);
         }
-        if (!ok && lead) {
-            // the copies in flight land (bounded) before shared memory is released
-            atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
-            for (int i = max(0, issued - NS * NU); i < issued; ++i) {
-                const int ki = i / NU, v = i % NU;
-                (void)mbar_wait_bounded(full(ki % NS, v == 0 ? NP : v - 1), (ki / NS) & 1);
-            }
-        }
+        if (!ok && lead) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+        n_issued = issued;
         __syncwarp();
     } else if (warp == 5) {
         // ================= scores (the warp converged) =========================================
@@ -472,7 +471,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
             const bool asks = lane < NU || (lane == NU && s > 0) || (lane == NU + 1 && first);
             const uint32_t b = lane < NU ? full(st, lane) : lane == NU ? bar(SM::B_SR) : bar(SM::B_Q);
             const uint32_t parity = lane < NU ? (ks / NS) & 1 : lane == NU ? (s - 1) & 1 : seg & 1;
-            ok = wait_warp(asks, b, parity, abort_flag);
+            ok = wait_warp(asks, b, parity, abort_flag, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
             const Desc kd = d_k.at(st * PAGE);
@@ -512,7 +511,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
         int kp = 1;
         bool ok = true;
         for (int pv = 0; pv < n_pages; ++pv) {
-            ok = wait_warp(lead, bar(SM::B_P), pv & 1, abort_flag);
+            ok = wait_warp(lead, bar(SM::B_P), pv & 1, abort_flag, p.wait_ns);
             if (!ok) break;
             // O^T += C^T P^T, unit by unit; each unit's slot is free after it
             tc_fence_after();
@@ -557,7 +556,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
                 // this sequence's queries to TMEM: lane = row of the image (32 hi, then 32 lo). The
                 // scores of the sequence before are complete, so its queries are not read any more
                 const int st = item % NS;
-                ok &= wait_warp(lane < NU, full(st, min(lane, NP)), (item / NS) & 1, abort_flag);
+                ok &= wait_warp(lane < NU, full(st, min(lane, NP)), (item / NS) & 1, abort_flag, p.wait_ns);
                 const uint8_t *row = sm + st * PAGE + (warp * 32 + lane) * 128;
                 const bool none = group * kRows + lane >= p.nq * p.H;  // no such query: its row is not written
 #pragma unroll 1
@@ -577,8 +576,9 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
                 tc_fence_before();
                 fence_proxy_async_smem();  // the slot's next filling comes after these reads
                 bar_scores();
-                if (warp == 0 && lane < NU) mbar_arrive(free_(st, lane));
-                if (lane == 0) mbar_arrive(bar(SM::B_Q));
+                // (not after a wait that gave up: the slot's copy may not have landed)
+                if (ok && warp == 0 && lane < NU) mbar_arrive(free_(st, lane));
+                if (ok && lane == 0) mbar_arrive(bar(SM::B_Q));
             }
             ++item;
             // the last position this row sees (-1: no such row)
@@ -592,7 +592,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
                 if (warp < 2) {
                     // the scores and, for page_ok, the page
                     ok &= wait_warp(lane < 2, lane ? full(st, 0) : bar(SM::B_S),
-                                    (lane ? item / NS : k) & 1, abort_flag);
+                                    (lane ? item / NS : k) & 1, abort_flag, p.wait_ns);
                     tc_fence_after();
                     {
                         uint32_t r[64];
@@ -663,7 +663,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
                     bar_softmax();
                     if (w.at > w.seg_begin) {
                         // the earlier output to the new bases, once the product into it is done
-                        ok = wait_warp(lead, bar(SM::B_O), (k - 1) & 1, abort_flag);
+                        ok = wait_warp(lead, bar(SM::B_O), (k - 1) & 1, abort_flag, p.wait_ns);
                         tc_fence_after();
 #pragma unroll 1
                         for (int u = 0; u < NP; ++u) {
@@ -693,7 +693,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     // P [32 rows][64 keys], rows of 128 bytes, 128-byte swizzle, once the product
                     // before has read it
-                    if (k > 0) ok &= wait_warp(lead, bar(SM::B_O), (k - 1) & 1, abort_flag);
+                    if (k > 0) ok &= wait_warp(lead, bar(SM::B_O), (k - 1) & 1, abort_flag, p.wait_ns);
                     uint8_t *row = sm + SM::OFF_P + lane * 128;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -716,7 +716,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
                 if (lane == 0) mbar_arrive(bar(SM::B_P));
             }
             const size_t piece = part_index(p, range, b, group);
-            if (ok) ok = wait_warp(lead, bar(SM::B_O), (k - 1) & 1, abort_flag);
+            if (ok) ok = wait_warp(lead, bar(SM::B_O), (k - 1) & 1, abort_flag, p.wait_ns);
             ok = !bar_softmax_or(!ok);
             if (!ok) {
                 // this piece and the range's later ones are marked as missing
@@ -751,6 +751,13 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag && warp == 4 && lane == 0) {
+        // the copies in flight land (bounded) before shared memory is released
+        for (int i = max(0, n_issued - NS * NU); i < n_issued; ++i) {
+            const int ki = i / NU, v = i % NU;
+            (void)mbar_wait_bounded(full(ki % NS, v == 0 ? NP : v - 1), (ki / NS) & 1, p.wait_ns);
+        }
+    }
     if (warp == 5) {
         __syncwarp();
         tc_fence_after();
@@ -1049,6 +1056,7 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t s) {
     p.start = reinterpret_cast<int4 *>(ws + pl.off_start);
     p.ranges = reinterpret_cast<int2 *>(ws + pl.off_ranges);
     p.cum = reinterpret_cast<int32_t *>(ws + pl.off_cum);
+    p.skip_cta = a.skip.cta; p.wait_ns = a.skip.wait_ns;
     cudaError_t e = a.d == 128 ? launch_absorb<128>(p, s) : launch_absorb<64>(p, s);
     if (e != cudaSuccess) return e;
     switch (a.d_c / 128) {

@@ -103,6 +103,8 @@ struct PrefillParams {
     float scale_log2, q_scale;  // scale * log2(e) without the power of two that the queries take
     __half *kr;             // [B][s_pad][64]
     __half *k, *v;          // [B][heads][s_pad][d]
+    int skip_cta;                // of the launch: see CopySkip
+    unsigned long long wait_ns;
 };
 
 // A sequence's cached positions and new tokens; both 0 if the lengths were refused.
@@ -248,6 +250,8 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     if (tid == 0) {
         for (int i = 0; i < SM::N_BARS; ++i)
             mbar_init(bar(i), i >= SM::B_READ && i < SM::B_READ + kExpAcc ? 4 : i == SM::B_MOVED ? 8 : 1);
+        // a test may have the first stage wait for bytes that no copy brings
+        if ((int)blockIdx.x == p.skip_cta) mbar_expect_tx(bar(SM::B_WFULL), 16);
         fence_barrier_init();
         *abort_flag = 0;
     }
@@ -260,6 +264,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+    int n_loaded = 0;  // of warp 8: stages of weights
 
     if (warp == 8) {
         const bool lead = elect_one();
@@ -300,31 +305,28 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
                                bar(SM::B_A), kc * 64, pg[h] * kPT);
         bool ok = true;
         while (n < n_all) {
-            if (round > 0) ok = wait_warp(lead, bar(SM::B_WFREE + w), (round - 1) & 1, abort_flag);
-            else if (n == SM::EARLY) ok = wait_warp(lead, bar(SM::B_MOVED), 0, abort_flag);
+            if (round > 0) ok = wait_warp(lead, bar(SM::B_WFREE + w), (round - 1) & 1, abort_flag, p.wait_ns);
+            else if (n == SM::EARLY) ok = wait_warp(lead, bar(SM::B_MOVED), 0, abort_flag, p.wait_ns);
             if (!ok) break;
             load_w();
         }
-        if (!ok && lead) {
-            // the copies in flight land (bounded) before shared memory is released
-            atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
-            (void)mbar_wait_bounded(bar(SM::B_A), 0);
-            for (int i = max(0, n - SM::NW); i < n; ++i)
-                (void)mbar_wait_bounded(bar(SM::B_WFULL + i % SM::NW), (i / SM::NW) & 1);
-        }
+        if (!ok && lead) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+        n_loaded = n;
         __syncwarp();
     } else if (warp == 9) {
         const bool lead = elect_one();
         const Desc d_w(smem_desc_sw128(sb, 16, 1024));
         constexpr uint32_t ID = idesc_bf16(128, 128, 0, 0);
-        auto wait = [&](int i, uint32_t parity) { wait_warp(lead, bar(i), parity, abort_flag); };
-        wait(SM::B_MOVED, 0);
+        auto wait = [&](int i, uint32_t parity) { return wait_warp(lead, bar(i), parity, abort_flag, p.wait_ns); };
+        bool ok = wait(SM::B_MOVED, 0);
         int w = 0, round = 0;
-        for (int st = 0; st < n_steps; ++st) {
+        for (int st = 0; st < n_steps && ok; ++st) {
             const int acc = st % kExpAcc;
-            if (st >= kExpAcc) wait(SM::B_READ + acc, (st / kExpAcc - 1) & 1);
-            for (int kc = 0; kc < n_kc; ++kc) {
-                wait(SM::B_WFULL + w, round & 1);
+            if (st >= kExpAcc) ok = wait(SM::B_READ + acc, (st / kExpAcc - 1) & 1);
+            for (int kc = 0; kc < n_kc && ok; ++kc) {
+                // after a wait that gave up nothing is issued: no stage is freed whose copy has not landed
+                ok = wait(SM::B_WFULL + w, round & 1);
+                if (!ok) break;
                 tc_fence_after();
                 const Desc wd = d_w.at(SM::stage(w));
 #pragma unroll
@@ -354,7 +356,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         const bool lead = elect_one();
         bool out = false;
         // the latent rows to TMEM as the products' A operand, half of the dims per four warps
-        wait_warp(lead, bar(SM::B_A), 0, abort_flag);
+        wait_warp(lead, bar(SM::B_A), 0, abort_flag, p.wait_ns);
         if (!uniform(*abort_flag)) {
             const int row = quarter * 32 + lane;
             for (int kc = warp >> 2; kc < n_kc; kc += 2) {
@@ -373,7 +375,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         }
         for (int st = warp >> 2; st < n_steps; st += 2) {
             const int acc = st % kExpAcc;
-            const bool ready = wait_warp(lead, bar(SM::B_ACC + acc), (st / kExpAcc) & 1, abort_flag);
+            const bool ready = wait_warp(lead, bar(SM::B_ACC + acc), (st / kExpAcc) & 1, abort_flag, p.wait_ns);
             const bool values = STEPS == 1 || st % 2 == 1;  // the same in all steps of a set of warps
             if (!ready && !values) break;  // reported by the products' warp
             tc_fence_after();
@@ -451,6 +453,12 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag && warp == 8 && lane == 0) {
+        // the copies in flight land (bounded) before shared memory is released
+        (void)mbar_wait_bounded(bar(SM::B_A), 0, p.wait_ns);
+        for (int i = max(0, n_loaded - SM::NW); i < n_loaded; ++i)
+            (void)mbar_wait_bounded(bar(SM::B_WFULL + i % SM::NW), (i / SM::NW) & 1, p.wait_ns);
+    }
     if (warp == 9) {
         __syncwarp();
         tc_fence_after();
@@ -517,6 +525,8 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     if (tid == 0) {
         for (int i = 0; i < SM::N_BARS; ++i)
             mbar_init(bar(i), i == SM::B_Q ? 8 : (i == SM::B_P || i == SM::B_P + 1 || i == SM::B_SR) ? 4 : 1);
+        // a test may have the first block wait for bytes that no copy brings
+        if ((int)blockIdx.x == p.skip_cta) mbar_expect_tx(bar(SM::B_FULL), 16);
         fence_barrier_init();
         *abort_flag = 0;
     }
@@ -570,6 +580,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     griddep_wait();  // keys and values are kernel 2's
 
     const int last = nt1 > 0;  // the last query tile
+    int n_loaded = 0;          // of warp 9: blocks
     if (warp == 9) {
         // ===== copies: the blocks of K_0, K_1, V_0, K_2, V_1, ... in the order of their use, block n into
         // slot n % NR (the warp converged) ========================================================
@@ -583,7 +594,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                 const RingFree by = old.freed_by(n_tiles);
                 const int free = by == kFreeOutput ? SM::o(last, i) : by == kFreeKeys ? SM::B_K + ring_barrier(i)
                                                                                       : SM::s(last, i);
-                ok = wait_warp(lead, bar(free), ring_parity(i), abort_flag);
+                ok = wait_warp(lead, bar(free), ring_parity(i), abort_flag, p.wait_ns);
                 if (!ok) break;
                 old.next(n_tiles);
             }
@@ -597,12 +608,8 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
             at.next(n_tiles);
             if (++slot == NR) slot = 0;
         }
-        if (!ok && lead) {
-            // the copies in flight land (bounded) before shared memory is released
-            atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
-            for (int i = max(0, n - NR); i < n; ++i)
-                (void)mbar_wait_bounded(bar(SM::B_FULL + i % NR), (i / NR) & 1);
-        }
+        if (!ok && lead) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
+        n_loaded = n;
         __syncwarp();
     } else if (warp == 8) {
         // ===== products: S_0(i+1), O_0(i), S_1(i+1), O_1(i) (the warp converged). A tile's scores are
@@ -620,13 +627,16 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         auto wait_for = [&](int n, int count, int i, int parity) {
             const int u = n + lane;
             const bool block = lane < count;
-            wait_warp(block || (lane == count && i >= 0), bar(block ? SM::B_FULL + u % NR : max(i, 0)),
-                      (block ? u / NR : parity) & 1, abort_flag);
+            const bool ok = wait_warp(block || (lane == count && i >= 0),
+                                      bar(block ? SM::B_FULL + u % NR : max(i, 0)),
+                                      (block ? u / NR : parity) & 1, abort_flag, p.wait_ns);
             tc_fence_after();
+            return ok;
         };
+        // after a wait that gave up nothing is issued: no block is freed whose copy has not landed
         auto issue_s = [&](int j, int i) {  // S = Q_j K_i^T
             const int n = ring_key<D>(i);
-            wait_for(n, j == 0 || i >= nt0 ? KB : 0, n_s > 0 ? SM::B_SR : -1, n_s - 1);
+            if (!wait_for(n, j == 0 || i >= nt0 ? KB : 0, n_s > 0 ? SM::B_SR : -1, n_s - 1)) return false;
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 const Desc k = d_k.at(((uint32_t)(n + kb) % NR) * kBlk);
@@ -638,10 +648,11 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
             }
             umma_commit_if(lead, bar(SM::s(j, i)));
             ++n_s;
+            return true;
         };
         auto issue_o = [&](int j, int i) {  // O_j (+)= P_j V_i, P_j from TMEM
             const int n = ring_value<D>(i, n_tiles);
-            wait_for(n, j == 0 || i >= nt0 ? VB : 0, SM::B_P + j, i);
+            if (!wait_for(n, j == 0 || i >= nt0 ? VB : 0, SM::B_P + j, i)) return false;
             const uint32_t slot = (uint32_t)n % NR;
             const uint32_t o = tmem + SM::T_O + 128 * j, pj = tmem + SM::T_P + 64 * j;
             const Desc v = d_v.at(slot * kBlk);
@@ -659,13 +670,14 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                     umma_ts_if(lead, o + 64, pj + 8 * kk, d_v.at(kk * 2048), ID_O64, kk > 0 ? 1u : more);
             }
             umma_commit_if(lead, bar(SM::o(j, i)));
+            return true;
         };
-        wait_warp(lead, bar(SM::B_Q), 0, abort_flag);
-        for (int i = -1; i < n_tiles; ++i) {
-            if (i + 1 < nt0) issue_s(0, i + 1);
-            if (i >= 0 && i < nt0) issue_o(0, i);
-            if (i + 1 < nt1) issue_s(1, i + 1);
-            if (i >= 0 && i < nt1) issue_o(1, i);
+        bool ok = wait_warp(lead, bar(SM::B_Q), 0, abort_flag, p.wait_ns);
+        for (int i = -1; i < n_tiles && ok; ++i) {
+            if (i + 1 < nt0) ok = issue_s(0, i + 1);
+            if (ok && i >= 0 && i < nt0) ok = issue_o(0, i);
+            if (ok && i + 1 < nt1) ok = issue_s(1, i + 1);
+            if (ok && i >= 0 && i < nt1) ok = issue_o(1, i);
         }
         if (lead) {
             if (*abort_flag) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
@@ -709,7 +721,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                     l_run *= pow2(e - e_i);
                     e = e_i;
                 }
-                wait_warp(lead, bar(SM::s(qt, i)), ring_parity(i), abort_flag);
+                wait_warp(lead, bar(SM::s(qt, i)), ring_parity(i), abort_flag, p.wait_ns);
                 tc_fence_after();
                 float x[kTile];
                 {
@@ -778,7 +790,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                     l_run += (a0 + a1) + (b0 + b1);
                 }
                 // the product before has read P and added to O: the row's earlier output to the new base, then P
-                if (i > 0) wait_warp(lead, bar(SM::o(qt, i - 1)), ring_parity(i - 1), abort_flag);
+                if (i > 0) wait_warp(lead, bar(SM::o(qt, i - 1)), ring_parity(i - 1), abort_flag, p.wait_ns);
                 tc_fence_after();
                 __syncwarp();  // the row-dependent branches above rejoin before the TMEM accesses
                 if (__any_sync(0xffffffffu, move) && i > 0) {
@@ -802,7 +814,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         };
         if (c_min == c_max) attend(std::false_type());
         else attend(std::true_type());
-        wait_warp(lead, bar(SM::o(qt, nt - 1)), ring_parity(nt - 1), abort_flag);
+        wait_warp(lead, bar(SM::o(qt, nt - 1)), ring_parity(nt - 1), abort_flag, p.wait_ns);
         const bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
         if (ok) {
             tc_fence_after();
@@ -835,6 +847,11 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag && warp == 9 && lane == 0) {
+        // the copies in flight land (bounded) before shared memory is released
+        for (int i = max(0, n_loaded - NR); i < n_loaded; ++i)
+            (void)mbar_wait_bounded(bar(SM::B_FULL + i % NR), (i / NR) & 1, p.wait_ns);
+    }
     if (warp == 8) {
         __syncwarp();
         tc_fence_after();
@@ -903,6 +920,8 @@ cudaError_t launch_d(const LatentPrefillArgs &a, cudaStream_t s) {
         p.h0 = h0;
         p.heads = std::min(group, a.H - h0);
         p.v = p.k + (size_t)a.B * p.heads * s_pad * D;
+        p.skip_cta = h0 == 0 ? a.skip_kv.cta : -1;
+        p.wait_ns = a.skip_kv.wait_ns;
         // shares of the heads per position tile: the fewest rounds of CTAs, each costing its heads
         // and about one more for loading the tile's latent rows
         const long long tiles = (long long)a.B * (s_pad / kTile), sms = device_sms();
@@ -926,6 +945,8 @@ cudaError_t launch_d(const LatentPrefillArgs &a, cudaStream_t s) {
         e = launch_pdl(latent_kv_kernel<D>, dim3((unsigned)(tiles * p.splits)), dim3(kExpandThreads),
                        ExpandSmem::ALLOC, s, tmc, tmuk, tmuv, p);
         if (e != cudaSuccess) break;
+        p.skip_cta = h0 == 0 ? a.skip_prompt.cta : -1;
+        p.wait_ns = a.skip_prompt.wait_ns;
         e = launch_pdl(latent_attend_prompt_kernel<D>, dim3((unsigned)(p.n_qb * bh)), dim3(kAttThreads),
                        AttendSmem<D>::ALLOC, s, tmk, tmv, tmr, p);
     }

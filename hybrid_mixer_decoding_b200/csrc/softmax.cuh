@@ -147,14 +147,18 @@ __device__ __forceinline__ bool mbar_test_warp(bool lead, uint32_t bar, uint32_t
 // leaves the others free to reach the next product before it. A wait that gave up shows in `abort`
 // too; a caller that goes on (over what memory holds, with waits that return at once) looks at the
 // flag before it writes results.
-__device__ __forceinline__ bool wait_warp(bool asks, uint32_t bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool wait_warp(bool asks, uint32_t bar, uint32_t parity, volatile int *abort,
+                                          unsigned long long limit_ns = kWaitLimitNs) {
     if (mbar_test_warp(asks, bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
     while (true) {
         if (mbar_test_warp(asks, bar, parity)) return true;
-        const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+        const bool late = globaltimer_ns() - t0 > limit_ns;
         if (late) *abort = 1;
-        if (__any_sync(0xffffffffu, late || *abort)) return false;
+        if (__any_sync(0xffffffffu, late || *abort)) {
+            __syncwarp();  // the flag comes before what any lane does next
+            return false;
+        }
     }
 }
 // The copies of a converged warp, issued by its lane with `lead` (the same holds for their operands).

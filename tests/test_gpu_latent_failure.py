@@ -1,0 +1,68 @@
+"""A copy that never lands, in the latent kernels and the scored step: the CTA gives up within its limit,
+reports HMD_DEVERR_TIMEOUT and leaves what depends on it as it was; every other output, and the next call,
+equals an undisturbed run bit for bit. See test_gpu_failure.py for the hook."""
+import pytest
+import torch
+
+import hybrid_mixer_decoding_b200 as hmd
+from hybrid_mixer_decoding_b200 import _lib
+from test_gpu_latent import BF, Latent, prefill
+
+pytestmark = pytest.mark.gpu
+WAIT_NS = 1_000_000  # 1 ms
+KEPT = 9.0  # what the outputs hold before
+
+
+def run_thrice(call, kernel, cta, pool):
+    """(outputs of an undisturbed call, of one with a missing copy); checks errors and a third call."""
+    before = pool.clone()
+    assert hmd.hmd_device_errors(clear=True) == 0
+    want = call()
+    torch.cuda.synchronize()
+    assert hmd.hmd_device_errors(clear=True) == 0
+    appended = pool.clone()
+    pool.copy_(before)
+    hmd.hmd_test_arm_copy_skip(kernel, cta, WAIT_NS)
+    got = call()
+    torch.cuda.synchronize()
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVERR_TIMEOUT
+    assert torch.equal(pool.view(torch.int16), appended.view(torch.int16))
+    assert torch.equal(call(), want)
+    assert hmd.hmd_device_errors(clear=True) == 0
+    return want, got
+
+
+def check_kept(want, got, kept):
+    assert (got[kept] == KEPT).all()
+    rest = torch.ones_like(got, dtype=torch.bool)
+    rest[kept] = False
+    assert torch.equal(got[rest], want[rest])
+
+
+@pytest.mark.parametrize("cta,sequence", [(0, 0), (2, 0), (3, 1), (8, 2)])
+def test_absorbed_attention(cta, sequence):
+    """One page per range: CTAs 0-2 have the pages of sequence 0, 3-7 of 1, 8 of 2."""
+    c = Latent([130, 300, 64], 16, 128, 512, seed=1)
+    q, new_c = c.new(1)
+    want, got = run_thrice(lambda: c.decode(q, new_c), _lib.TEST_LATENT_ATTEND, cta, c.pool)
+    check_kept(want, got, (sequence,))
+
+
+@pytest.mark.parametrize("d,d_c", [(128, 512), (64, 128)])
+def test_absorbed_attention_of_several_pages_and_row_groups(d, d_c):
+    """256 rows (token, head) in eight groups, ranges of several pages: group 1 of the first range has the
+    second half of the heads of token 0."""
+    c = Latent([5000], 64, d, d_c, seed=2)
+    q, new_c = c.new(4)
+    want, got = run_thrice(lambda: c.decode(q, new_c), _lib.TEST_LATENT_ATTEND, 1, c.pool)
+    check_kept(want, got, (0, 0, slice(32, 64)))
+
+
+@pytest.mark.parametrize("d,d_c", [(128, 512), (64, 256)])
+@pytest.mark.parametrize("T", [600, 1500])
+def test_prompt_attention(d, d_c, T):
+    """CTA 1 has the last query block of head 1 of sequence 0."""
+    c = Latent([T, T], 2, d, d_c, seed=3)
+    q, new_c = c.randn(2, T, 2, d + 64), c.randn(2, T, d_c + 64)
+    want, got = run_thrice(lambda: prefill(c, q, new_c), _lib.TEST_LATENT_PROMPT, 1, c.pool)
+    check_kept(want, got, (0, slice((T - 1) // 256 * 256, T), 1))
