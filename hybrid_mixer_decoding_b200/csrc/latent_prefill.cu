@@ -64,9 +64,10 @@ constexpr float kHalfMax = 65504.f;
 // the largest at 1, 100,000 keys of 2^-25.5 each were in the row's sum and not in its output.)
 constexpr float kTop = 15.f, kFresh = 9.f;
 // A head's values in a tile are stored times 2^e, e = kMaxExp - kExpStep * code, the code in the last bits of
-// its first kExpBits values. The largest e leaves a row's sum, which has every weight times 2^e, far from
+// its first kExpBits values (kMissing: kernel 2 gave up on the tile). The largest e leaves a row's sum, which has every weight times 2^e, far from
 // fp32's ends: 2^75 a key, and the 2^-125 at which the softmax clamps a masked key's weight is 2^-65.
 constexpr int kMaxExp = 60, kExpStep = 20, kExpBits = 3;
+constexpr uint32_t kMissing = 7;
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // Instruction descriptor of kind::f16 with fp16 A/B and fp32 D: the bf16 one with both type fields 0.
@@ -318,6 +319,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         const Desc d_w(smem_desc_sw128(sb, 16, 1024));
         constexpr uint32_t ID = idesc_bf16(128, 128, 0, 0);
         auto wait = [&](int i, uint32_t parity) { return wait_warp(lead, bar(i), parity, abort_flag, p.wait_ns); };
+        griddep_wait();  // what the first wait is for comes after it: the kernel before is not part of its limit
         bool ok = wait(SM::B_MOVED, 0);
         int w = 0, round = 0;
         for (int st = 0; st < n_steps && ok; ++st) {
@@ -458,6 +460,12 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         (void)mbar_wait_bounded(bar(SM::B_A), 0, p.wait_ns);
         for (int i = max(0, n_loaded - SM::NW); i < n_loaded; ++i)
             (void)mbar_wait_bounded(bar(SM::B_WFULL + i % SM::NW), (i / SM::NW) & 1, p.wait_ns);
+    }
+    if (*abort_flag && warp < 8) {
+        // not all of these heads' keys and values are there: the attention leaves out what needs them
+        for (int h = ha + tid; h < hb; h += 256)
+            *reinterpret_cast<uint2 *>(p.v + (((size_t)b * p.heads + h) * p.s_pad + pos0) * D) =
+                make_uint2(0x00010001u, 0x00000001u);
     }
     if (warp == 9) {
         __syncwarp();
@@ -712,10 +720,13 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         auto attend = [&](auto mixed) {
             const unsigned short *e_at = reinterpret_cast<const unsigned short *>(v0) + (lane & 3);
             uint32_t e_bit = 0;
+            bool missing = false;
             if constexpr (decltype(mixed)::value) e_bit = *e_at;
             for (int i = 0; i < nt; ++i) {
                 if constexpr (decltype(mixed)::value) {
-                    const int e_i = e_of(__ballot_sync(0xffffffffu, e_bit & 1u) & ((1u << kExpBits) - 1));
+                    const uint32_t code = __ballot_sync(0xffffffffu, e_bit & 1u) & ((1u << kExpBits) - 1);
+                    const int e_i = e_of(code);
+                    missing |= code == kMissing;
                     if (i + 1 < nt) e_bit = e_at[(size_t)(i + 1) * kTile * D];
                     m_base += (float)(e_i - e);
                     l_run *= pow2(e - e_i);
@@ -811,11 +822,13 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(SM::B_P + qt));
             }
+            if (missing) l_run = -1.f;
         };
-        if (c_min == c_max) attend(std::false_type());
+        if (c_min == c_max && c_max != kMissing) attend(std::false_type());
         else attend(std::true_type());
         wait_warp(lead, bar(SM::o(qt, nt - 1)), ring_parity(nt - 1), abort_flag, p.wait_ns);
-        const bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
+        // (o stays as it was, too, where kernel 2 gave up and reported it)
+        const bool ok = __all_sync(0xffffffffu, *abort_flag == 0 && !(l_run < 0.f));
         if (ok) {
             tc_fence_after();
             const float inv = l_run > 0.f ? pow2(-e) / l_run : 0.f;
@@ -920,8 +933,9 @@ cudaError_t launch_d(const LatentPrefillArgs &a, cudaStream_t s) {
         p.h0 = h0;
         p.heads = std::min(group, a.H - h0);
         p.v = p.k + (size_t)a.B * p.heads * s_pad * D;
-        p.skip_cta = h0 == 0 ? a.skip_kv.cta : -1;
-        p.wait_ns = a.skip_kv.wait_ns;
+        const CopySkip none;
+        const CopySkip &skip_kv = h0 == 0 ? a.skip_kv : none, &skip_prompt = h0 == 0 ? a.skip_prompt : none;
+        p.skip_cta = skip_kv.cta; p.wait_ns = skip_kv.wait_ns;
         // shares of the heads per position tile: the fewest rounds of CTAs, each costing its heads
         // and about one more for loading the tile's latent rows
         const long long tiles = (long long)a.B * (s_pad / kTile), sms = device_sms();
@@ -945,8 +959,7 @@ cudaError_t launch_d(const LatentPrefillArgs &a, cudaStream_t s) {
         e = launch_pdl(latent_kv_kernel<D>, dim3((unsigned)(tiles * p.splits)), dim3(kExpandThreads),
                        ExpandSmem::ALLOC, s, tmc, tmuk, tmuv, p);
         if (e != cudaSuccess) break;
-        p.skip_cta = h0 == 0 ? a.skip_prompt.cta : -1;
-        p.wait_ns = a.skip_prompt.wait_ns;
+        p.skip_cta = skip_prompt.cta; p.wait_ns = skip_prompt.wait_ns;
         e = launch_pdl(latent_attend_prompt_kernel<D>, dim3((unsigned)(p.n_qb * bh)), dim3(kAttThreads),
                        AttendSmem<D>::ALLOC, s, tmk, tmv, tmr, p);
     }

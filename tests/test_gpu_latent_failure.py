@@ -66,3 +66,21 @@ def test_prompt_attention(d, d_c, T):
     q, new_c = c.randn(2, T, 2, d + 64), c.randn(2, T, d_c + 64)
     want, got = run_thrice(lambda: prefill(c, q, new_c), _lib.TEST_LATENT_PROMPT, 1, c.pool)
     check_kept(want, got, (0, slice((T - 1) // 256 * 256, T), 1))
+
+
+@pytest.mark.parametrize("d,d_c", [(128, 512), (64, 256)])
+@pytest.mark.parametrize("cta", [0, 2, 4, 7])
+def test_expansion(d, d_c, cta):
+    """One head: CTA t expands tile t % 5 of sequence t // 5. Queries before its positions are as ever."""
+    c = Latent([600, 600], 1, d, d_c, seed=4)
+    q, new_c = c.randn(2, 600, 1, d + 64), c.randn(2, 600, d_c + 64)
+    want, got = run_thrice(lambda: prefill(c, q, new_c), _lib.TEST_LATENT_KV, cta, c.pool)
+    check_kept(want, got, (cta // 5, slice(cta % 5 * 128, 600)))
+
+
+def test_expansion_of_one_group_of_heads():
+    """A workspace for one head at a time, filled by each: the first head's group gives up on tile 1."""
+    c = Latent([600], 3, 128, 512, seed=5)
+    q, new_c = c.randn(1, 600, 3, 192), c.randn(1, 600, 576)
+    want, got = run_thrice(lambda: prefill(c, q, new_c, heads_in_ws=1), _lib.TEST_LATENT_KV, 1, c.pool)
+    check_kept(want, got, (0, slice(128, 600), 0))
