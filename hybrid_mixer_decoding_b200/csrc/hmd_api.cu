@@ -591,8 +591,9 @@ hmd_status_t kv_cache_evict(int budget, int recent, int B, int Hkv, int d, int p
         (!slots && n_slots < B) || (dst_table == page_table && dst_max_pages != max_pages) ||
         (weights_out == weights && w_out_len != w_len))
         return fail(HMD_ERR_SHAPE);
-    // grids of one block per (sequence, kv-head) and 64 rows, or 16 columns
-    if (max_seq_len >= kMaxLen ||
+    // grids of one block per (sequence, kv-head) and 64 rows, or 16 columns; the rows of kept are
+    // walked in steps of some thousands
+    if (max_seq_len >= kMaxLen || budget >= kMaxLen ||
         (long long)B * Hkv * std::max<long long>(keep / 64 + 1, d / 16 + 1) >= (1LL << 31))
         return fail(HMD_ERR_UNSUPPORTED);
     if (!aligned16(k_pool) || !aligned16(v_pool)) return fail(HMD_ERR_ARG);

@@ -302,19 +302,20 @@ __global__ void __launch_bounds__(kMoveThreads) evict_pack_kernel(const EvictArg
     const int tid = threadIdx.x, bg = blockIdx.x / n_cols, col = blockIdx.x - bg * n_cols;
     const int b = bg / a.Hkv, g = bg - b * a.Hkv;
     const int32_t *kept = a.kept + (size_t)bg * a.budget;
+    const int n = min(a.budget, a.max_seq_len);  // -1 from there on
     if (pack_rows && bg % a.Hkv == 0 && col == 0 && tid == 0) a.new_lens[b] = row_of(a, b).n_keep;
     if (!pack_rows || col == a.d / 16) {  // the weights: 4-byte rows
         const int slot = a.slots ? a.slots[b] : b;
         if (slot < 0 || slot >= a.n_slots) return;  // reported by the choosing kernel
         const float *w = a.weights + ((size_t)slot * a.Hkv + g) * a.w_len;
         float *out = a.weights_out + ((size_t)slot * a.Hkv + g) * a.w_out_len;
-        for (int i0 = 0; i0 < a.budget; i0 += 4 * kMoveThreads) {
+        for (int i0 = 0; i0 < n; i0 += 4 * kMoveThreads) {
             float x[4];
             int j[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int i = i0 + u * kMoveThreads + tid;
-                j[u] = i < a.budget ? kept[i] : -1;
+                j[u] = i < n ? kept[i] : -1;
                 x[u] = j[u] >= 0 ? w[j[u]] : 0.f;
             }
             __syncthreads();  // every load of this block before any store into its sources
@@ -328,13 +329,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_pack_kernel(const EvictArg
     __nv_bfloat16 *pool = static_cast<__nv_bfloat16 *>(col < cols ? a.k_pool : a.v_pool);
     const int c = (col % cols) * 32 + (tid & 3) * 8;
     constexpr int kRows = kMoveThreads / 4, kUnroll = 8;
-    for (int i0 = 0; i0 < a.budget; i0 += kUnroll * kRows) {
+    for (int i0 = 0; i0 < n; i0 += kUnroll * kRows) {
         uint4 x[kUnroll];
         int j[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int i = i0 + u * kRows + tid / 4;
-            j[u] = i < a.budget ? kept[i] : -1;
+            j[u] = i < n ? kept[i] : -1;
             if (j[u] == i) j[u] = -1;  // already there
             if (j[u] >= 0) {
                 bool ok;

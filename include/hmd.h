@@ -364,7 +364,7 @@ HMD_API hmd_status_t attn_verify_scored(int n_q, int B, int Hq, int Hkv, int d, 
  *   held. L = 0 is an empty row; a length outside [0, max_seq_len] or a bad slot sets the error
  *   word, and the sequence comes out empty (new length 0, nothing moved); a bad page's rows are
  *   not moved and set HMD_DEVERR_PAGE.
- * Supported: bf16 pools, d in {64, 128}; page_tokens == 64; 0 <= recent <= budget, budget >= 1.
+ * Supported: bf16 pools, d in {64, 128}; page_tokens == 64; 0 <= recent <= budget, 1 <= budget < 2^30.
  * Attention does not depend on the order of the keys, so decoding continues at new_lens[b] + 1.  */
 HMD_API hmd_status_t kv_cache_evict(int budget, int recent, int B, int Hkv, int d, int page_tokens,
                                     void *k_pool, void *v_pool, int n_pages,

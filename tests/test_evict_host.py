@@ -69,3 +69,9 @@ def test_binding_refuses_types_layouts_and_devices():
         hmd.attn_verify_scored(**{**args, "k_pool": args["k_pool"].transpose(0, 1)})
     with pytest.raises(ValueError, match="current CUDA device"):
         hmd.attn_verify_scored(**args)
+
+
+@pytest.mark.parametrize("budget", [1 << 30, (1 << 31) - 1])
+def test_evict_refuses_budgets_its_loops_cannot_count(budget):
+    assert _evict(budget=budget, dst_pages=10, w_out_len=640) == UNSUP
+    assert _evict(budget=budget, recent=budget, dst=FAKE, dst_pages=10, w_out=FAKE, w_out_len=640) == UNSUP

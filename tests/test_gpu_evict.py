@@ -282,3 +282,9 @@ def test_captured_and_replayed_on_another_stream():
     torch.cuda.synchronize()
     for t, r in zip((o, c.w, w_out, kept, new_lens, c.k, c.v), ref):
         assert torch.equal(t, r)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_budget_far_above_the_lengths(in_place):
+    c = Cache([300, 0, 65], 2, 64, seed=12, extra=15)
+    check_evict(c, 200_000, 77, in_place)
