@@ -6,7 +6,8 @@ import torch
 
 import hybrid_mixer_decoding_b200 as hmd
 from hybrid_mixer_decoding_b200 import _lib
-from test_gpu_latent import BF, Latent, prefill
+from test_gpu_evict import Cache, new_tokens, scored
+from test_gpu_latent import Latent, prefill
 
 pytestmark = pytest.mark.gpu
 WAIT_NS = 1_000_000  # 1 ms
@@ -84,3 +85,31 @@ def test_expansion_of_one_group_of_heads():
     q, new_c = c.randn(1, 600, 3, 192), c.randn(1, 600, 576)
     want, got = run_thrice(lambda: prefill(c, q, new_c, heads_in_ws=1), _lib.TEST_LATENT_KV, 1, c.pool)
     check_kept(want, got, (0, slice(128, 600), 0))
+
+
+@pytest.mark.parametrize("nq", [1, 3])
+def test_scored_step(nq):
+    """CTA 0 has the first keys of kv-head 0 of sequence 0: its heads' outputs and all of its weights stay."""
+    Hq, Hkv, d, G = 8, 2, 128, 4
+    c = Cache([300, 270], Hkv, d, seed=6)
+    q, nk, nv = new_tokens(c, nq, Hq, Hkv, d)
+    k0, v0, w0 = c.k.clone(), c.v.clone(), c.w.clone()
+
+    def step():
+        c.k.copy_(k0), c.v.copy_(v0), c.w.copy_(w0)
+        o = scored(c, q, nk, nv, torch.full_like(q, KEPT))
+        torch.cuda.synchronize()
+        return o, c.w.clone(), c.k.clone(), c.v.clone()
+
+    want = step()
+    assert hmd.hmd_device_errors(clear=True) == 0
+    hmd.hmd_test_arm_copy_skip(_lib.TEST_ATTN_SPLIT, 0, WAIT_NS)
+    got = step()
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVERR_TIMEOUT
+    check_kept(want[0], got[0], (0, slice(None), slice(0, G)))
+    assert torch.equal(got[1][0, 0], w0[0, 0])
+    assert torch.equal(got[1][0, 1], want[1][0, 1]) and torch.equal(got[1][1], want[1][1])
+    assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
+    again = step()
+    assert hmd.hmd_device_errors(clear=True) == 0
+    assert all(torch.equal(a, b) for a, b in zip(again, want))

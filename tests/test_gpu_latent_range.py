@@ -5,11 +5,13 @@ times a power of two (half a step, 2^-11 of each; three values of a tile 2^-10):
 most 3 * 2^-11 of its terms, weights by as much, by 2^-11 themselves and by the exponential's 2^-13. The
 part of a score that comes from the shared rows is exact here (small integers and powers of two).
 """
+import copy
+
 import pytest
 import torch
 
 import hybrid_mixer_decoding_b200 as hmd
-from test_gpu_latent import DR, Latent, prefill
+from test_gpu_latent import DR, Latent, check_prefill, prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +121,42 @@ def test_values_beyond_fp16_are_clipped_and_reported():
     assert o.isfinite().all() and o.abs().max() <= 65536
     c.w_uv *= 2.0 ** -18
     c.check(prefill(c, c.q, c.c, scale=0.125), 0.125)
+
+
+def alone(c, b):
+    """Sequence b of a batch as a batch of one, on the same pool."""
+    one = copy.copy(c)
+    one.table, one.lens_list = c.table[b:b + 1], c.lens_list[b:b + 1]
+    return one
+
+
+def test_a_clipped_query_counts_as_the_end_of_the_range():
+    c = Latent([150, 150], 2, 64, 128, seed=51)
+    q, new_c = c.randn(2, 150, 2, 128), c.randn(2, 150, 192)
+    q[1, 100, 1, 5] = -1e6
+    o = prefill(c, q, new_c)
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVWARN_RANGE
+    # every other row is as with a query inside the range
+    q[1, 100, 1, 5] = -65280
+    near = prefill(c, q, new_c)
+    assert hmd.hmd_device_errors(clear=True) == 0
+    rest = torch.ones_like(o, dtype=torch.bool)
+    rest[1, 100, 1] = False
+    assert torch.equal(o[rest], near[rest])
+    check_prefill(c, q, new_c, near, [0, 0], [150, 150])
+    # that row's scores are thousands, in which fp16 keys leave errors of about 3, so its weights are not
+    # determined: it is some mean of the values up to its position (to the output's rounding)
+    V = c.rows(1, 101)[:, :128].double() @ c.w_uv[1].double().T
+    row, half_step = o[1, 100, 1].double(), 2.0 ** -8 * V.abs().amax(0)
+    assert (row <= V.amax(0) + half_step).all() and (row >= V.amin(0) - half_step).all()
+
+
+@pytest.mark.parametrize("bad", [0, 1])
+def test_a_bad_page_leaves_the_other_sequence(bad):
+    c = Latent([100, 100], 3, 128, 256, seed=52, max_len=300)
+    q, new_c = c.randn(2, 50, 3, 192), c.randn(2, 50, 320)
+    c.table[bad, 0] = c.pool.shape[0]
+    o = prefill(c, q, new_c, [64, 70], [50, 41])
+    assert hmd.hmd_device_errors(clear=True) == hmd.DEVERR_PAGE
+    b = 1 - bad
+    check_prefill(alone(c, b), q[b:b + 1], new_c[b:b + 1], o[b:b + 1], [[64, 70][b]], [[50, 41][b]])
