@@ -720,13 +720,10 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         auto attend = [&](auto mixed) {
             const unsigned short *e_at = reinterpret_cast<const unsigned short *>(v0) + (lane & 3);
             uint32_t e_bit = 0;
-            bool missing = false;
             if constexpr (decltype(mixed)::value) e_bit = *e_at;
             for (int i = 0; i < nt; ++i) {
                 if constexpr (decltype(mixed)::value) {
-                    const uint32_t code = __ballot_sync(0xffffffffu, e_bit & 1u) & ((1u << kExpBits) - 1);
-                    const int e_i = e_of(code);
-                    missing |= code == kMissing;
+                    const int e_i = e_of(__ballot_sync(0xffffffffu, e_bit & 1u) & ((1u << kExpBits) - 1));
                     if (i + 1 < nt) e_bit = e_at[(size_t)(i + 1) * kTile * D];
                     m_base += (float)(e_i - e);
                     l_run *= pow2(e - e_i);
@@ -822,13 +819,14 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(SM::B_P + qt));
             }
-            if (missing) l_run = -1.f;
         };
-        if (c_min == c_max && c_max != kMissing) attend(std::false_type());
+        // (kernel 2 gave up on a tile: this CTA does too. Kept in a register of the loop, for the query tile
+        // alone, it was 1% of the kernel.)
+        if (c_max == kMissing) *abort_flag = 1;
+        if (c_min == c_max) attend(std::false_type());
         else attend(std::true_type());
         wait_warp(lead, bar(SM::o(qt, nt - 1)), ring_parity(nt - 1), abort_flag, p.wait_ns);
-        // (o stays as it was, too, where kernel 2 gave up and reported it)
-        const bool ok = __all_sync(0xffffffffu, *abort_flag == 0 && !(l_run < 0.f));
+        const bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
         if (ok) {
             tc_fence_after();
             const float inv = l_run > 0.f ? pow2(-e) / l_run : 0.f;

@@ -609,8 +609,8 @@ typedef enum {
  * its outputs untouched (delta decode: its state slice and its columns of o; attention: the
  * query heads of its kv-head for that sequence, whose combine is skipped, and the weights of the
  * scored form; latent attention: the rows of o that need what the CTA computes, which are those of
- * its row group of the sequence, of its head and query block, or of the queries of its heads that
- * see its positions); every other CTA runs
+ * its row group of the sequence, of its head and query block, or of its heads' queries that see
+ * its positions, with others of their blocks of 256); every other CTA runs
  * normally. A cta beyond the launch's grid arms nothing that fires; cta = -1 disarms.
  * HMD_ERR_ARG for a bad kernel, cta < -1 or wait_ns out of range.                             */
 HMD_API hmd_status_t hmd_test_arm_copy_skip(hmd_test_kernel_t kernel, int cta, uint64_t wait_ns);
