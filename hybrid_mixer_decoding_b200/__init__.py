@@ -9,7 +9,7 @@ from ._lib import (BF16, BatchPlan, group_sequences, mixer_decode_step_batch, DE
                    KDA, SWA, DecodeIO, HmdError, KVCache, LatentCache, StateCache, attn_decode,
                    attn_decode_static_ws, attn_prefill, attn_prefill_ext, attn_decode_workspace_size,
                    attn_latent_decode, attn_latent_decode_workspace_size, attn_latent_prefill,
-                   attn_latent_prefill_workspace_size, DEVWARN_RANGE,
+                   attn_latent_prefill_workspace_size, DEVWARN_ALL, DEVWARN_RANGE,
                    attn_verify, attn_verify_scored, attn_verify_scored_workspace_size,
                    attn_verify_workspace_size, delta_rule_decode, delta_rule_decode_act,
                    delta_rule_decode_chain,
@@ -23,7 +23,7 @@ __all__ = ["BF16", "BatchPlan", "group_sequences", "mixer_decode_step_batch", "D
            "GDN", "KDA", "SWA", "DecodeIO", "HmdError", "KVCache", "LatentCache", "StateCache", "attn_decode",
            "attn_decode_static_ws", "attn_decode_workspace_size", "attn_latent_decode",
            "attn_latent_decode_workspace_size", "attn_latent_prefill",
-           "attn_latent_prefill_workspace_size", "DEVWARN_RANGE", "attn_prefill", "attn_prefill_ext",
+           "attn_latent_prefill_workspace_size", "DEVWARN_ALL", "DEVWARN_RANGE", "attn_prefill", "attn_prefill_ext",
            "attn_verify", "attn_verify_scored", "attn_verify_scored_workspace_size",
            "attn_verify_workspace_size", "delta_rule_decode", "delta_rule_decode_act",
            "delta_rule_decode_chain",

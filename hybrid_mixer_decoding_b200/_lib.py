@@ -16,7 +16,7 @@ STATUS = {0: "HMD_OK", 1: "HMD_ERR_ARG", 2: "HMD_ERR_SHAPE", 3: "HMD_ERR_DTYPE",
           4: "HMD_ERR_OOM", 5: "HMD_ERR_CUDA", 6: "HMD_ERR_UNSUPPORTED",
           7: "HMD_ERR_DEVICE_CHECK"}
 DEVERR_TIMEOUT, DEVERR_PAGE, DEVERR_SLOT, DEVERR_SEQLEN, DEVERR_GATE = 0x1, 0x2, 0x4, 0x8, 0x10
-DEVWARN_RANGE = 0x20
+DEVWARN_RANGE = DEVWARN_ALL = 0x20
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhmd.so")
 _lib = None
@@ -355,7 +355,8 @@ def attn_verify_scored_workspace_size(n_q, B, Hq, Hkv, d, page_tokens, max_seq_l
 def attn_verify_scored(q, new_k, new_v, k_pool, v_pool, weights, page_table, seq_lens,
                        max_seq_len, o, workspace, slots=None, stream=None) -> None:
     """attn_verify over an FA cache that also adds every key's softmax weight to weights
-    [n_slots,Hkv,w_len] fp32 (see include/hmd.h); n_q = 1 is the decode step. q,o [B,n_q,Hq,d];
+    [n_slots,Hkv,w_len] fp32 (see include/hmd.h); n_q = 1 is the decode step. All n_q tokens count,
+    accepted or not. q,o [B,n_q,Hq,d];
     new_k,new_v [B,n_q,Hkv,d]; slots int32 [B] or None (row b)."""
     B, n_q, Hq, d = _dims(q, 4, "q")
     n_pages, Hkv, PT, _ = _dims(k_pool, 4, "k_pool")

@@ -67,7 +67,8 @@ CopySkip take_copy_skip(int kernel);
 
 // Launches `kernel` on stream s with programmatic stream serialisation: it may be scheduled
 // while the previous kernel in the stream drains, and waits for it (griddep_wait) before its
-// first global-memory access, so results are those of an ordinary launch.
+// first access to what that or an earlier kernel may write (see there for a call's own inputs), so
+// results are those of an ordinary launch.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t s, Args &&...args) {

@@ -114,8 +114,12 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 
 // Programmatic dependent launch. griddep_wait: block until the grids this launch depends on
 // have completed and their writes are visible (a no-op for a launch without such a dependency);
-// every kernel calls it before its first global-memory access. griddep_launch_dependents: allow
-// the next kernel in the stream to be scheduled (it still waits in its own griddep_wait).
+// every kernel calls it before its first access to global memory that another kernel may write.
+// griddep_launch_dependents: allow the next kernel in the stream to be scheduled (it still waits in
+// its own griddep_wait). A kernel may read a call's own inputs (weights, lengths, queries) before it
+// waits only if the kernel before it belongs to the same call, does not write them, and allows it to be
+// scheduled after its own griddep_wait (or was itself scheduled in this way): then all that came before
+// the call is complete. After a kernel that allows it first, such a read is a race.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -58,7 +58,9 @@ typedef enum {
 #define HMD_DEVERR_SLOT      0x4u  /* a state-slot index was outside [0, n_slots) */
 #define HMD_DEVERR_SEQLEN    0x8u  /* a sequence length was < 1 or above the stated maximum */
 #define HMD_DEVWARN_RANGE    0x20u /* a value outside fp16's range was clipped to it
-                                      (attn_latent_prefill) */
+                                      (attn_latent_prefill): the call is complete */
+#define HMD_DEVWARN_ALL      0x20u /* the bits of completed calls: *bits & ~HMD_DEVWARN_ALL has those
+                                      of failed ones */
 #define HMD_DEVERR_GATE      0x10u /* reserved: no longer raised (the chunked prefill accepts
                                       every gate range) */
 
@@ -332,6 +334,9 @@ HMD_API hmd_status_t attn_decode_static_ws(hmd_kind_t kind, int window, int B, i
  *   gains sum over the n_q tokens and the group's query heads of p_j; the slots of the new tokens
  *   (positions L - n_q .. L - 1) start from 0, so a fresh row needs no clearing beyond the
  *   positions a prefill filled. Entries from L on are left as they were.
+ * All n_q tokens count, whether a caller keeps them or not: nothing takes the weights of a rejected
+ * draft's queries out again (its own slots start from 0 when they are written next). To count only
+ * accepted tokens, verify with attn_verify and run this call on those that were accepted.
  * No two sequences of a call may share a row. To count a prompt's last queries, prefill all but
  * its last n_q tokens and run those through this call. A bad slot skips the sequence's weights
  * and sets HMD_DEVERR_SLOT. The append is attn_verify's; o is too, bit for bit where both split

@@ -1,5 +1,6 @@
 """Refusals of the latent-attention entry points: a status on the host, before any launch."""
 import ctypes
+import re
 
 import pytest
 import torch
@@ -108,3 +109,13 @@ def test_binding_refuses_weights():
                        (w[:, :64], "current CUDA device")]:
         with pytest.raises((TypeError, ValueError), match=match):
             _lib._head_stride(-1, "w_uk", bad, 4, 64, 128)
+
+
+def test_warnings_can_be_told_from_errors():
+    errors = (hmd.DEVERR_TIMEOUT, hmd.DEVERR_PAGE, hmd.DEVERR_SLOT, hmd.DEVERR_SEQLEN, hmd.DEVERR_GATE)
+    assert not any(e & hmd.DEVWARN_ALL for e in errors)
+    assert hmd.DEVWARN_RANGE & ~hmd.DEVWARN_ALL == 0
+    text = open(hmd._lib.__file__.replace("hybrid_mixer_decoding_b200/_lib.py", "include/hmd.h")).read()
+    for name in ("RANGE", "ALL"):
+        value = re.search(rf"#define HMD_DEVWARN_{name}\s+0x([0-9a-f]+)u", text).group(1)
+        assert int(value, 16) == getattr(hmd, f"DEVWARN_{name}")
