@@ -52,6 +52,18 @@ auto once_per_device(F f) -> decltype(f()) {
     return results[dev];
 }
 
+// Streaming multiprocessors of the current device (148, as on B200, where it cannot be asked).
+inline int sm_count() {
+    return once_per_device([] {
+        int dev = 0, v = 0;
+        if (cudaGetDevice(&dev) == cudaSuccess &&
+            cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
+            return v;
+        cudaGetLastError();
+        return 148;
+    });
+}
+
 // Records `s` as this host thread's last error (read by hmd_last_error) and returns it; for
 // entry points defined outside the API file.
 hmd_status_t record_status(hmd_status_t s);

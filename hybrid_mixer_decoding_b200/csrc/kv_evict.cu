@@ -40,7 +40,6 @@ constexpr int kBins = 2048;           // 11 bits a digit
 constexpr int kCacheKeys = 49152;     // weights held in shared memory: 192 KiB
 constexpr int kMaxRanks = 8;          // CTAs of a cluster (of 16, few fit at once: 58 us instead of 24)
 constexpr int kShare = 4096;          // a CTA of a cluster has at least this many entries
-constexpr int kSms = 148;
 constexpr int kMoveThreads = 256;
 constexpr int kRowsPerBlock = 64;     // rows moved by one CTA into other pages
 
@@ -366,9 +365,10 @@ cudaError_t launch_kv_evict(const EvictArgs &a, cudaStream_t s) {
     if (attr_err != cudaSuccess) return attr_err;
     const int heads = a.B * a.Hkv;
     // Split an entry list over a cluster while every CTA keeps at least kShare entries and the
-    // clusters of all heads fit the GPU at once (two CTAs per SM).
+    // clusters of all heads fit the GPU at once (two CTAs per SM, which shared memory allows up to about
+    // 22,000 cached entries a CTA; longer shares run in two rounds).
     int n_ranks = 1;
-    while (n_ranks < kMaxRanks && a.max_seq_len / (2 * n_ranks) >= kShare && heads * 2 * n_ranks <= 2 * kSms) n_ranks *= 2;
+    while (n_ranks < kMaxRanks && a.max_seq_len / (2 * n_ranks) >= kShare && heads * n_ranks <= sm_count()) n_ranks *= 2;
     const int share = ((a.max_seq_len + 31) / 32 + n_ranks - 1) / n_ranks * 32;
     const bool cached = share <= kCacheKeys;
     cudaLaunchConfig_t cfg{};

@@ -931,17 +931,6 @@ __global__ void __launch_bounds__(kExpThreads, 1) latent_expand_kernel(const Lat
 }
 
 // ---- host side ---------------------------------------------------------------------------------
-int device_sms() {
-    return once_per_device([] {
-        int dev = 0, v = 0;
-        if (cudaGetDevice(&dev) == cudaSuccess &&
-            cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
-            return v;
-        cudaGetLastError();
-        return 148;
-    });
-}
-
 struct Plan {
     int n_groups, n_ranges;
     size_t off_o, off_ml, off_start, off_ranges, off_cum, bytes;
@@ -951,7 +940,7 @@ Plan make_plan(int nq, int B, int H, int dc, int max_seq_len) {
     pl.n_groups = (int)(((long long)nq * H + kRows - 1) / kRows);
     const long long pages = (long long)B * (((long long)max_seq_len + kPT - 1) / kPT);
     // one CTA per SM: the groups of one range run side by side and share its pages through L2
-    pl.n_ranges = (int)std::min<long long>(std::max(1, device_sms() / pl.n_groups), pages);
+    pl.n_ranges = (int)std::min<long long>(std::max(1, sm_count() / pl.n_groups), pages);
     const size_t pieces = (size_t)(pl.n_ranges + B) * pl.n_groups;
     pl.off_o = (size_t)B * pl.n_groups * (dc / 64 + 1) * kBlk;
     pl.off_ml = pl.off_o + pieces * kRows * dc * sizeof(float);
@@ -1004,7 +993,7 @@ cudaError_t launch_expand_t(const LatentParams &p, int tokens, cudaStream_t s) {
 template <int D, int NP>
 cudaError_t launch_expand_np(const LatentParams &p, cudaStream_t s) {
     int tokens = 4;
-    while (tokens < 32 && (long long)p.H * ((p.B * p.nq + tokens - 1) / tokens) > device_sms()) tokens *= 2;
+    while (tokens < 32 && (long long)p.H * ((p.B * p.nq + tokens - 1) / tokens) > sm_count()) tokens *= 2;
     return tokens > 16 ? launch_expand_t<D, NP, 32>(p, tokens, s) : launch_expand_t<D, NP, 16>(p, tokens, s);
 }
 template <int D>

@@ -871,17 +871,6 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
 }
 
 // ---- host side -----------------------------------------------------------------------------------
-int device_sms() {
-    return once_per_device([] {
-        int dev = 0, v = 0;
-        if (cudaGetDevice(&dev) == cudaSuccess &&
-            cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
-            return v;
-        cudaGetLastError();
-        return 148;
-    });
-}
-
 size_t padded(int T, int max_prefix) {
     return ((size_t)T + max_prefix + kTile - 1) / kTile * kTile;
 }
@@ -936,7 +925,7 @@ cudaError_t launch_d(const LatentPrefillArgs &a, cudaStream_t s) {
         p.skip_cta = skip_kv.cta; p.wait_ns = skip_kv.wait_ns;
         // shares of the heads per position tile: the fewest rounds of CTAs, each costing its heads
         // and about one more for loading the tile's latent rows
-        const long long tiles = (long long)a.B * (s_pad / kTile), sms = device_sms();
+        const long long tiles = (long long)a.B * (s_pad / kTile), sms = sm_count();
         long long best = -1;
         for (int n = 1; n <= p.heads; ++n) {
             const int per = (p.heads + n - 1) / n;
