@@ -92,6 +92,16 @@ __device__ __forceinline__ bool clip_half(float &x) {
     return out;
 }
 
+// For the products' warp after a wait that gave up: it goes on over what memory holds, with waits that return
+// at once, and frees slots whose copies may not have landed. So it first waits (bounded) until the
+// copying warp, which sees the flag too, fills no more of them. (Stopping the products instead cost 1 to 2%.)
+__device__ __forceinline__ void await_stop(volatile int *copies_end, unsigned long long limit_ns) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (!__any_sync(0xffffffffu, *copies_end || globaltimer_ns() - t0 > 2 * limit_ns)) {
+    }
+    __syncwarp();
+}
+
 struct PrefillParams {
     const __nv_bfloat16 *q, *c;
     __nv_bfloat16 *pool, *o;
@@ -174,7 +184,7 @@ struct ExpandSmem {
     static constexpr int B_A = 0, B_MOVED = 1, B_WFULL = 2, B_WFREE = B_WFULL + NW, B_ACC = B_WFREE + NW,
                          B_READ = B_ACC + kExpAcc, B_END = B_READ + kExpAcc, N_BARS = B_END + 1;
     static constexpr uint32_t OFF_MAX = OFF_MISC + 448;  // [two sets of warps][two steps][four warps]
-    static_assert(N_BARS * 8 + 8 <= 448, "barriers");
+    static_assert(N_BARS * 8 + 12 <= 448, "barriers");
     __device__ static uint32_t stage(int w) { return (w < EARLY ? w + NW - EARLY : w - EARLY) * W_STAGE; }
 };
 static_assert(ExpandSmem::ALLOC <= 232448, "shared memory per CTA");
@@ -236,6 +246,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
     auto bar = [&](int i) { return bars + 8 * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SM::OFF_MISC + 8 * SM::N_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + SM::OFF_MISC + 8 * SM::N_BARS + 4);
+    volatile int *copies_end = abort_flag + 1;  // the copying warp asks for no more
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int tiles = p.s_pad / kTile, tile = blockIdx.x / p.splits;
     const int b = tile / tiles, pos0 = (tile - b * tiles) * kTile;
@@ -255,6 +266,7 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         if ((int)blockIdx.x == p.skip_cta) mbar_expect_tx(bar(SM::B_WFULL), 16);
         fence_barrier_init();
         *abort_flag = 0;
+        *copies_end = 0;
     }
     if (warp == 9) {
         __syncwarp();
@@ -313,22 +325,23 @@ latent_kv_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant_
         }
         if (!ok && lead) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
         n_loaded = n;
+        *copies_end = 1;
         __syncwarp();
     } else if (warp == 9) {
         const bool lead = elect_one();
         const Desc d_w(smem_desc_sw128(sb, 16, 1024));
         constexpr uint32_t ID = idesc_bf16(128, 128, 0, 0);
-        auto wait = [&](int i, uint32_t parity) { return wait_warp(lead, bar(i), parity, abort_flag, p.wait_ns); };
+        auto wait = [&](int i, uint32_t parity) {
+            if (!wait_warp(lead, bar(i), parity, abort_flag, p.wait_ns)) await_stop(copies_end, p.wait_ns);
+        };
         griddep_wait();  // what the first wait is for comes after it: the kernel before is not part of its limit
-        bool ok = wait(SM::B_MOVED, 0);
+        wait(SM::B_MOVED, 0);
         int w = 0, round = 0;
-        for (int st = 0; st < n_steps && ok; ++st) {
+        for (int st = 0; st < n_steps; ++st) {
             const int acc = st % kExpAcc;
-            if (st >= kExpAcc) ok = wait(SM::B_READ + acc, (st / kExpAcc - 1) & 1);
-            for (int kc = 0; kc < n_kc && ok; ++kc) {
-                // after a wait that gave up nothing is issued: no stage is freed whose copy has not landed
-                ok = wait(SM::B_WFULL + w, round & 1);
-                if (!ok) break;
+            if (st >= kExpAcc) wait(SM::B_READ + acc, (st / kExpAcc - 1) & 1);
+            for (int kc = 0; kc < n_kc; ++kc) {
+                wait(SM::B_WFULL + w, round & 1);
                 tc_fence_after();
                 const Desc wd = d_w.at(SM::stage(w));
 #pragma unroll
@@ -492,7 +505,7 @@ struct AttendSmem {
     static constexpr int B_FULL = 0, B_S = NR, B_O = B_S + 2 * kRingPhases, B_K = B_O + 2 * kRingPhases,
                          B_P = B_K + kRingPhases, B_SR = B_P + 2, B_Q = B_SR + 1, B_END = B_Q + 1,
                          N_BARS = B_END + 1;
-    static_assert(N_BARS * 8 + 8 <= 256, "barriers");
+    static_assert(N_BARS * 8 + 12 <= 256, "barriers");
     __device__ static int s(int j, int i) { return B_S + j * kRingPhases + ring_barrier(i); }
     __device__ static int o(int j, int i) { return B_O + j * kRingPhases + ring_barrier(i); }
     // in TMEM: O_0, O_1, S (both query tiles' in turn), P_0, P_1
@@ -513,6 +526,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
     auto bar = [&](int i) { return bars + 8 * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + SM::OFF_BAR + 8 * SM::N_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + SM::OFF_BAR + 8 * SM::N_BARS + 4);
+    volatile int *copies_end = abort_flag + 1;  // the copying warp asks for no more
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     // longest query blocks of all heads first (a wave of CTAs on a few heads' blocks of all lengths,
     // which keeps their keys in L2, ended 8% later)
@@ -537,6 +551,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         if ((int)blockIdx.x == p.skip_cta) mbar_expect_tx(bar(SM::B_FULL), 16);
         fence_barrier_init();
         *abort_flag = 0;
+        *copies_end = 0;
     }
     if (warp == 8) {
         __syncwarp();
@@ -618,6 +633,7 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         }
         if (!ok && lead) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
         n_loaded = n;
+        *copies_end = 1;
         __syncwarp();
     } else if (warp == 8) {
         // ===== products: S_0(i+1), O_0(i), S_1(i+1), O_1(i) (the warp converged). A tile's scores are
@@ -635,16 +651,14 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
         auto wait_for = [&](int n, int count, int i, int parity) {
             const int u = n + lane;
             const bool block = lane < count;
-            const bool ok = wait_warp(block || (lane == count && i >= 0),
-                                      bar(block ? SM::B_FULL + u % NR : max(i, 0)),
-                                      (block ? u / NR : parity) & 1, abort_flag, p.wait_ns);
+            if (!wait_warp(block || (lane == count && i >= 0), bar(block ? SM::B_FULL + u % NR : max(i, 0)),
+                           (block ? u / NR : parity) & 1, abort_flag, p.wait_ns))
+                await_stop(copies_end, p.wait_ns);
             tc_fence_after();
-            return ok;
         };
-        // after a wait that gave up nothing is issued: no block is freed whose copy has not landed
         auto issue_s = [&](int j, int i) {  // S = Q_j K_i^T
             const int n = ring_key<D>(i);
-            if (!wait_for(n, j == 0 || i >= nt0 ? KB : 0, n_s > 0 ? SM::B_SR : -1, n_s - 1)) return false;
+            wait_for(n, j == 0 || i >= nt0 ? KB : 0, n_s > 0 ? SM::B_SR : -1, n_s - 1);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 const Desc k = d_k.at(((uint32_t)(n + kb) % NR) * kBlk);
@@ -656,11 +670,10 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
             }
             umma_commit_if(lead, bar(SM::s(j, i)));
             ++n_s;
-            return true;
         };
         auto issue_o = [&](int j, int i) {  // O_j (+)= P_j V_i, P_j from TMEM
             const int n = ring_value<D>(i, n_tiles);
-            if (!wait_for(n, j == 0 || i >= nt0 ? VB : 0, SM::B_P + j, i)) return false;
+            wait_for(n, j == 0 || i >= nt0 ? VB : 0, SM::B_P + j, i);
             const uint32_t slot = (uint32_t)n % NR;
             const uint32_t o = tmem + SM::T_O + 128 * j, pj = tmem + SM::T_P + 64 * j;
             const Desc v = d_v.at(slot * kBlk);
@@ -678,14 +691,13 @@ latent_attend_prompt_kernel(const __grid_constant__ CUtensorMap tmk, const __gri
                     umma_ts_if(lead, o + 64, pj + 8 * kk, d_v.at(kk * 2048), ID_O64, kk > 0 ? 1u : more);
             }
             umma_commit_if(lead, bar(SM::o(j, i)));
-            return true;
         };
-        bool ok = wait_warp(lead, bar(SM::B_Q), 0, abort_flag, p.wait_ns);
-        for (int i = -1; i < n_tiles && ok; ++i) {
-            if (i + 1 < nt0) ok = issue_s(0, i + 1);
-            if (ok && i >= 0 && i < nt0) ok = issue_o(0, i);
-            if (ok && i + 1 < nt1) ok = issue_s(1, i + 1);
-            if (ok && i >= 0 && i < nt1) ok = issue_o(1, i);
+        if (!wait_warp(lead, bar(SM::B_Q), 0, abort_flag, p.wait_ns)) await_stop(copies_end, p.wait_ns);
+        for (int i = -1; i < n_tiles; ++i) {
+            if (i + 1 < nt0) issue_s(0, i + 1);
+            if (i >= 0 && i < nt0) issue_o(0, i);
+            if (i + 1 < nt1) issue_s(1, i + 1);
+            if (i >= 0 && i < nt1) issue_o(1, i);
         }
         if (lead) {
             if (*abort_flag) atomicOr(&g_err, HMD_DEVERR_TIMEOUT);
