@@ -26,8 +26,8 @@
 // by TMA (units of 128 dims, each freed as soon as its product is done), warps 5 and 6 issue the two
 // products, warps 0-3 are the softmax. O^T accumulates at an exponent base per row that moves only when the
 // row's scores exceed it by more than 2^8 (then O^T is rescaled in TMEM). B = 32, 32 heads, 4096 to
-// 8192 keys: 48 us, 226 MB, 4.7 TB/s (after the first pages at the rate of HBM; its start and the wait
-// for kernel 1 are 7 us). With 96 rows a sequence (three groups, B = 16, 2048 to 4097 keys) 34 us,
+// 8192 keys: 48 us, 226 MB, 4.7 TB/s (its start and the wait for kernel 1 are 7 us; in the 41 after them
+// 5.5 TB/s, where the FA decode reaches 6.5). With 96 rows a sequence (three groups, B = 16, 2048 to 4097 keys) 34 us,
 // bound by the tensor core: a page costs 36 products of 48 cycles (N = 64) and 16 of 40 for 32 rows.
 // Kernel 3 (merge and expand), one CTA per (head, 16 or 32 tokens): joins the ranges' partial sums
 // while W_uv[h] is copied to shared memory (asked for while kernel 2 ends: 69.6 -> 67.8 us for the batch

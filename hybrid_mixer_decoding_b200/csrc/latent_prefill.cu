@@ -25,7 +25,9 @@
 // C is the products' A operand and stays in TMEM, so that only the weights stream through shared memory
 // (a 128 x 128 product with both operands there reads 128 bytes a cycle, all it has: 74 us for 8192
 // positions of 32 heads, 59 us so); two accumulators, so one step's results are stored while the next
-// is computed. It is bound by the weights' way from L2: 256 KB a head and tile.
+// is computed. It is bound by the warp that copies the weights, 256 KB a head and tile from L2 in stages of
+// 16 KB: a stage takes 400 cycles, of which its products are 256 (one predicate more in that warp's loop
+// made 66 us of 59, the test of a flag 79).
 // Kernel 3 (attend): one CTA per (sequence, head, 256 queries): two query tiles of 128 whose
 // softmax groups alternate with the tensor core, as in the FA prefill; K tiles are d/64 + 1
 // blocks (the last one k_r, shared by the heads), V tiles d/64, all in one ring of blocks. A softmax group
@@ -33,8 +35,9 @@
 // its own P: a tile's scores are complete before the softmax of the tile before is done (with S and P
 // of a group in one place a key tile took 3400 cycles, softmax and products of a group in turn; now
 // 2900). d = 128: the products of a key tile alone take 2560, and with the copies they move 340 KB through
-// shared memory, 2660 cycles of its 128 bytes. B = 2, T = 4096, 32 heads: 397 us in all (1.04 PFLOP/s), 460
-// in a row under the power limit; B = 3, 1000 after 2801: 234 us. A CTA's start and end are about 12000 cycles.
+// shared memory, 2660 cycles of its 128 bytes. B = 2, T = 4096, 32 heads: 405 us in all (1.02 PFLOP/s), 457
+// to 483 in a row under the power limit; B = 3, 1000 after 2801: 237, 241 to 251 in a row. A CTA's start and
+// end are about 12000 cycles, a fifth of the kernel at T = 4096.
 // If the workspace holds fewer heads than H, kernels 2 and 3 run once per group of heads.
 #include <cuda.h>
 #include <cuda_fp16.h>
