@@ -11,13 +11,13 @@
 // adds nothing visible. Its range is 65504: larger keys, values or queries are clipped and reported
 // (HMD_DEVWARN_RANGE). Downwards it ends at 2^-14, so the values of a head in a tile of 128 positions are
 // stored times 2^e, e = 0, 20, 40 or 60, with which the largest of them is at 2^-5 or above (or as near as
-// e = 60 brings it): values are held to 2^-11, or to 2^-20 of the largest. Most often e is 0
-// everywhere, or the same; where it is not, the softmax lowers a tile's exponents by e and adds its weights
-// times 2^e to the row's sum, so that tiles of any sizes add up (a loop of its own: in the common one this
-// took 2 to 4% of the kernel). e goes with the values, in the last bits of three of them (those to 2^-10). Keys and queries need no such factor:
-// what they lose below 2^-14, at most 2^-25, moves a score by 2^-25 scale sum |q| (or |k|), with the usual
-// scale 4e-7 for 192 dims of size 1 and 0.03 at the end of fp16's range. So that this holds for any scale, the
-// power of two in one of 2 or more goes to the queries.
+// e = 60 brings it): values are held to 2^-11, or to 2^-20 of the largest. Most often e is 0 everywhere, or the
+// same; where it is not, the softmax lowers a tile's exponents by e and adds its weights times 2^e to the
+// row's sum, so that tiles of any sizes add up (a loop of its own: in the common one this took 2 to 4% of the
+// kernel). e goes with the values, in the last bits of three of them (those to 2^-10). Keys and queries need no
+// such factor: what they lose below 2^-14, at most 2^-25, moves a score by 2^-25 scale sum |q| (or |k|), with
+// the usual scale 4e-7 for 192 dims of size 1 and 0.03 at the end of fp16's range. So that this holds for any
+// scale, the power of two in one of 2 or more goes to the queries.
 //
 // Kernel 1 (rows): appends the new rows to the cache and converts every position's shared part
 // k_r to fp16. Kernel 2 (expand): one CTA per (128 positions, a share of the heads):
@@ -67,8 +67,9 @@ constexpr float kHalfMax = 65504.f;
 // the largest at 1, 100,000 keys of 2^-25.5 each were in the row's sum and not in its output.)
 constexpr float kTop = 15.f, kFresh = 9.f;
 // A head's values in a tile are stored times 2^e, e = kMaxExp - kExpStep * code, the code in the last bits of
-// its first kExpBits values (kMissing: kernel 2 gave up on the tile). The largest e leaves a row's sum, which has every weight times 2^e, far from
-// fp32's ends: 2^75 a key, and the 2^-125 at which the softmax clamps a masked key's weight is 2^-65.
+// its first kExpBits values (kMissing: kernel 2 gave up on the tile). The largest e leaves a row's sum, which
+// has every weight times 2^e, far from fp32's ends: 2^75 a key, and the 2^-125 at which the softmax clamps a
+// masked key's weight is 2^-65.
 constexpr int kMaxExp = 60, kExpStep = 20, kExpBits = 3;
 constexpr uint32_t kMissing = 7;
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
