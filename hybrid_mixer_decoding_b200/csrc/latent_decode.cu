@@ -692,7 +692,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_const
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     // P [32 rows][64 keys], rows of 128 bytes, 128-byte swizzle, once the product
-                    // before has read it
+                    // before has read it. bf16 as the latent rows, the one type a product can have beside them:
+                    // 2^-8 of a weight at random signs, as in the FA decode; the sum has them in full
                     if (k > 0) ok &= wait_warp(lead, bar(SM::B_O), (k - 1) & 1, abort_flag, p.wait_ns);
                     uint8_t *row = sm + SM::OFF_P + lane * 128;
 #pragma unroll
